@@ -256,6 +256,105 @@ int fwt_host_static_i32(const int32_t* re_in, const int32_t* im_in, int32_t* re_
                         fwt_stream_t stream);
 size_t fwt_host_static_workspace_bytes(void);
 
+/*
+ * ---- Feed-forward operators -------------------------------------------------------
+ *
+ * The rotation that language models apply before they hold activations and weights
+ * in 8 bits, the product of such operands, and the gated projections around it:
+ *
+ *     h = act(x Wg^T) * (x Wu^T)          fwt_gated      (fwt_gated_backward: gradients)
+ *     q, s = quantised rotation of h      fwt_quantize_blocks
+ *     y = q Wd^T                          fwt_matmul_blocks, Wd quantised the same way
+ *
+ * H is symmetric and, normalised, its own inverse, so rotating both operands of a
+ * product along the contraction leaves the product as it is, while an outlier of one
+ * element spreads over its group and costs the others fewer bits.
+ *
+ * Matrices are row-major with a leading dimension `ld_*` in elements (ld >= columns;
+ * rows may be a window of a larger matrix).  Sizes are free, from 0 on.  Input matrices
+ * and their rows start on 16-byte boundaries (pointer, and ld times the element size);
+ * fwt_quantize_blocks alone also takes inputs aligned to their elements only, and
+ * outputs C, h, dx and dw_* need no more than that either.  8-bit outputs are 16-byte
+ * aligned in both.  Nothing outside the rows' `columns` elements is read into a result
+ * or written.  Outputs overlap nothing.  Device pointers, streams, ownership and errors
+ * are as above: no allocation, no synchronisation, argument errors before any launch.
+ */
+enum fwt_real { FWT_F32 = 0, FWT_BF16 = 1, FWT_F16 = 2 };
+enum fwt_activation {
+  FWT_SILU = 0, /* g / (1 + exp(-g)) */
+  FWT_GELU = 1, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+  FWT_RELU = 2  /* max(g, 0); its derivative at 0 is 0 */
+};
+
+/*
+ * Rotation and quantisation to 8-bit floating point (e4m3: 4 exponent bits, 3 mantissa
+ * bits, largest value 448) with one fp32 scale for each block of 128.
+ *
+ * x is rows x cols of x_type (enum fwt_real).  The blocks run along `axis`: 1 along the
+ * columns, 0 along the rows (down a column).  Lines are what crosses it: rows for axis
+ * 1, columns for axis 0.  With r = rot_bits (0 .. 7) each aligned group of 2^r elements
+ * along the axis becomes 2^{-r/2} H_{2^r} times itself (r = 0: unchanged); the length
+ * is extended with zeros to L, a multiple of 2^r, for that.  Each block of 128 elements
+ * along the axis by `lines` (1 or 128) lines across it gets
+ *
+ *     s = max(max |y| / 448, 2^-126),   q = e4m3(y * (1 / s))  (to nearest even).
+ *
+ * q: lines-major, nl x L bytes (nl = rows for axis 1; cols for axis 0, that is
+ * transposed), line i at q + i * ld_q, ld_q a multiple of 16, at least L.  scale:
+ * ceil(nl / lines) x ceil(L / 128) floats, row i at scale + i * ld_scale.  A block that
+ * holds an Inf or NaN, or overflows in the rotation, gets a NaN scale and NaN codes.
+ * Rotation sums and scales are fp32.  Either extent may be 0 (nothing is written).
+ */
+int fwt_quantize_blocks(const void* x, int x_type, int64_t rows, int64_t cols, int64_t ld_x,
+                        int rot_bits, int axis, int lines, void* q, int64_t ld_q, float* scale,
+                        int64_t ld_scale, fwt_stream_t stream);
+
+/*
+ * Product of two 8-bit operands with block scales:
+ *
+ *     C[i, j] = sum_t a_scale[i, t] * b_scale[j / b_lines, t] * sum_{k in block t} a[i, k] b[j, k]
+ *
+ * a: m x k e4m3 with one scale per line and block of 128 along k; b: n x k e4m3 with one
+ * scale per block of 128 along k by b_lines (1 or 128) lines.  C: m x n of c_type.  Both
+ * operands run along the contraction, as fwt_quantize_blocks writes them (for the
+ * gradient products, along either axis).  Products and sums are fp32, in an order that
+ * depends on the sizes alone, with one rounding to c_type.  m or n = 0: nothing is
+ * written; k = 0: C is zero.
+ */
+int fwt_matmul_blocks(const void* a, int64_t ld_a, const float* a_scale, int64_t ld_a_scale,
+                      const void* b, int64_t ld_b, const float* b_scale, int64_t ld_b_scale,
+                      int b_lines, void* c, int c_type, int64_t ld_c, int64_t m, int64_t n,
+                      int64_t k, fwt_stream_t stream);
+
+/*
+ * Gated projections: h = act(x w_gate^T) * (x w_up^T), in one kernel.  x: m x d, w_gate
+ * and w_up: f x d, h: m x f, all of `type` (FWT_BF16 or FWT_F16).  Both products, the
+ * activation (enum fwt_activation) and their product stay in fp32; h is the one rounding.
+ * m or f = 0: nothing is written; d = 0: h is zero.
+ */
+int fwt_gated(const void* x, int64_t ld_x, const void* w_gate, int64_t ld_gate, const void* w_up,
+              int64_t ld_up, void* h, int64_t ld_h, int type, int activation, int64_t m,
+              int64_t f, int64_t d, fwt_stream_t stream);
+
+/*
+ * Its gradients.  grad: m x f, the gradient of h.  With g = x w_gate^T and u = x w_up^T
+ * computed again (nothing is kept from the forward call),
+ *
+ *     dg = grad * u * act'(g),  du = grad * act(g)
+ *     dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.
+ *
+ * dg and du are rounded to `type` once, in the workspace, as the operands of the second
+ * products; sums are fp32.  dx (m x d) may be NULL, and dw_gate and dw_up (f x d) both
+ * NULL, where they are not wanted.  Outputs are written, not added to.  workspace: DEVICE
+ * memory, 16-byte aligned, of at least fwt_gated_backward_workspace_bytes(m, f) bytes.
+ */
+int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t ld_x,
+                       const void* w_gate, int64_t ld_gate, const void* w_up, int64_t ld_up,
+                       void* dx, int64_t ld_dx, void* dw_gate, int64_t ld_dw_gate, void* dw_up,
+                       int64_t ld_dw_up, int type, int activation, int64_t m, int64_t f,
+                       int64_t d, void* workspace, size_t workspace_bytes, fwt_stream_t stream);
+size_t fwt_gated_backward_workspace_bytes(int64_t m, int64_t f);
+
 /* Static text for a status code (never NULL). */
 const char* fwt_status_string(int status);
 

@@ -8,7 +8,8 @@ The functions named like the C ABI (``fwt_batched_c32`` ...) take raw device
 pointers and marshal arguments only; every step of the transform runs in the
 CUDA kernels of ``libfwt_gb300.so``.  ``transform`` is the tensor-level wrapper:
 it checks dtypes, devices and contiguity, then calls the C ABI on the current
-PyTorch stream.  There is no CPU fallback: without the compiled library (see
+PyTorch stream.  ``quantize_blocks``, ``matmul_blocks``, ``gated`` and
+``gated_backward`` (``feed_forward.py``) are the feed-forward operators.  There is no CPU fallback: without the compiled library (see
 ``build.py``) every call raises.
 """
 from __future__ import annotations
@@ -22,6 +23,8 @@ LIBRARY = os.path.join(_HERE, "libfwt_gb300.so")
 FWT_OK, FWT_ERR_INVALID_ARG, FWT_ERR_MISALIGNED = 0, 1, 2
 FWT_ERR_UNSUPPORTED, FWT_ERR_CUDA, FWT_ERR_TIMEOUT = 3, 4, 5
 FWT_C32, FWT_C64, FWT_I32 = 0, 1, 2
+FWT_F32, FWT_BF16, FWT_F16 = 0, 1, 2  # element types of the feed-forward operators
+FWT_SILU, FWT_GELU, FWT_RELU = 0, 1, 2
 DTYPES = {"c32": FWT_C32, "c64": FWT_C64, "i32": FWT_I32}
 
 
@@ -120,6 +123,18 @@ def library() -> ctypes.CDLL:
         lib.fwt_trace_events.restype = ci
         lib.fwt_trace_count.argtypes = []
         lib.fwt_trace_count.restype = ci
+        lib.fwt_quantize_blocks.argtypes = [vp, ci, i64, i64, i64, ci, ci, ci, vp, i64, vp, i64, vp]
+        lib.fwt_quantize_blocks.restype = ci
+        lib.fwt_matmul_blocks.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, ci, i64, i64,
+                                          i64, i64, vp]
+        lib.fwt_matmul_blocks.restype = ci
+        lib.fwt_gated.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, ci, ci, i64, i64, i64, vp]
+        lib.fwt_gated.restype = ci
+        lib.fwt_gated_backward.argtypes = [vp, i64] * 7 + [ci, ci, i64, i64, i64, vp,
+                                                           ctypes.c_size_t, vp]
+        lib.fwt_gated_backward.restype = ci
+        lib.fwt_gated_backward_workspace_bytes.argtypes = [i64, i64]
+        lib.fwt_gated_backward_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
     return _lib
 
@@ -582,3 +597,6 @@ def transform_host(re, im=None, out_re=None, out_im=None, normalize: bool = True
         else:
             torch.cuda.synchronize(workspace.device)
     return out_re, out_im
+
+
+from .feed_forward import gated, gated_backward, matmul_blocks, quantize_blocks  # noqa: E402,F401

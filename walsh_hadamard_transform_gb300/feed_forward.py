@@ -1,0 +1,219 @@
+"""Feed-forward operators on CUDA tensors: the rotation fused with 8-bit block
+quantisation, the product of such operands, and the gated projections with their
+gradients.
+
+    h = gated(x, w_gate, w_up)                       act(x w_gate^T) * (x w_up^T)
+    q, s = quantize_blocks(h, rotate=7)              rotated, 8 bits, a scale for each 128
+    y = matmul_blocks(q, s, w_q, w_s)                w_q, w_s = quantize_blocks(w, rotate=7, lines=128)
+
+The rotation is its own inverse, so rotating both operands of a product along the
+contraction leaves the product as it is.  Matrices are 2-D tensors whose rows are
+contiguous (stride 1 along the columns) and may be a window of a larger matrix;
+operands of products start every row on a 16-byte boundary.  Outputs made here have
+such rows too (padded where the width asks for it).  Every call runs on ``stream``
+(default: the current PyTorch stream) and does not synchronise.
+"""
+from __future__ import annotations
+
+import walsh_hadamard_transform_gb300 as _fwt
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
+_REALS = None
+_E4M3 = None
+
+
+def _reals():
+    global _REALS, _E4M3
+    if _REALS is None:
+        torch = _fwt._torch_mod()
+        _E4M3 = torch.float8_e4m3fn
+        _REALS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return _REALS
+
+
+def _matrix(t, name, device, dtype=None, shape=None):
+    """Row stride of a 2-D CUDA tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: every tensor must be on one CUDA device")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {(rows, cols)}")
+    row, col = t.stride()
+    if col != 1 and cols > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows <= 1:
+        return max(cols + -cols % 16, row if row >= cols else 0)
+    return row
+
+
+def _empty(rows, cols, dtype, device, multiple):
+    """A new rows x cols tensor, its rows a multiple of ``multiple`` elements apart."""
+    torch = _fwt._torch_mod()
+    wide = -cols % multiple
+    t = torch.empty((rows, cols + wide), dtype=dtype, device=device)
+    return t[:, :cols] if wide else t
+
+
+
+def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None, stream=None):
+    """Rotates ``x`` (rows, cols) along ``axis`` and quantises it to 8-bit e4m3.
+
+    Each aligned group of ``2**rotate`` elements (0 <= rotate <= 7) along the axis is
+    multiplied by the normalised H, the length extended with zeros to whole groups; then
+    each block of 128 elements along the axis by ``lines`` (1 or 128) lines across it gets
+    an fp32 scale max|y| / 448 and codes e4m3(y / scale).  ``axis=1``: along the columns,
+    codes (rows, L).  ``axis=0``: down the rows, codes transposed (cols, L), so that they
+    run along the contraction of a gradient product.
+
+    ``x``: float32, bfloat16 or float16.  ``out``: (codes, scale) to write to.  Returns
+    (codes, scale): float8_e4m3fn (lines of codes, L) and float32 of a row for each
+    ``lines`` lines and a column for each block.
+    """
+    torch = _fwt._torch_mod()
+    reals = _REALS or _reals()
+    kind, device = reals.get(x.dtype), x.device
+    if kind is None:
+        raise TypeError(f"unsupported dtype {x.dtype}: use float32, bfloat16 or float16")
+    if axis not in (0, 1) or lines not in (1, 128) or not 0 <= rotate <= 7:
+        raise ValueError("axis is 0 or 1, lines 1 or 128 and rotate 0 .. 7")
+    ld = _matrix(x, "x", device)
+    rows, cols = x.shape
+    across, length = (rows, cols) if axis else (cols, rows)
+    length += -length % (1 << rotate)
+    shape = (-(-across // lines), -(-length // 128))
+    if out is None:
+        q = _empty(across, length, _E4M3, device, 16)
+        scale = _empty(*shape, torch.float32, device, 4)
+    else:
+        q, scale = out
+    ld_q = _matrix(q, "codes", device, _E4M3, (across, length))
+    ld_s = _matrix(scale, "scale", device, torch.float32, shape)
+    handle = _fwt._stream_handle(stream, device)
+    st = _fwt._on_device(device, lambda: _fwt.library().fwt_quantize_blocks(
+        x.data_ptr(), kind, rows, cols, ld, rotate, axis, lines, q.data_ptr(), ld_q,
+        scale.data_ptr(), ld_s, handle))
+    if st != _fwt.FWT_OK:
+        raise _fwt.FwtError(st, f"fwt_quantize_blocks({rows} x {cols}, axis={axis})")
+    return q, scale
+
+
+def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
+    """C = A B^T of 8-bit operands with block scales, as ``quantize_blocks`` writes them.
+
+    ``a``: float8_e4m3fn (m, k), ``a_scale``: float32 (m, ceil(k / 128)).  ``b``: (n, k),
+    ``b_scale`` a row for each line, (n, ceil(k / 128)), or for each 128 of them.  C is
+    (m, n) of ``out_dtype`` (bfloat16 by default, float16 or float32), or ``out``.
+    """
+    torch = _fwt._torch_mod()
+    reals = _REALS or _reals()
+    device = a.device
+    ld_a = _matrix(a, "a", device, _E4M3)
+    m, k = a.shape
+    ld_b = _matrix(b, "b", device, _E4M3)
+    n = b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError(f"a and b have {k} and {b.shape[1]} elements along the contraction")
+    blocks = -(-k // 128)
+    ld_as = _matrix(a_scale, "a_scale", device, torch.float32, (m, blocks))
+    lines = 1 if b_scale.dim() == 2 and b_scale.shape[0] == n else 128
+    ld_bs = _matrix(b_scale, "b_scale", device, torch.float32, (-(-n // lines), blocks))
+    if out is None:
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in reals:
+            raise TypeError(f"unsupported dtype {out_dtype}: use float32, bfloat16 or float16")
+        out = _empty(m, n, out_dtype, device, 16 // out_dtype.itemsize)
+    elif out.dtype not in reals or (out_dtype is not None and out.dtype != out_dtype):
+        raise TypeError(f"out: unsupported dtype {out.dtype}")
+    ld_c = _matrix(out, "out", device, None, (m, n))
+    handle = _fwt._stream_handle(stream, device)
+    st = _fwt._on_device(device, lambda: _fwt.library().fwt_matmul_blocks(
+        a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b, b_scale.data_ptr(),
+        ld_bs, lines, out.data_ptr(), reals[out.dtype], ld_c, m, n, k, handle))
+    if st != _fwt.FWT_OK:
+        raise _fwt.FwtError(st, f"fwt_matmul_blocks(m={m}, n={n}, k={k})")
+    return out
+
+
+def _gated_arguments(x, w_gate, w_up, activation):
+    kind, device = (_REALS or _reals()).get(x.dtype), x.device
+    if kind not in (1, 2):
+        raise TypeError(f"unsupported dtype {x.dtype}: use bfloat16 or float16")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation {activation!r}: use one of {sorted(_ACTIVATIONS)}")
+    ld_x = _matrix(x, "x", device, x.dtype)
+    d = x.shape[1]
+    f = w_gate.shape[0]
+    ld_g = _matrix(w_gate, "w_gate", device, x.dtype, (f, d))
+    ld_u = _matrix(w_up, "w_up", device, x.dtype, (f, d))
+    return kind, act, device, x.shape[0], f, d, ld_x, ld_g, ld_u
+
+
+def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T): both products, the activation and their product
+    in one kernel, fp32 inside and rounded once.
+
+    ``x`` (m, d), ``w_gate`` and ``w_up`` (f, d): bfloat16 or float16, all of one type.
+    ``activation``: "silu", "gelu" (the tanh form) or "relu".  Returns h (m, f)."""
+    kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up, activation)
+    if out is None:
+        out = _empty(m, f, x.dtype, device, 8)
+    ld_h = _matrix(out, "out", device, x.dtype, (m, f))
+    handle = _fwt._stream_handle(stream, device)
+    st = _fwt._on_device(device, lambda: _fwt.library().fwt_gated(
+        x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, out.data_ptr(), ld_h,
+        kind, act, m, f, d, handle))
+    if st != _fwt.FWT_OK:
+        raise _fwt.FwtError(st, f"fwt_gated(m={m}, f={f}, d={d})")
+    return out
+
+
+def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, workspace=None,
+                   want=("x", "w"), stream=None):
+    """Gradients of ``gated`` for ``grad``, the gradient of h (m, f).
+
+    Returns (dx, dw_gate, dw_up), of the inputs' shapes and type; those not named in
+    ``want`` ("x", and "w" for both weights) are not computed and None.  ``out``: the
+    three tensors to write to.  ``workspace``: a CUDA tensor of at least
+    ``fwt_gated_backward_workspace_bytes(m, f)`` bytes for the gradients of the two
+    products (allocated here when None)."""
+    torch = _fwt._torch_mod()
+    kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up, activation)
+    ld_dy = _matrix(grad, "grad", device, x.dtype, (m, f))
+    want_x, want_w = "x" in want, "w" in want
+    if out is None:
+        out = (_empty(m, d, x.dtype, device, 8) if want_x else None,
+               _empty(f, d, x.dtype, device, 8) if want_w else None,
+               _empty(f, d, x.dtype, device, 8) if want_w else None)
+    dx, dw_gate, dw_up = out
+    if want_x != (dx is not None) or want_w != (dw_gate is not None) or want_w != (dw_up is not None):
+        raise ValueError("out must hold the gradients named in want, and no other")
+    ld_dx = _matrix(dx, "dx", device, x.dtype, (m, d)) if want_x else 0
+    ld_dg = _matrix(dw_gate, "dw_gate", device, x.dtype, (f, d)) if want_w else 0
+    ld_du = _matrix(dw_up, "dw_up", device, x.dtype, (f, d)) if want_w else 0
+    if workspace is None:
+        workspace = torch.empty(fwt_gated_backward_workspace_bytes(m, f), dtype=torch.uint8,
+                                device=device)
+        if stream is not None:
+            # the allocator must not hand the memory on before `stream` is done with it
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream")
+                                    else torch.cuda.ExternalStream(int(stream), device=device))
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    handle = _fwt._stream_handle(stream, device)
+    pointer = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    st = _fwt._on_device(device, lambda: _fwt.library().fwt_gated_backward(
+        grad.data_ptr(), ld_dy, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u,
+        pointer(dx), ld_dx, pointer(dw_gate), ld_dg, pointer(dw_up), ld_du, kind, act, m, f, d,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+    if st != _fwt.FWT_OK:
+        raise _fwt.FwtError(st, f"fwt_gated_backward(m={m}, f={f}, d={d})")
+    return dx, dw_gate, dw_up
+
+
+def fwt_gated_backward_workspace_bytes(m: int, f: int) -> int:
+    return int(_fwt.library().fwt_gated_backward_workspace_bytes(int(m), int(f)))
