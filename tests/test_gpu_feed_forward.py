@@ -170,6 +170,7 @@ MATMUL = [  # m, n, k, lines, out
     (129, 300, 700, 128, "f32"), (200, 1100, 1152, 1, "f32"), (257, 2057, 385, 1, "f16"),
     (300, 513, 2049, 128, "bf16"), (1024, 1024, 1024, 128, "f32"), (1500, 3000, 640, 128, "bf16"),
     (3, 50000, 160, 128, "bf16"), (4000, 5, 200, 1, "f32"), (640, 384, 1, 128, "f32"),
+    (2307, 2500, 400, 128, "bf16"), (2500, 2307, 261, 1, "f32"), (2049, 2560, 640, 128, "f16"),
 ]
 
 
@@ -244,6 +245,7 @@ GATED = [  # m, d, f, dtype, act
     (40, 640, 384, "bf16", "silu"), (64, 1000, 1000, "f16", "silu"), (128, 64, 128, "bf16", "gelu"),
     (129, 1001, 531, "f16", "gelu"), (333, 200, 1031, "bf16", "silu"), (700, 513, 900, "bf16", "relu"),
     (1030, 1024, 1024, "f16", "silu"), (3, 1, 5, "bf16", "silu"), (130, 3, 70, "f16", "silu"),
+    (1500, 200, 2105, "bf16", "gelu"), (1281, 513, 3000, "f16", "silu"),
 ]
 
 
@@ -319,6 +321,7 @@ BACKWARD = [
     (7, 130, 257, "f16", "relu"), (16, 512, 512, "bf16", "gelu"), (33, 1001, 531, "bf16", "silu"),
     (100, 64, 72, "f16", "silu"), (128, 128, 128, "bf16", "silu"), (130, 257, 700, "bf16", "gelu"),
     (517, 333, 401, "f16", "gelu"), (600, 1024, 900, "bf16", "silu"), (1025, 128, 260, "bf16", "relu"),
+    (1500, 1303, 2105, "bf16", "silu"), (2307, 2500, 300, "f16", "gelu"),
 ]
 
 

@@ -40,5 +40,9 @@ cudaError_t launch_gated_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, in
 cudaError_t launch_gated_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int type, int m,
                             int f, int d, cudaStream_t st);
 
+// Read and clear the device error words of the kernels that wait (synchronising).
+cudaError_t read_device_error_gated(unsigned int* out);
+cudaError_t read_device_error_matmul(unsigned int* out);
+
 }  // namespace ff
 }  // namespace fwt

@@ -1,0 +1,78 @@
+// Host helpers of the feed-forward launchers: tensor maps and per-device set-up.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "feed_forward.cuh"
+
+namespace fwt {
+
+// The driver's tensor-map encoder, resolved once at run time (nullptr if absent).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace ff {
+
+// rows x cols, 128-byte boxes of `box_rows` rows with 128-byte swizzle; zero outside.
+inline bool swizzled_map(CUtensorMap* out, const void* p, int bytes, CUtensorMapDataType type,
+                         int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * bytes)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), (cuuint32_t)box_rows};
+  const cuuint32_t steps[2] = {1, 1};
+  return encode(out, type, 2, const_cast<void*>(p), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Multiprocessors of the current device, asked once for each device.
+inline int multiprocessors() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Launches `kernel` in clusters of `cluster` CTAs; its shared-memory limit is raised by the
+// first launch on each device.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), std::atomic<uint64_t>& ready, unsigned grid,
+                           unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
+                           const Args&... args) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (!(ready.load(std::memory_order_acquire) & bit) || !bit) {
+    err = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)smem);
+    if (err != cudaSuccess) return err;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace ff
+}  // namespace fwt

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fwt.h"
+#include "feed_forward.cuh"
 #include "registry.cuh"
 
 namespace fwt {
@@ -1122,15 +1123,17 @@ int fwt_selftest_bounded_wait(fwt_stream_t stream) {
 }
 
 int fwt_device_status(void) {
-  unsigned int e[3] = {0, 0, 0};
+  unsigned int e[5] = {0, 0, 0, 0, 0};
   cudaError_t err = fwt::read_device_error_c32(&e[0]);
   if (err == cudaSuccess) err = fwt::read_device_error_c64(&e[1]);
   if (err == cudaSuccess) err = fwt::read_device_error_i32(&e[2]);
+  if (err == cudaSuccess) err = fwt::ff::read_device_error_gated(&e[3]);
+  if (err == cudaSuccess) err = fwt::ff::read_device_error_matmul(&e[4]);
   if (err != cudaSuccess) {
     fwt::g_last_cuda_error = (int)err;
     return FWT_ERR_CUDA;
   }
-  return (e[0] | e[1] | e[2]) ? FWT_ERR_TIMEOUT : FWT_OK;
+  return (e[0] | e[1] | e[2] | e[3] | e[4]) ? FWT_ERR_TIMEOUT : FWT_OK;
 }
 
 int fwt_set_l2_chunk_bytes(long long bytes) {
