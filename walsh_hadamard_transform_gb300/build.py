@@ -1,6 +1,6 @@
 """Build the CUDA library ``libfwt_gb300.so`` in-tree with nvcc (sm_103a only).
 
-Twelve translation units are compiled in parallel and linked into one shared
+Fourteen translation units are compiled in parallel and linked into one shared
 library next to this file; objects go to ``_build/`` at the repository root.
 """
 from __future__ import annotations
@@ -20,7 +20,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libfwt_gb300.so")
 SOURCES = ["fwt_api.cu", "host_pipeline.cu", "rows_c32.cu", "rows_c64.cu", "rows_i32.cu",
            "cols_c32.cu", "cols_c64.cu", "cols_i32.cu",
-           "ff_api.cu", "quantize.cu", "matmul_blocks.cu", "gated.cu"]
+           "ff_api.cu", "quantize.cu", "matmul_blocks.cu", "gated.cu",
+           "matmul_tokens.cu", "gated_tokens.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -30,5 +30,11 @@ __device__ __forceinline__ void activation(float g, float& value, float& slope) 
   }
 }
 
+__device__ __forceinline__ void activate(int act, float g, float& value, float& slope) {
+  if (act == FWT_SILU) activation<FWT_SILU>(g, value, slope);
+  else if (act == FWT_GELU) activation<FWT_GELU>(g, value, slope);
+  else activation<FWT_RELU>(g, value, slope);
+}
+
 }  // namespace ff
 }  // namespace fwt

@@ -29,6 +29,13 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
 cudaError_t launch_gated(CMat x, CMat w_gate, CMat w_up, Mat h, int type, int activation, int m,
                          int f, int d, cudaStream_t st);
 
+// The same for at most kMostTokens lines of the first operand.
+constexpr int kMostTokens = 32;
+cudaError_t launch_matmul_tokens(CMat a, CMat a_scale, CMat b, CMat b_scale, int b_lines, Mat c,
+                                 int c_type, int m, int n, int k, cudaStream_t st);
+cudaError_t launch_gated_tokens(CMat x, CMat w_gate, CMat w_up, Mat h, int type, int activation,
+                                int m, int f, int d, cudaStream_t st);
+
 // dg and du into the workspace matrices, rows of ld elements (a multiple of 8).
 cudaError_t launch_gated_gradients(CMat grad, CMat x, CMat w_gate, CMat w_up, Mat dg, Mat du,
                                    int type, int activation, int m, int f, int d,

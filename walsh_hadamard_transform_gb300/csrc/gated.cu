@@ -131,12 +131,6 @@ __device__ __forceinline__ void load32(const T* row, int col, int n, uint32_t (&
   }
 }
 
-__device__ __forceinline__ void activate(int act, float g, float& value, float& slope) {
-  if (act == FWT_SILU) activation<FWT_SILU>(g, value, slope);
-  else if (act == FWT_GELU) activation<FWT_GELU>(g, value, slope);
-  else activation<FWT_RELU>(g, value, slope);
-}
-
 template <typename T, int MODE, int CG, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
@@ -153,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile int gave_up;
 
   const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
   const int steps = p.k_blocks * p.phases;
   const int tiles = p.tiles_m * p.tiles_n * p.outputs;
@@ -172,47 +166,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = tmem_base;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // copies
     [&] {
       int stage = 0;
-      uint32_t parity = 1;
+      uint32_t parity = 1, bars = smem_u32(&full[0]);
+      if constexpr (CG == 2) bars = map_to_rank(bars, 0);
       for (int index = first; index < tiles; index += stride) {
         const Tile t = tile_at(p, index, 128 * CG, kCols);
         for (int s = 0; s < steps; ++s) {
           if (!wait_or_leave(&empty[stage], parity, &gave_up)) return;
-          uint32_t bar = smem_u32(&full[stage]);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::kStage * CG);
-          if constexpr (CG == 2) bar = map_to_rank(bar, 0);
+          const uint32_t bar = bars + 8 * stage;
           const int phase = MODE == kDx ? s / p.k_blocks : 0;
           const int k = (MODE == kDx ? s - phase * p.k_blocks : s) * kTileK;
           const uint32_t a = ring + stage * C::kStage, b = a + C::kABytes;
           const CUtensorMap* ma = &maps.a[MODE == kDw ? t.output : phase];
           const int row = t.m0 + (int)rank * 128;
-          if constexpr (kAcrossA) {
-            tma_load_tile<CG>(a, ma, row, k, bar);
-            tma_load_tile<CG>(a + 8192, ma, row + 64, k, bar);
-          } else {
-            tma_load_tile<CG>(a, ma, k, row, bar);
-          }
-          if constexpr (kPairedWeights) {
-            if constexpr (CG == 2) {
-              tma_load_tile<CG>(b, &maps.b[rank], k, t.n0, bar);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::kStage * CG);
+            if constexpr (kAcrossA) {
+              tma_load_tile<CG>(a, ma, row, k, bar);
+              tma_load_tile<CG>(a + 8192, ma, row + 64, k, bar);
             } else {
-              tma_load_tile<CG>(b, &maps.b[0], k, t.n0, bar);
-              tma_load_tile<CG>(b + C::kBBytes / 2, &maps.b[1], k, t.n0, bar);
+              tma_load_tile<CG>(a, ma, k, row, bar);
             }
-          } else {
-            const CUtensorMap* mb = &maps.b[phase];
+            if constexpr (kPairedWeights) {
+              if constexpr (CG == 2) {
+                tma_load_tile<CG>(b, &maps.b[rank], k, t.n0, bar);
+              } else {
+                tma_load_tile<CG>(b, &maps.b[0], k, t.n0, bar);
+                tma_load_tile<CG>(b + C::kBBytes / 2, &maps.b[1], k, t.n0, bar);
+              }
+            } else {
+              const CUtensorMap* mb = &maps.b[phase];
 #pragma unroll
-            for (int c = 0; c < BN / CG / 64; ++c)
-              tma_load_tile<CG>(b + c * 8192, mb, t.n0 + (int)rank * (BN / CG) + 64 * c, k, bar);
+              for (int c = 0; c < BN / CG / 64; ++c)
+                tma_load_tile<CG>(b + c * 8192, mb, t.n0 + (int)rank * (BN / CG) + 64 * c, k, bar);
+            }
           }
+          __syncwarp();
           if (++stage == C::kStages) stage = 0, parity ^= 1;
         }
       }
     }();
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // products
     [&] {
       int stage = 0, acc = 0;
@@ -224,17 +221,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait_or_leave(&full[stage], parity, &gave_up)) return;
           tmem_fence_after();
           const uint32_t a = ring + stage * C::kStage, b = a + C::kABytes;
+          const uint64_t da = operand(a, kAcrossA ? 8192 : 16), db = operand(b, kAcrossB ? 8192 : 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk) {
-            // 16 along the contraction: 32 bytes of a swizzle row, or 16 rows of 128 bytes
-            const uint64_t da = operand(a + kk * (kAcrossA ? 2048 : 32), kAcrossA ? 8192 : 16);
-            const uint64_t db = operand(b + kk * (kAcrossB ? 2048 : 32), kAcrossB ? 8192 : 16);
-            mma_tile<CG, 2>(tmem + acc * BN, da, db, kIdesc, s + kk > 0);
+            for (int kk = 0; kk < kTileK / 16; ++kk)  // 16 along the contraction: 32 bytes of a
+              mma_tile<CG, 2>(tmem + acc * BN,        // swizzle row, or 16 rows (units of 16)
+                              da + kk * (kAcrossA ? 128 : 2), db + kk * (kAcrossB ? 128 : 2),
+                              kIdesc, s + kk > 0);
+            mma_commit<CG>(&empty[stage]);
           }
-          mma_commit<CG>(&empty[stage]);
+          __syncwarp();
           if (++stage == C::kStages) stage = 0, parity ^= 1;
         }
-        mma_commit<CG>(&acc_full[acc]);
+        if (elect_one()) mma_commit<CG>(&acc_full[acc]);
+        __syncwarp();
         if (++acc == 2) acc = 0, acc_parity ^= 1;
       }
     }();
@@ -402,6 +402,7 @@ cudaError_t run_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int m, int 
 
 cudaError_t launch_gated(CMat x, CMat w_gate, CMat w_up, Mat h, int type, int act, int m, int f,
                          int d, cudaStream_t st) {
+  if (m <= kMostTokens) return launch_gated_tokens(x, w_gate, w_up, h, type, act, m, f, d, st);
   GemmParams p{};
   p.m = m, p.n = f, p.act = act;
   p.out[0] = h.p, p.ld_out[0] = h.ld, p.vec = vector_rows(h);

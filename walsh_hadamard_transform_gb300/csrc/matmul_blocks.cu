@@ -60,33 +60,6 @@ struct Config {
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
-  return v;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-// Two fp32 operations at once, each rounded as the single one is.
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // The scales of one line, read four blocks at a time, one group ahead.
 struct Scales {
   const float* row;  // null: a line outside the matrix
@@ -116,47 +89,43 @@ struct Scales {
 };
 
 template <typename C>
-__device__ __forceinline__ uint32_t pack2(float2 v) {
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (std::is_same<C, __half>::value) {
-    const __half2 h = __floats2half2_rn(v.x, v.y);
+    const __half2 h = __floats2half2_rn(a, b);
     return *(const uint32_t*)&h;
   } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *(const uint32_t*)&h;
   }
 }
 
-// N values (in pairs) of a row of C to columns [col, col + N), those below n.
+// N values of a row of C to columns [col, col + N), those below n.
 template <int N>
 __device__ __forceinline__ void store_row(const BlocksParams& p, int row, int col,
-                                          const uint64_t (&acc)[N / 2]) {
+                                          const float (&acc)[N]) {
+  const bool vec = p.vec_c && col + N <= p.n;
   if (p.c_type == FWT_F32) {
     float* c = (float*)p.c + (int64_t)row * p.ld_c + col;
-    if (p.vec_c && col + N <= p.n) {
+    if (vec) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const float2 lo = unpair(acc[i / 2]), hi = unpair(acc[i / 2 + 1]);
-        *(float4*)(c + i) = make_float4(lo.x, lo.y, hi.x, hi.y);
-      }
+      for (int i = 0; i < N; i += 4)
+        *(float4*)(c + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 v = unpair(acc[i / 2]);
-        if (col + i < p.n) c[i] = i & 1 ? v.y : v.x;
-      }
+      for (int i = 0; i < N; ++i)
+        if (col + i < p.n) c[i] = acc[i];
     }
     return;
   }
   unsigned short* c = (unsigned short*)p.c + (int64_t)row * p.ld_c + col;
-  const bool half = p.c_type == FWT_F16, vec = p.vec_c && col + N <= p.n;
+  const bool half = p.c_type == FWT_F16;
 #pragma unroll
   for (int i = 0; i < N; i += 8) {
     uint32_t v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpair(acc[i / 2 + j]);
-      v[j] = half ? pack2<__half>(f) : pack2<__nv_bfloat16>(f);
-    }
+    for (int j = 0; j < 4; ++j)
+      v[j] = half ? pack2<__half>(acc[i + 2 * j], acc[i + 2 * j + 1])
+                  : pack2<__nv_bfloat16>(acc[i + 2 * j], acc[i + 2 * j + 1]);
     if (vec) {
       *(uint4*)(c + i) = make_uint4(v[0], v[1], v[2], v[3]);
     } else {
@@ -182,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float b_scales[2][LINES == 1 ? BN : 4];
 
   const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
   const int tiles = p.tiles_m * p.tiles_n;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
@@ -213,27 +182,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     if constexpr (BN == 256)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegisters));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // copies
       [&] {
         int stage = 0;
-        uint32_t parity = 1;
+        uint32_t parity = 1, bars = smem_u32(&full[0]);
+        if constexpr (CG == 2) bars = map_to_rank(bars, 0);
         for (int index = first; index < tiles; index += stride) {
           int m0, n0;
           place(index, m0, n0);
           for (int t = 0; t < p.blocks; ++t) {
             if (!wait_or_leave(&empty[stage], parity, &gave_up)) return;
-            uint32_t bar = smem_u32(&full[stage]);
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::kStage * CG);
-            if constexpr (CG == 2) bar = map_to_rank(bar, 0);
             const uint32_t a = ring + stage * C::kStage;
-            tma_load_tile<CG>(a, &maps.a, t * kBlock, m0 + (int)rank * 128, bar);
-            tma_load_tile<CG>(a + C::kABytes, &maps.b, t * kBlock, n0 + (int)rank * (BN / CG), bar);
+            const uint32_t bar = bars + 8 * stage;
+            if (elect_one()) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::kStage * CG);
+              tma_load_tile<CG>(a, &maps.a, t * kBlock, m0 + (int)rank * 128, bar);
+              tma_load_tile<CG>(a + C::kABytes, &maps.b, t * kBlock, n0 + (int)rank * (BN / CG), bar);
+            }
+            __syncwarp();
             if (++stage == C::kStages) stage = 0, parity ^= 1;
           }
         }
       }();
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // products
       [&] {
         int stage = 0, slot = 0;
@@ -244,12 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_or_leave(&full[stage], parity, &gave_up)) return;
             tmem_fence_after();
             const uint32_t a = ring + stage * C::kStage, b = a + C::kABytes;
+            const uint64_t da = operand(a, 16), db = operand(b, 16);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kBlock / 32; ++kk)  // 32 bytes of a swizzle row each
-              mma_tile<CG, 1>(tmem + slot * BN, operand(a + kk * 32, 16), operand(b + kk * 32, 16),
-                              kIdesc, kk > 0);
-            mma_commit<CG>(&empty[stage]);
-            mma_commit<CG>(&slot_full[slot]);
+              for (int kk = 0; kk < kBlock / 32; ++kk)  // 32 bytes of a swizzle row each
+                mma_tile<CG, 1>(tmem + slot * BN, da + 2 * kk, db + 2 * kk, kIdesc, kk > 0);
+              mma_commit<CG>(&empty[stage]);
+              mma_commit<CG>(&slot_full[slot]);
+            }
+            __syncwarp();
             if (++stage == C::kStages) stage = 0, parity ^= 1;
             if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
           }
@@ -279,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           sb.start(thread < BN && n0 + thread < p.n ? p.b_scale + (int64_t)(n0 + thread) * p.ld_bs
                                                     : nullptr, p.blocks, p.vec_bs);
-        uint64_t acc[kHalf / 2];
+        float acc[kHalf];
 #pragma unroll
-        for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
+        for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
         for (int t = 0; t < p.blocks; ++t) {
           float s = sa.at(t);
           buffer ^= 1;
@@ -296,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_or_leave(&scales_ready[buffer], ready_parity, &gave_up)) return;
             if (buffer) ready_parity ^= 1;
           }
-          const uint64_t ss = pair(s, s);
           if (!wait_or_leave(&slot_full[slot], slot_parity, &gave_up)) return;
           tmem_fence_after();
           const uint32_t at = tmem + slot * BN + half * kHalf + ((uint32_t)quarter << 21);
@@ -308,13 +282,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 16 < kHalf) tmem_load16(at + c + 16, v[(c / 16 + 1) & 1]);
             const uint32_t(&x)[16] = v[(c / 16) & 1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint64_t scale = ss;
+            for (int i = 0; i < 16; i += 4) {
+              float4 f = make_float4(s, s, s, s);
               if constexpr (LINES == 1) {
-                const float2 f = *(const float2*)&b_scales[buffer][half * kHalf + c + 2 * i];
-                scale = mul2(ss, pair(f.x, f.y));
+                f = *(const float4*)&b_scales[buffer][half * kHalf + c + i];
+                f.x *= s, f.y *= s, f.z *= s, f.w *= s;
               }
-              acc[c / 2 + i] = fma2(pair(x[2 * i], x[2 * i + 1]), scale, acc[c / 2 + i]);
+              float* sum = &acc[c + i];
+              sum[0] = fmaf(__uint_as_float(x[i]), f.x, sum[0]);
+              sum[1] = fmaf(__uint_as_float(x[i + 1]), f.y, sum[1]);
+              sum[2] = fmaf(__uint_as_float(x[i + 2]), f.z, sum[2]);
+              sum[3] = fmaf(__uint_as_float(x[i + 3]), f.w, sum[3]);
             }
           }
           tmem_fence_before();
@@ -370,6 +348,8 @@ bool vector_rows(const void* p, int64_t ld_bytes) {
 
 cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int b_lines, Mat c,
                                  int c_type, int m, int n, int k, cudaStream_t st) {
+  if (m <= kMostTokens)
+    return launch_matmul_tokens(a, a_scale, b, b_scale, b_lines, c, c_type, m, n, k, st);
   BlocksParams p{};
   p.a_scale = (const float*)a_scale.p, p.ld_as = a_scale.ld;
   p.b_scale = (const float*)b_scale.p, p.ld_bs = b_scale.ld;

@@ -21,6 +21,15 @@ namespace ff {
 constexpr uint32_t kSwizzleRow = 128;   // bytes
 constexpr uint32_t kSwizzleAtom = 1024; // bytes, 8 rows
 
+// True in one thread of the (whole) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -39,8 +48,10 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Says that reads of tensor memory are done (after tmem_fence_before()); orders no other
+// memory, as a release at cluster scope would (measured: a thousand clocks).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
@@ -196,14 +207,35 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 
 // ---- waits ---------------------------------------------------------------------------
 
-// A wait of a role of a kernel: bounded, and over at once when another role of the CTA has
-// given up.  false: leave the role's loop.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// A wait of a whole warp: at most about a second, and over at once when another role of the
+// CTA has given up.  false, in every lane: leave the role's loop.
 __device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (*gave_up) return false;
-  if (mbar_wait_bounded(bar, parity)) return true;
-  *gave_up = 1;
-  return false;
+  bool done = mbar_poll(bar, parity);
+  if (!done) {
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 1; i < (1u << 28); ++i) {
+      done = mbar_poll(bar, parity);
+      if (done) break;
+      if ((i & 63u) == 0 && (*gave_up || global_ns() - t0 > 1000000000ull)) break;
+    }
+    if (!done && !*gave_up) {
+      atomicOr(&g_device_error, kErrTmaTimeout);
+      *gave_up = 1;
+    }
+  }
+  return __all_sync(~0u, done);
 }
 
 // After a wait that gave up: time for copies and products in flight to end before the
