@@ -29,7 +29,8 @@ namespace ff {
 namespace {
 
 constexpr int kBlock = 128;  // elements of the contraction that share a scale: one stage
-constexpr int kRingBytes = 196608;
+constexpr int kSharedBytes = 230400;  // of 232448: the rest is for alignment and barriers
+constexpr int kStoreBytes = 8 * 4096;  // a piece of C of each of eight warps, see store_rows
 constexpr int kThreads = 384;  // a warp each for copies and products (of four), eight for the sums
 // Registers of a thread: 168 at launch (384 threads), moved from the first warpgroup to the
 // two that hold 128 sums a thread: 128 * 72 + 256 * 216 = 384 * 168.
@@ -51,42 +52,34 @@ struct BlocksMaps {
   CUtensorMap a, b;
 };
 
-template <int CG, int BN>
+// CG: CTAs that share a tile.  BN: its columns.  LINES: lines of b that share a scale.
+template <int CG, int BN, int LINES>
 struct Config {
   static constexpr int kABytes = 128 * 128, kBBytes = BN / CG * 128;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = kRingBytes / kStage;
   static constexpr int kSlots = 512 / BN > 4 ? 4 : 512 / BN;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+  // scales of four blocks: one of a for each row; of b for each column, or each 128
+  static constexpr int kBScales = LINES == 1 ? BN : BN == 256 ? 2 : 1;
+  static constexpr int kScales = 4 * (128 + kBScales);  // floats
+  static constexpr int kFixed = 2 * kScales * 4 + kStoreBytes;
+  static constexpr int kStages = (kSharedBytes - kFixed) / kStage < 8 ? (kSharedBytes - kFixed) / kStage : 8;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kFixed + 1024;
 };
 
-// The scales of one line, read four blocks at a time, one group ahead.
-struct Scales {
-  const float* row;  // null: a line outside the matrix
-  int blocks;
-  bool vec;
-  float4 now, next;
-
-  __device__ __forceinline__ float4 group(int t) const {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!row || t >= blocks) return v;
-    if (vec && t + 4 <= blocks) return __ldg((const float4*)(row + t));
-    v.x = __ldg(row + t);
-    if (t + 1 < blocks) v.y = __ldg(row + t + 1);
-    if (t + 2 < blocks) v.z = __ldg(row + t + 2);
-    if (t + 3 < blocks) v.w = __ldg(row + t + 3);
-    return v;
-  }
-  __device__ __forceinline__ void start(const float* r, int n, bool v) {
-    row = r, blocks = n, vec = v;
-    next = group(0);
-  }
-  // The scale of block t; called for t = 0, 1, 2, ...
-  __device__ __forceinline__ float at(int t) {
-    if ((t & 3) == 0) now = next, next = group(t + 4);
-    return (t & 2) ? ((t & 1) ? now.w : now.z) : ((t & 1) ? now.y : now.x);
-  }
-};
+// The scales of four blocks of one line from block `t` on; zero past the line's end and for
+// lines outside the matrix.
+__device__ __forceinline__ float4 scales4(const float* base, int64_t ld, int line, int lines, int t,
+                                          int blocks, bool vec) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (line >= lines) return v;
+  const float* row = base + line * ld + t;
+  if (vec && t + 4 <= blocks) return __ldg((const float4*)row);
+  v.x = __ldg(row);
+  if (t + 1 < blocks) v.y = __ldg(row + 1);
+  if (t + 2 < blocks) v.z = __ldg(row + 2);
+  if (t + 3 < blocks) v.w = __ldg(row + 3);
+  return v;
+}
 
 template <typename C>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -99,58 +92,73 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-// N values of a row of C to columns [col, col + N), those below n.
-template <int N>
-__device__ __forceinline__ void store_row(const BlocksParams& p, int row, int col,
-                                          const float (&acc)[N]) {
-  const bool vec = p.vec_c && col + N <= p.n;
-  if (p.c_type == FWT_F32) {
-    float* c = (float*)p.c + (int64_t)row * p.ld_c + col;
-    if (vec) {
+// A warp's rows of C, N columns from `col`, one row a thread: in pieces of 128 bytes a row
+// through the warp's 4 KB of shared memory (16-byte chunks swizzled by row), so that global
+// stores are whole 128-byte lines.  Stored from the registers as they lie, 16 bytes a row and
+// instruction, they took a quarter of a tile's time.
+template <int N, typename C>
+__device__ __forceinline__ void store_rows(const BlocksParams& p, uint8_t* piece, int row0, int lane,
+                                           int col, const float (&acc)[N]) {
+  constexpr int kPiece = 128 / sizeof(C) < N ? 128 / sizeof(C) : N;  // columns
+  constexpr int kChunks = kPiece * sizeof(C) / 16, kPer = 16 / sizeof(C);
+  const bool vec = p.vec_c != 0;
 #pragma unroll
-      for (int i = 0; i < N; i += 4)
-        *(float4*)(c + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-    } else {
+  for (int c = 0; c < N; c += kPiece) {
+    if (col + c >= p.n) return;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (col + i < p.n) c[i] = acc[i];
+    for (int i = 0; i < kChunks; ++i) {
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(C) == 4)
+          v[j] = __float_as_uint(acc[c + i * kPer + j]);
+        else
+          v[j] = pack2<C>(acc[c + i * kPer + 2 * j], acc[c + i * kPer + 2 * j + 1]);
+      }
+      *(uint4*)(piece + lane * 128 + ((i ^ (lane & 7)) & (kChunks - 1)) * 16) =
+          make_uint4(v[0], v[1], v[2], v[3]);
     }
-    return;
-  }
-  unsigned short* c = (unsigned short*)p.c + (int64_t)row * p.ld_c + col;
-  const bool half = p.c_type == FWT_F16;
+    __syncwarp();
 #pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    uint32_t v[4];
+    for (int i = 0; i < kChunks; ++i) {
+      const int r = i * (32 / kChunks) + lane / kChunks, chunk = lane & (kChunks - 1);
+      const uint4 v = *(const uint4*)(piece + r * 128 + ((chunk ^ (r & 7)) & (kChunks - 1)) * 16);
+      const int at = col + c + chunk * kPer;
+      if (row0 + r < p.m && at < p.n) {
+        C* out = (C*)p.c + (int64_t)(row0 + r) * p.ld_c + at;
+        if (vec && at + kPer <= p.n) {
+          *(uint4*)out = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = half ? pack2<__half>(acc[i + 2 * j], acc[i + 2 * j + 1])
-                  : pack2<__nv_bfloat16>(acc[i + 2 * j], acc[i + 2 * j + 1]);
-    if (vec) {
-      *(uint4*)(c + i) = make_uint4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + i + j < p.n) c[i + j] = (unsigned short)(v[j / 2] >> (16 * (j & 1)));
+          for (int j = 0; j < kPer; ++j)
+            if (at + j < p.n) {
+              if constexpr (sizeof(C) == 4) *(uint32_t*)(out + j) = w[j];
+              else *(unsigned short*)(out + j) = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
+            }
+        }
+      }
     }
+    __syncwarp();
   }
 }
 
 template <int CG, int BN, int LINES>
 __global__ void __launch_bounds__(kThreads, 1)
     blocks_kernel(const __grid_constant__ BlocksMaps maps, const BlocksParams p) {
-  using C = Config<CG, BN>;
+  using C = Config<CG, BN, LINES>;
   constexpr uint32_t kIdesc = instruction(0, false, false, 128 * CG, BN);
   constexpr int kHalf = BN / 2;  // columns of a warp
 
   extern __shared__ uint8_t dynamic[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], slot_full[C::kSlots],
-      slot_empty[C::kSlots], scales_ready[2];
+      slot_empty[C::kSlots], scales_full[2], scales_empty[2];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
-  __shared__ __align__(16) float b_scales[2][LINES == 1 ? BN : 4];
 
   const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
+  uint8_t* after_ring = dynamic + (ring - smem_u32(dynamic)) + C::kStages * C::kStage;
+  float* scales = (float*)(after_ring + kStoreBytes);  // [2][4][rows, then of b]
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
   const int tiles = p.tiles_m * p.tiles_n;
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < C::kSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], 8 * CG);
-    for (int i = 0; i < 2; ++i) mbar_init(&scales_ready[i], 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&scales_full[i], 2), mbar_init(&scales_empty[i], 8);
     gave_up = 0;
     prefetch_map(&maps.a), prefetch_map(&maps.b);
   }
@@ -212,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0, slot_parity = 1;
         for (int index = first; index < tiles; index += stride) {
           for (int t = 0; t < p.blocks; ++t) {
-            if (!wait_or_leave(&slot_empty[slot], slot_parity, &gave_up)) return;
             if (!wait_or_leave(&full[stage], parity, &gave_up)) return;
+            if (!wait_or_leave(&slot_empty[slot], slot_parity, &gave_up)) return;
             tmem_fence_after();
             const uint32_t a = ring + stage * C::kStage, b = a + C::kABytes;
             const uint64_t da = operand(a, 16), db = operand(b, 16);
@@ -230,62 +238,82 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }();
+    } else if (warp >= 2) {
+      // scales: two warps bring those of four blocks at a time to shared memory, a row of
+      // kScales / 4 floats for each block
+      [&] {
+        int buffer = 0;
+        uint32_t parity = 1;
+        const int thread = threadIdx.x - 64;
+        constexpr int kRow = C::kScales / 4;
+        for (int index = first; index < tiles; index += stride) {
+          int m0, n0;
+          place(index, m0, n0);
+          for (int t = 0; t < p.blocks; t += 4) {
+            float4 a[2], b[LINES == 1 ? BN / 64 : 1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              a[i] = scales4(p.a_scale, p.ld_as, m0 + (int)rank * 128 + thread + 64 * i, p.m, t,
+                             p.blocks, p.vec_as);
+            if constexpr (LINES == 1) {
+#pragma unroll
+              for (int i = 0; i < BN / 64; ++i)
+                b[i] = scales4(p.b_scale, p.ld_bs, n0 + thread + 64 * i, p.n, t, p.blocks, p.vec_bs);
+            } else if (thread < C::kBScales) {
+              b[0] = scales4(p.b_scale, p.ld_bs, n0 / 128 + thread, (p.n + 127) / 128, t, p.blocks,
+                             p.vec_bs);
+            }
+            if (!wait_or_leave(&scales_empty[buffer], parity, &gave_up)) return;
+            float* to = scales + buffer * C::kScales;
+            auto put = [&](int at, float4 v) {
+              to[at] = v.x, to[at + kRow] = v.y, to[at + 2 * kRow] = v.z, to[at + 3 * kRow] = v.w;
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i) put(thread + 64 * i, a[i]);
+            if constexpr (LINES == 1) {
+#pragma unroll
+              for (int i = 0; i < BN / 64; ++i) put(128 + thread + 64 * i, b[i]);
+            } else if (thread < C::kBScales) {
+              put(128 + thread, b[0]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&scales_full[buffer]);
+            buffer ^= 1;
+            if (buffer == 0) parity ^= 1;
+          }
+        }
+      }();
     }
   } else {
     if constexpr (BN == 256)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegisters));
     // sums: warp w reads lanes 32 (w mod 4) on, a row of the tile each, and half its columns
     [&] {
-      int slot = 0, buffer = 1;
-      uint32_t slot_parity = 0, ready_parity = 0;
+      int slot = 0, buffer = 0;
+      uint32_t slot_parity = 0, parity = 0;
       const int quarter = warp & 3, half = (warp - 4) >> 2;
-      const int thread = threadIdx.x - 128;
       uint32_t release = smem_u32(&slot_empty[0]);
       if constexpr (CG == 2) release = map_to_rank(release, 0);
+      uint8_t* piece = after_ring + (warp - 4) * 4096;
+      const uint32_t lanes = tmem + half * kHalf + ((uint32_t)quarter << 21);
       for (int index = first; index < tiles; index += stride) {
         int m0, n0;
         place(index, m0, n0);
-        const int row = m0 + (int)rank * 128 + quarter * 32 + lane;
-        const int col = n0 + half * kHalf;
-        Scales sa, sb;
-        sa.start(row < p.m ? p.a_scale + (int64_t)row * p.ld_as : nullptr, p.blocks, p.vec_as);
-        if constexpr (LINES == 128)
-          sb.start(col < p.n ? p.b_scale + (int64_t)(col / 128) * p.ld_bs : nullptr, p.blocks, p.vec_bs);
-        else
-          sb.start(thread < BN && n0 + thread < p.n ? p.b_scale + (int64_t)(n0 + thread) * p.ld_bs
-                                                    : nullptr, p.blocks, p.vec_bs);
         float acc[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
         for (int t = 0; t < p.blocks; ++t) {
-          float s = sa.at(t);
-          buffer ^= 1;
-          const float sbt = sb.at(t);
-          if constexpr (LINES == 128) {
-            s *= sbt;
-          } else {
-            if (thread < BN) b_scales[buffer][thread] = sbt;
-            // a warp that is here for t + 2 has seen every warp arrive for t + 1, done with t
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&scales_ready[buffer]);
-            if (!wait_or_leave(&scales_ready[buffer], ready_parity, &gave_up)) return;
-            if (buffer) ready_parity ^= 1;
-          }
-          if (!wait_or_leave(&slot_full[slot], slot_parity, &gave_up)) return;
-          tmem_fence_after();
-          const uint32_t at = tmem + slot * BN + half * kHalf + ((uint32_t)quarter << 21);
-          uint32_t v[2][16];
-          tmem_load16(at, v[0]);
+          if ((t & 3) == 0 && !wait_or_leave(&scales_full[buffer], parity, &gave_up)) return;
+          const float* row = scales + buffer * C::kScales + (t & 3) * (C::kScales / 4);
+          float s = row[quarter * 32 + lane];
+          if constexpr (LINES == 128) s *= row[128 + (BN == 256 ? half : 0)];
+          uint32_t v[2][32];
+          auto add = [&](int c, const uint32_t(&x)[32]) {
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 16) {
-            tmem_wait_loads();
-            if (c + 16 < kHalf) tmem_load16(at + c + 16, v[(c / 16 + 1) & 1]);
-            const uint32_t(&x)[16] = v[(c / 16) & 1];
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < 32; i += 4) {
               float4 f = make_float4(s, s, s, s);
               if constexpr (LINES == 1) {
-                f = *(const float4*)&b_scales[buffer][half * kHalf + c + i];
+                f = *(const float4*)&row[128 + half * kHalf + c + i];
                 f.x *= s, f.y *= s, f.z *= s, f.w *= s;
               }
               float* sum = &acc[c + i];
@@ -294,17 +322,43 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[2] = fmaf(__uint_as_float(x[i + 2]), f.z, sum[2]);
               sum[3] = fmaf(__uint_as_float(x[i + 3]), f.w, sum[3]);
             }
+          };
+          if (!wait_or_leave(&slot_full[slot], slot_parity, &gave_up)) return;
+          tmem_fence_after();
+          const uint32_t at = lanes + slot * BN;
+          tmem_load32(at, v[0]);
+          if constexpr (kHalf >= 64) tmem_load32(at + 32, v[1]);
+          tmem_wait_loads();
+          if constexpr (kHalf == 128) {
+            add(0, v[0]);
+            tmem_load32(at + 64, v[0]);
+            add(32, v[1]);
+            tmem_load32(at + 96, v[1]);
+            tmem_wait_loads();
           }
+          // the slot is read: it goes back before the last sums, as the next block's products
+          // but one wait for it
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) {
             if constexpr (CG == 2) mbar_arrive_cluster(release + 8 * slot);
             else mbar_arrive(&slot_empty[slot]);
           }
+          __syncwarp();
           if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
+          add(kHalf == 128 ? 64 : 0, v[0]);
+          if constexpr (kHalf >= 64) add(kHalf == 128 ? 96 : 32, v[1]);
+          if ((t & 3) == 3 || t + 1 == p.blocks) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&scales_empty[buffer]);
+            buffer ^= 1;
+            if (buffer == 0) parity ^= 1;
+          }
         }
-        if (row < p.m && col < p.n) store_row<kHalf>(p, row, col, acc);
-        __syncwarp();
+        const int row0 = m0 + (int)rank * 128 + quarter * 32, col = n0 + half * kHalf;
+        if (p.c_type == FWT_F32) store_rows<kHalf, float>(p, piece, row0, lane, col, acc);
+        else if (p.c_type == FWT_BF16) store_rows<kHalf, __nv_bfloat16>(p, piece, row0, lane, col, acc);
+        else store_rows<kHalf, __half>(p, piece, row0, lane, col, acc);
       }
     }();
   }
@@ -327,7 +381,7 @@ cudaError_t launch_config(const BlocksMaps& maps, BlocksParams p, cudaStream_t s
   if (tiles > 0x7fffff00) return cudaErrorInvalidConfiguration;
   const int64_t grid = std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
   return launch_cluster(blocks_kernel<CG, BN, LINES>, ready, (unsigned)grid, kThreads,
-                        Config<CG, BN>::kSmem, CG, st, maps, p);
+                        Config<CG, BN, LINES>::kSmem, CG, st, maps, p);
 }
 
 template <int CG, int BN>

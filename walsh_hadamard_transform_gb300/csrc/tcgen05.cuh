@@ -223,7 +223,8 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
 // CTA has given up.  false, in every lane: leave the role's loop.
 __device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
   bool done = mbar_poll(bar, parity);
-  if (!done) {
+  for (int i = 0; i < 32 && !done; ++i) done = mbar_poll(bar, parity);
+  if (!done) {  // the timer is slow to read: not before it is needed
     const unsigned long long t0 = global_ns();
     for (uint32_t i = 1; i < (1u << 28); ++i) {
       done = mbar_poll(bar, parity);
