@@ -16,6 +16,8 @@
 // and g + 8.  So inputs are 16-byte loads, codes 8-byte stores, and only the maximum of a
 // block crosses lanes (two shuffles a line, where butterflies across lanes would take four
 // shuffles an element and be bound by them).  Bound: HBM.
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -24,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "feed_forward.cuh"
+#include "ff_host.cuh"
 #include "fwt.h"
 
 namespace fwt {
@@ -41,7 +44,8 @@ struct QuantizeParams {
   int blocks, strips;    // blocks of 128 along the axis, strips of 16 lines
   int r;
   float norm;  // 2^(-r/2)
-  int vec;     // rows of x start on 16-byte boundaries
+  int rounds;  // blocks a warp goes through
+  int vec;     // rows of x start on 16-byte boundaries (axis 0: on two elements')
 };
 
 template <typename T>
@@ -86,55 +90,103 @@ __device__ __forceinline__ uint32_t sign16(int ek, int en, int r) {
   return one | ((__popc(ek & en & low) & 1) << 15);
 }
 
-// Eight elements along the axis from position `pos` of line `line`, as packed 16-bit pairs
-// (one set for each piece).  Zero outside the matrix.
+// What a thread loads of one block: 8 consecutive elements in each group of 32 of its two
+// lines.  Axis 1: lines g and g + 8 of the strip, 16 bytes along a row at a time.  Axis 0:
+// lines 2 g and 2 g + 1, which lie side by side in every row of x, both with one load.
 template <typename T, int AXIS>
-__device__ __forceinline__ void load8(const QuantizeParams& p, int line, int pos,
-                                      uint32_t (&out)[Input<T>::kPieces][4]) {
-  const T* x = (const T*)p.x;
-  if constexpr (sizeof(T) == 2) {
-    if (AXIS == 1 && p.vec && line < p.nl && pos + 8 <= p.length) {
-      const uint4 v = __ldg((const uint4*)(x + (int64_t)line * p.ld_x + pos));
-      out[0][0] = v.x, out[0][1] = v.y, out[0][2] = v.z, out[0][3] = v.w;
-      return;
-    }
-    uint32_t e[8];
+struct Block {
+  uint32_t w[4][2 * sizeof(T)][2];  // group; axis 1: words of a line, line; axis 0: see below
+
+  static __device__ __forceinline__ int line(int strip, int g, int s) {
+    return strip * 16 + (AXIS == 1 ? g + 8 * s : 2 * g + s);
+  }
+
+  // Zero outside the matrix.
+  __device__ __forceinline__ void load(const QuantizeParams& p, int strip, int block, int g, int t) {
+    constexpr int kWords = 2 * (int)sizeof(T);  // 32-bit words of 8 elements
+    const T* x = (const T*)p.x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t at = AXIS == 1 ? (int64_t)line * p.ld_x + pos + j
-                                   : (int64_t)(pos + j) * p.ld_x + line;
-      e[j] = line < p.nl && pos + j < p.length ? __ldg((const unsigned short*)x + at) : 0;
-    }
+    for (int grp = 0; grp < 4; ++grp) {
+      const int pos = block * 128 + 32 * grp + 8 * t;
+      if constexpr (AXIS == 1) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[0][j] = e[2 * j] | (e[2 * j + 1] << 16);
-  } else {
-    float e[8];
-    if (AXIS == 1 && p.vec && line < p.nl && pos + 8 <= p.length) {
-      const float4* v = (const float4*)(x + (int64_t)line * p.ld_x + pos);
-      const float4 lo = __ldg(v), hi = __ldg(v + 1);
-      e[0] = lo.x, e[1] = lo.y, e[2] = lo.z, e[3] = lo.w;
-      e[4] = hi.x, e[5] = hi.y, e[6] = hi.z, e[7] = hi.w;
-    } else {
+        for (int s = 0; s < 2; ++s) {
+          const int l = line(strip, g, s);
+          const T* from = x + (int64_t)l * p.ld_x + pos;
+          if (p.vec && l < p.nl && pos + 8 <= p.length) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t at = AXIS == 1 ? (int64_t)line * p.ld_x + pos + j
-                                     : (int64_t)(pos + j) * p.ld_x + line;
-        e[j] = line < p.nl && pos + j < p.length ? __ldg((const float*)x + at) : 0.f;
-      }
-    }
-    // Truncation leaves no piece larger than its input; 8 + 8 + 8 significant bits.
+            for (int i = 0; i < kWords; i += 4) {
+              const uint4 v = __ldg((const uint4*)from + i / 4);
+              w[grp][i][s] = v.x, w[grp][i + 1][s] = v.y, w[grp][i + 2][s] = v.z, w[grp][i + 3][s] = v.w;
+            }
+          } else {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+            for (int i = 0; i < kWords; ++i) w[grp][i][s] = 0;
+            if (l < p.nl) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = __float_as_uint(e[2 * j]) & 0xffff0000u;
-        const uint32_t hi = __float_as_uint(e[2 * j + 1]) & 0xffff0000u;
-        out[k][j] = (lo >> 16) | hi;
-        e[2 * j] -= __uint_as_float(lo);
-        e[2 * j + 1] -= __uint_as_float(hi);
+              for (int j = 0; j < 8; ++j)
+                if (pos + j < p.length) {
+                  if constexpr (sizeof(T) == 2)
+                    w[grp][j / 2][s] |= (uint32_t)__ldg((const unsigned short*)from + j) << (16 * (j & 1));
+                  else
+                    w[grp][j][s] = __ldg((const uint32_t*)from + j);
+                }
+            }
+          }
+        }
+      } else {
+        // element j of both lines: one word (16-bit types, w[..][j / 2][j & 1]) or two
+        const int l = line(strip, g, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const T* from = x + (int64_t)(pos + j) * p.ld_x + l;
+          const bool in = pos + j < p.length;
+          if constexpr (sizeof(T) == 2) {
+            uint32_t v = 0;
+            if (p.vec && in && l + 1 < p.nl) {
+              v = __ldg((const uint32_t*)from);
+            } else {
+              if (in && l < p.nl) v = __ldg((const unsigned short*)from);
+              if (in && l + 1 < p.nl) v |= (uint32_t)__ldg((const unsigned short*)from + 1) << 16;
+            }
+            w[grp][j / 2][j & 1] = v;
+          } else {
+            uint2 v = make_uint2(0, 0);
+            if (p.vec && in && l + 1 < p.nl) {
+              v = __ldg((const uint2*)from);
+            } else {
+              if (in && l < p.nl) v.x = __ldg((const uint32_t*)from);
+              if (in && l + 1 < p.nl) v.y = __ldg((const uint32_t*)from + 1);
+            }
+            w[grp][j][0] = v.x, w[grp][j][1] = v.y;
+          }
+        }
       }
     }
   }
+
+  // Elements 2 i and 2 i + 1 of a group of line s, as 16-bit pairs: the k-th piece.  An fp32
+  // input is taken apart as it is read: call with k = 0, 1, 2 in turn.  Truncation leaves no
+  // piece larger than its input, and 8 + 8 + 8 significant bits hold it exactly.
+  __device__ __forceinline__ uint32_t pair(int grp, int i, int s) {
+    if constexpr (sizeof(T) == 2) {
+      if constexpr (AXIS == 1) return w[grp][i][s];
+      else return __byte_perm(w[grp][i][0], w[grp][i][1], s ? 0x7632 : 0x5410);
+    } else {
+      uint32_t &lo = w[grp][2 * i][s], &hi = w[grp][2 * i + 1][s];
+      const uint32_t top_lo = lo & 0xffff0000u, top_hi = hi & 0xffff0000u;
+      lo = __float_as_uint(__uint_as_float(lo) - __uint_as_float(top_lo));
+      hi = __float_as_uint(__uint_as_float(hi) - __uint_as_float(top_hi));
+      return (top_lo >> 16) | top_hi;
+    }
+  }
+};
+
+// max(|a|, b), NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(b));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
@@ -144,31 +196,27 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// Warps of a CTA: consecutive blocks of one strip (axis 1) or consecutive strips of one
-// block (axis 0), so that a CTA reads long runs of rows; with 128 lines to a scale, the
-// eight strips of one tile.
+// Warps of a CTA: consecutive blocks of one strip (axis 1) or consecutive strips (axis 0), so
+// that a CTA reads long runs of rows; with 128 lines to a scale, the eight strips of one tile.
+// Each then goes on along the axis, `rounds` blocks in all, the loads of the next block on
+// their way while one is worked on.
 template <int LINES>
 constexpr int kWarps = LINES == 1 ? 4 : 8;
 
 template <typename T, int AXIS, int LINES>
 __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizeParams p) {
   constexpr int W = kWarps<LINES>;
+  constexpr bool kAhead = sizeof(T) == 2;  // fp32 blocks take twice the registers
+  constexpr int kStep = AXIS == 1 && LINES == 1 ? W : 1;
   using M = typename Input<T>::Mma;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  int strip, block;
-  if constexpr (LINES == 128) {
-    block = blockIdx.x % p.blocks;
-    strip = blockIdx.x / p.blocks * W + warp;
-  } else if constexpr (AXIS == 1) {
-    const int per = (p.blocks + W - 1) / W;
-    block = blockIdx.x % per * W + warp;
-    strip = blockIdx.x / per;
-  } else {
-    const int per = (p.strips + W - 1) / W;
-    strip = blockIdx.x % per * W + warp;
-    block = blockIdx.x / per;
-  }
+  const int per = (p.blocks + kStep * p.rounds - 1) / (kStep * p.rounds);  // CTAs along the axis
+  int block = blockIdx.x % per * (kStep * p.rounds);
+  int strip = blockIdx.x / per;
+  if constexpr (kStep == W) block += warp;
+  else strip = strip * W + warp;
   if (LINES == 1 && (block >= p.blocks || strip >= p.strips)) return;
+  const int end = min(p.blocks, block + kStep * p.rounds);
 
   uint32_t b[2][2];
 #pragma unroll
@@ -178,117 +226,126 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
     for (int h = 0; h < 2; ++h)
       b[n][h] = sign16<M>(8 * t + 2 * h, en, p.r) | (sign16<M>(8 * t + 2 * h + 1, en, p.r) << 16);
   }
+  const int lines[2] = {Block<T, AXIS>::line(strip, g, 0), Block<T, AXIS>::line(strip, g, 1)};
 
-  const int line = strip * 16 + g, pos = block * 128 + 8 * t;
-  float y[4][2][2][4];  // group of 32, bit 2, bit 1, (line, bit 0)
+  Block<T, AXIS> x;
+  x.load(p, strip, block, g, t);
+  for (int round = 0; block < end; block += kStep, ++round) {
+    float y[4][2][2][4];  // group of 32, bit 2, bit 1, (line, bit 0)
 #pragma unroll
-  for (int grp = 0; grp < 4; ++grp) {
-    uint32_t u[Input<T>::kPieces][4], v[Input<T>::kPieces][4];
-    load8<T, AXIS>(p, line, pos + 32 * grp, u);
-    load8<T, AXIS>(p, line + 8, pos + 32 * grp, v);
+    for (int grp = 0; grp < 4; ++grp)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[grp][h][n][i] = 0.f;
+          for (int i = 0; i < 4; ++i) y[grp][h][n][i] = 0.f;
 #pragma unroll
-        for (int k = Input<T>::kPieces - 1; k >= 0; --k) {
-          const uint32_t a[4] = {u[k][2 * h], v[k][2 * h], u[k][2 * h + 1], v[k][2 * h + 1]};
-          mma16<M>(y[grp][h][n], a, b[n]);
+        for (int k = 0; k < Input<T>::kPieces; ++k) {
+          const uint32_t a[4] = {x.pair(grp, 2 * h, 0), x.pair(grp, 2 * h, 1),
+                                 x.pair(grp, 2 * h + 1, 0), x.pair(grp, 2 * h + 1, 1)};
+          mma16<M>(y[grp][h][0], a, b[0]);
+          mma16<M>(y[grp][h][1], a, b[1]);
         }
       }
-  }
-#pragma unroll
-  for (int grp = 0; grp < 4; ++grp)
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = y[grp][0][n][i], hi = y[grp][1][n][i];
-        if (p.r > 2) y[grp][0][n][i] = lo + hi, y[grp][1][n][i] = lo - hi;
-      }
-#pragma unroll
-  for (int bit = 1; bit < 4; bit <<= 1)
-    if (p.r > (bit == 1 ? 5 : 6)) {
+    if (kAhead && block + kStep < end) x.load(p, strip, block + kStep, g, t);
+
+    if (p.r > 2) {
 #pragma unroll
       for (int grp = 0; grp < 4; ++grp)
-        if (!(grp & bit))
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float lo = y[grp][h][n][i], hi = y[grp | bit][h][n][i];
-                y[grp][h][n][i] = lo + hi, y[grp | bit][h][n][i] = lo - hi;
-              }
+          for (int i = 0; i < 4; ++i) {
+            const float lo = y[grp][0][n][i], hi = y[grp][1][n][i];
+            y[grp][0][n][i] = lo + hi, y[grp][1][n][i] = lo - hi;
+          }
     }
-
-  // The maximum by the bits of |y|: a NaN's are above every number's.
-  uint32_t top[2] = {0, 0};
 #pragma unroll
-  for (int grp = 0; grp < 4; ++grp)
+    for (int bit = 1; bit < 4; bit <<= 1)
+      if (p.r > (bit == 1 ? 5 : 6)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int grp = 0; grp < 4; ++grp)
+          if (!(grp & bit))
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[grp][h][n][i] *= p.norm;
-          top[i >> 1] = max(top[i >> 1], __float_as_uint(y[grp][h][n][i]) & 0x7fffffffu);
-        }
+              for (int n = 0; n < 2; ++n)
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    top[s] = max(top[s], __shfl_xor_sync(~0u, top[s], 1));
-    top[s] = max(top[s], __shfl_xor_sync(~0u, top[s], 2));
-  }
-  if constexpr (LINES == 128) {
-    __shared__ uint32_t tops[W];
-    uint32_t m = max(top[0], top[1]);
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
-    if (lane == 0) tops[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) m = max(m, tops[w]);
-    top[0] = top[1] = m;
-  }
-
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int l = line + 8 * s;
-    float scale = fmaxf(__fdiv_rn(__uint_as_float(top[s]), 448.f), 0x1p-126f);
-    if (top[s] >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
-    const float inv = __fdiv_rn(1.f, scale);
-    if (LINES == 1 ? t == 0 && l < p.nl : threadIdx.x == 0 && s == 0)
-      p.scale[(int64_t)(LINES == 1 ? l : l / 128) * p.ld_scale + block] = scale;
-    if (l >= p.nl) continue;
-    uint8_t* q = p.q + (int64_t)l * p.ld_q;
-#pragma unroll
-    for (int grp = 0; grp < 4; ++grp) {
-      uint2 code;
-      code.x = codes4(y[grp][0][0][2 * s] * inv, y[grp][0][0][2 * s + 1] * inv,
-                      y[grp][0][1][2 * s] * inv, y[grp][0][1][2 * s + 1] * inv);
-      code.y = codes4(y[grp][1][0][2 * s] * inv, y[grp][1][0][2 * s + 1] * inv,
-                      y[grp][1][1][2 * s] * inv, y[grp][1][1][2 * s + 1] * inv);
-      const int at = pos + 32 * grp;
-      if (at + 8 <= p.full) {
-        *(uint2*)(q + at) = code;
-      } else {
-        for (int j = 0; j < 8 && at + j < p.full; ++j)
-          q[at + j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
+                for (int i = 0; i < 4; ++i) {
+                  const float lo = y[grp][h][n][i], hi = y[grp | bit][h][n][i];
+                  y[grp][h][n][i] = lo + hi, y[grp | bit][h][n][i] = lo - hi;
+                }
       }
+
+    // 2^(-r/2) is left to the scale: |y| is the largest where the normalised value is
+    float top[2] = {0.f, 0.f};
+#pragma unroll
+    for (int grp = 0; grp < 4; ++grp)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i >> 1] = max_magnitude(y[grp][h][n][i], top[i >> 1]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      top[s] = max_magnitude(__shfl_xor_sync(~0u, top[s], 1), top[s]);
+      top[s] = max_magnitude(__shfl_xor_sync(~0u, top[s], 2), top[s]);
     }
+    if constexpr (LINES == 128) {
+      __shared__ float tops[2][W];  // in turn: a warp may be a round ahead of another
+      float m = max_magnitude(top[0], top[1]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) m = max_magnitude(__shfl_xor_sync(~0u, m, o), m);
+      if (lane == 0) tops[round & 1][warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) m = max_magnitude(tops[round & 1][w], m);
+      top[0] = top[1] = m;
+    }
+
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float scale = fmaxf(__fdiv_rn(top[s] * p.norm, 448.f), 0x1p-126f);
+      if (!(top[s] < INFINITY)) scale = __uint_as_float(0x7fffffffu);
+      const float factor = __fdiv_rn(1.f, scale) * p.norm;
+      const int l = lines[s];
+      if (LINES == 1 ? t == 0 && l < p.nl : threadIdx.x == 0 && s == 0)
+        p.scale[(int64_t)(LINES == 1 ? l : l / 128) * p.ld_scale + block] = scale;
+      if (l < p.nl) {
+        uint8_t* q = p.q + (int64_t)l * p.ld_q;
+#pragma unroll
+        for (int grp = 0; grp < 4; ++grp) {
+          uint2 code;
+          code.x = codes4(y[grp][0][0][2 * s] * factor, y[grp][0][0][2 * s + 1] * factor,
+                          y[grp][0][1][2 * s] * factor, y[grp][0][1][2 * s + 1] * factor);
+          code.y = codes4(y[grp][1][0][2 * s] * factor, y[grp][1][0][2 * s + 1] * factor,
+                          y[grp][1][1][2 * s] * factor, y[grp][1][1][2 * s + 1] * factor);
+          const int at = block * 128 + 32 * grp + 8 * t;
+          if (at + 8 <= p.full) {
+            *(uint2*)(q + at) = code;
+          } else {
+            for (int j = 0; j < 8 && at + j < p.full; ++j)
+              q[at + j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
+          }
+        }
+      }
+      __syncwarp();
+    }
+    if (!kAhead && block + kStep < end) x.load(p, strip, block + kStep, g, t);
   }
 }
 
 template <typename T, int AXIS, int LINES>
-cudaError_t launch(const QuantizeParams& p, cudaStream_t st) {
+cudaError_t launch(QuantizeParams p, cudaStream_t st) {
   constexpr int W = kWarps<LINES>;
-  const int64_t grid = LINES == 128 ? (int64_t)((p.strips + W - 1) / W) * p.blocks
-                       : AXIS == 1  ? (int64_t)((p.blocks + W - 1) / W) * p.strips
-                                    : (int64_t)((p.strips + W - 1) / W) * p.blocks;
+  constexpr int kStep = AXIS == 1 && LINES == 1 ? W : 1;
+  const int64_t across = kStep == W ? p.strips : (p.strips + W - 1) / W;
+  const int64_t steps = (p.blocks + kStep - 1) / kStep;
+  // as many blocks a warp as leave eight CTAs an SM, at most 4
+  p.rounds = (int)std::max<int64_t>(1, std::min<int64_t>(4, across * steps / (8 * multiprocessors())));
+  const int64_t grid = (steps + p.rounds - 1) / p.rounds * across;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   quantize_kernel<T, AXIS, LINES><<<(unsigned)grid, W * 32, 0, st>>>(p);
   return cudaGetLastError();
@@ -319,7 +376,8 @@ cudaError_t launch_quantize(CMat x, int x_type, int rows, int cols, int rot_bits
   p.r = rot_bits;
   p.norm = kNorm[rot_bits];
   const int size = x_type == FWT_F32 ? 4 : 2;
-  p.vec = ((uintptr_t)x.p & 15u) == 0 && (x.ld * size) % 16 == 0;
+  const int unit = axis ? 16 : 2 * size;
+  p.vec = (uintptr_t)x.p % (unsigned)unit == 0 && (x.ld * size) % unit == 0;
   if (x_type == FWT_F32) return launch<float>(p, axis, lines, st);
   if (x_type == FWT_BF16) return launch<__nv_bfloat16>(p, axis, lines, st);
   return launch<__half>(p, axis, lines, st);
