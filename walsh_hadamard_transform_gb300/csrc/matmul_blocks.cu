@@ -52,17 +52,19 @@ struct BlocksMaps {
   CUtensorMap a, b;
 };
 
-// CG: CTAs that share a tile.  BN: its columns.  LINES: lines of b that share a scale.
-template <int CG, int BN, int LINES>
+// CG: CTAs that share a tile.  BN: its columns.  LINES: lines of b that share a scale.  ROWS:
+// lines of a in a stage; with 64 the products read on into the next bytes for the other rows
+// of their 128, which are not stored.  SPLIT: CTAs of a cluster that share out a tile's blocks.
+template <int CG, int BN, int LINES, int ROWS, int SPLIT>
 struct Config {
-  static constexpr int kABytes = 128 * 128, kBBytes = BN / CG * 128;
+  static constexpr int kABytes = ROWS * 128, kBBytes = BN / CG * 128;
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kSlots = 512 / BN > 4 ? 4 : 512 / BN;
   // scales of four blocks: one of a for each row; of b for each column, or each 128
   static constexpr int kBScales = LINES == 1 ? BN : BN == 256 ? 2 : 1;
   static constexpr int kScales = 4 * (128 + kBScales);  // floats
   static constexpr int kFixed = 2 * kScales * 4 + kStoreBytes;
-  static constexpr int kStages = (kSharedBytes - kFixed) / kStage < 8 ? (kSharedBytes - kFixed) / kStage : 8;
+  static constexpr int kStages = (kSharedBytes - kFixed) / kStage < 12 ? (kSharedBytes - kFixed) / kStage : 12;
   static constexpr size_t kSmem = (size_t)kStages * kStage + kFixed + 1024;
 };
 
@@ -96,9 +98,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // through the warp's 4 KB of shared memory (16-byte chunks swizzled by row), so that global
 // stores are whole 128-byte lines.  Stored from the registers as they lie, 16 bytes a row and
 // instruction, they took a quarter of a tile's time.
-template <int N, typename C>
+template <typename C, int N>
 __device__ __forceinline__ void store_rows(const BlocksParams& p, uint8_t* piece, int row0, int lane,
                                            int col, const float (&acc)[N]) {
+  if constexpr (N * sizeof(C) < 16) {  // less than a chunk a row
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (row0 + lane < p.m && col + i < p.n)
+        ((C*)p.c)[(int64_t)(row0 + lane) * p.ld_c + col + i] = (C)acc[i];
+    return;
+  } else {
   constexpr int kPiece = 128 / sizeof(C) < N ? 128 / sizeof(C) : N;  // columns
   constexpr int kChunks = kPiece * sizeof(C) / 16, kPer = 16 / sizeof(C);
   const bool vec = p.vec_c != 0;
@@ -141,12 +150,14 @@ __device__ __forceinline__ void store_rows(const BlocksParams& p, uint8_t* piece
     }
     __syncwarp();
   }
+  }
 }
 
-template <int CG, int BN, int LINES>
+template <int CG, int BN, int LINES, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     blocks_kernel(const __grid_constant__ BlocksMaps maps, const BlocksParams p) {
-  using C = Config<CG, BN, LINES>;
+  using C = Config<CG, BN, LINES, ROWS, SPLIT>;
+  static_assert(CG == 1 || SPLIT == 1, "a pair shares the tile, not its blocks");
   constexpr uint32_t kIdesc = instruction(0, false, false, 128 * CG, BN);
   constexpr int kHalf = BN / 2;  // columns of a warp
 
@@ -162,7 +173,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
   const int tiles = p.tiles_m * p.tiles_n;
-  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int first = blockIdx.x / (CG * SPLIT), stride = gridDim.x / (CG * SPLIT);
+  // the CTA's blocks: all, or its share of them
+  const int share = (p.blocks + SPLIT - 1) / SPLIT;
+  const int begin = SPLIT == 1 ? 0 : min(p.blocks, (int)cluster_rank() * share);
+  const int end = SPLIT == 1 ? p.blocks : min(p.blocks, begin + share);
 
   // Tiles in groups of 8 rows of tiles, so that those in flight together share operands in L2.
   auto place = [&](int index, int& m0, int& n0) {
@@ -171,6 +186,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     index -= group * 8 * p.tiles_n;
     m0 = (group * 8 + index % height) * (128 * CG);
     n0 = index / height * BN;
+  };
+
+  bool met = false;  // whether the warp is past the cluster's first barrier
+
+  auto store = [&](uint8_t* piece, int row0, int col, const auto& sums) {
+    if (p.c_type == FWT_F32) store_rows<float>(p, piece, row0, lane, col, sums);
+    else if (p.c_type == FWT_BF16) store_rows<__nv_bfloat16>(p, piece, row0, lane, col, sums);
+    else store_rows<__half>(p, piece, row0, lane, col, sums);
   };
 
   if (threadIdx.x == 0) {
@@ -199,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int index = first; index < tiles; index += stride) {
           int m0, n0;
           place(index, m0, n0);
-          for (int t = 0; t < p.blocks; ++t) {
+          for (int t = begin; t < end; ++t) {
             if (!wait_or_leave(&empty[stage], parity, &gave_up)) return;
             const uint32_t a = ring + stage * C::kStage;
             const uint32_t bar = bars + 8 * stage;
@@ -218,23 +241,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       [&] {
         int stage = 0, slot = 0;
         uint32_t parity = 0, slot_parity = 1;
+        bool filled = false, returned = false;  // asked one block ahead
         for (int index = first; index < tiles; index += stride) {
-          for (int t = 0; t < p.blocks; ++t) {
-            if (!wait_or_leave(&full[stage], parity, &gave_up)) return;
-            if (!wait_or_leave(&slot_empty[slot], slot_parity, &gave_up)) return;
+          for (int t = begin; t < end; ++t) {
+            if (!wait_or_leave(&full[stage], parity, &gave_up, filled)) return;
+            if (!wait_or_leave(&slot_empty[slot], slot_parity, &gave_up, returned)) return;
             tmem_fence_after();
-            const uint32_t a = ring + stage * C::kStage, b = a + C::kABytes;
-            const uint64_t da = operand(a, 16), db = operand(b, 16);
+            const uint32_t a = ring + stage * C::kStage;
+            const uint64_t da = operand(a, 16), db = operand(a + C::kABytes, 16);
+            const uint32_t d = tmem + slot * BN;
+            uint64_t *emptied = &empty[stage], *summed = &slot_full[slot];
+            if (++stage == C::kStages) stage = 0, parity ^= 1;
+            if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
+            filled = mbar_test(&full[stage], parity);
+            returned = mbar_test(&slot_empty[slot], slot_parity);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kBlock / 32; ++kk)  // 32 bytes of a swizzle row each
-                mma_tile<CG, 1>(tmem + slot * BN, da + 2 * kk, db + 2 * kk, kIdesc, kk > 0);
-              mma_commit<CG>(&empty[stage]);
-              mma_commit<CG>(&slot_full[slot]);
+                mma_tile<CG, 1>(d, da + 2 * kk, db + 2 * kk, kIdesc, kk > 0);
+              mma_commit<CG>(emptied);
+              mma_commit<CG>(summed);
             }
             __syncwarp();
-            if (++stage == C::kStages) stage = 0, parity ^= 1;
-            if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
           }
         }
       }();
@@ -246,22 +274,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 1;
         const int thread = threadIdx.x - 64;
         constexpr int kRow = C::kScales / 4;
+        const bool vec_as = p.vec_as && begin % 4 == 0, vec_bs = p.vec_bs && begin % 4 == 0;
         for (int index = first; index < tiles; index += stride) {
           int m0, n0;
           place(index, m0, n0);
-          for (int t = 0; t < p.blocks; t += 4) {
+          for (int t = begin; t < end; t += 4) {
             float4 a[2], b[LINES == 1 ? BN / 64 : 1];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               a[i] = scales4(p.a_scale, p.ld_as, m0 + (int)rank * 128 + thread + 64 * i, p.m, t,
-                             p.blocks, p.vec_as);
+                             p.blocks, vec_as);
             if constexpr (LINES == 1) {
 #pragma unroll
               for (int i = 0; i < BN / 64; ++i)
-                b[i] = scales4(p.b_scale, p.ld_bs, n0 + thread + 64 * i, p.n, t, p.blocks, p.vec_bs);
+                b[i] = scales4(p.b_scale, p.ld_bs, n0 + thread + 64 * i, p.n, t, p.blocks, vec_bs);
             } else if (thread < C::kBScales) {
               b[0] = scales4(p.b_scale, p.ld_bs, n0 / 128 + thread, (p.n + 127) / 128, t, p.blocks,
-                             p.vec_bs);
+                             vec_bs);
             }
             if (!wait_or_leave(&scales_empty[buffer], parity, &gave_up)) return;
             float* to = scales + buffer * C::kScales;
@@ -302,9 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float acc[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
-        for (int t = 0; t < p.blocks; ++t) {
-          if ((t & 3) == 0 && !wait_or_leave(&scales_full[buffer], parity, &gave_up)) return;
-          const float* row = scales + buffer * C::kScales + (t & 3) * (C::kScales / 4);
+        for (int t = begin; t < end; ++t) {
+          const int turn = (t - begin) & 3;
+          if (turn == 0 && !wait_or_leave(&scales_full[buffer], parity, &gave_up)) return;
+          const float* row = scales + buffer * C::kScales + turn * (C::kScales / 4);
           float s = row[quarter * 32 + lane];
           if constexpr (LINES == 128) s *= row[128 + (BN == 256 ? half : 0)];
           uint32_t v[2][32];
@@ -348,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
           add(kHalf == 128 ? 64 : 0, v[0]);
           if constexpr (kHalf >= 64) add(kHalf == 128 ? 96 : 32, v[1]);
-          if ((t & 3) == 3 || t + 1 == p.blocks) {
+          if (turn == 3 || t + 1 == end) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&scales_empty[buffer]);
             buffer ^= 1;
@@ -356,14 +386,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int row0 = m0 + (int)rank * 128 + quarter * 32, col = n0 + half * kHalf;
-        if (p.c_type == FWT_F32) store_rows<kHalf, float>(p, piece, row0, lane, col, acc);
-        else if (p.c_type == FWT_BF16) store_rows<kHalf, __nv_bfloat16>(p, piece, row0, lane, col, acc);
-        else store_rows<kHalf, __half>(p, piece, row0, lane, col, acc);
+        if constexpr (SPLIT == 1) {
+          store(piece, row0, col, acc);
+        } else {
+          // Every CTA of the cluster leaves its sums in its own ring, which its products are
+          // done with, and adds up and stores a share of the columns, in the order of ranks.
+          constexpr int kShare = kHalf / SPLIT;
+          float* mine = (float*)(dynamic + (ring - smem_u32(dynamic))) + (warp - 4) * kHalf * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) mine[i * 32] = acc[i];
+          cluster_sync();
+          met = true;
+          const int from = (int)cluster_rank() * kShare;
+          float sum[kShare];
+#pragma unroll
+          for (int i = 0; i < kShare; ++i) sum[i] = 0.f;
+          const uint32_t there = smem_u32(mine) + from * 128;
+#pragma unroll
+          for (int r = 0; r < SPLIT; ++r) {
+            const uint32_t peer = map_to_rank(there, r);
+#pragma unroll
+            for (int i = 0; i < kShare; ++i) sum[i] += load_cluster(peer + i * 128);
+          }
+          store(piece, row0, col + from, sum);
+        }
       }
     }();
   }
 
   __syncwarp();
+  if constexpr (SPLIT > 1) {
+    if (!met) cluster_sync();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
   tmem_fence_before();
   __syncthreads();
   if (gave_up) drain();
@@ -372,26 +427,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_free<CG>(tmem, C::kSlots * BN);
 }
 
-template <int CG, int BN, int LINES>
+template <int CG, int BN, int LINES, int ROWS, int SPLIT>
 cudaError_t launch_config(const BlocksMaps& maps, BlocksParams p, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   p.tiles_m = (p.m + 128 * CG - 1) / (128 * CG);
   p.tiles_n = (p.n + BN - 1) / BN;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  if (tiles > 0x7fffff00) return cudaErrorInvalidConfiguration;
-  const int64_t grid = std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
-  return launch_cluster(blocks_kernel<CG, BN, LINES>, ready, (unsigned)grid, kThreads,
-                        Config<CG, BN, LINES>::kSmem, CG, st, maps, p);
+  if (tiles > 0x7fffff00 / SPLIT) return cudaErrorInvalidConfiguration;
+  const int64_t grid = SPLIT > 1 ? tiles * SPLIT : std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
+  return launch_cluster(blocks_kernel<CG, BN, LINES, ROWS, SPLIT>, ready, (unsigned)grid, kThreads,
+                        Config<CG, BN, LINES, ROWS, SPLIT>::kSmem, CG * SPLIT, st, maps, p);
 }
 
-template <int CG, int BN>
+template <int CG, int BN, int ROWS = 128, int SPLIT = 1>
 cudaError_t run(CMat a, CMat b, int b_lines, const BlocksParams& p, int k, cudaStream_t st) {
   BlocksMaps maps;
-  if (!swizzled_map(&maps.a, a.p, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.m, k, a.ld, 128) ||
+  if (!swizzled_map(&maps.a, a.p, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.m, k, a.ld, ROWS) ||
       !swizzled_map(&maps.b, b.p, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.n, k, b.ld, BN / CG))
     return cudaErrorInvalidValue;
-  return b_lines == 1 ? launch_config<CG, BN, 1>(maps, p, st)
-                      : launch_config<CG, BN, 128>(maps, p, st);
+  return b_lines == 1 ? launch_config<CG, BN, 1, ROWS, SPLIT>(maps, p, st)
+                      : launch_config<CG, BN, 128, ROWS, SPLIT>(maps, p, st);
+}
+
+// Tiles of 64 columns, each shared out over `split` CTAs.
+template <int ROWS>
+cudaError_t run_split(int split, CMat a, CMat b, int b_lines, const BlocksParams& p, int k,
+                      cudaStream_t st) {
+  if (split >= 8) return run<1, 64, ROWS, 8>(a, b, b_lines, p, k, st);
+  if (split >= 4) return run<1, 64, ROWS, 4>(a, b, b_lines, p, k, st);
+  if (split >= 2) return run<1, 64, ROWS, 2>(a, b, b_lines, p, k, st);
+  return run<1, 64, ROWS, 1>(a, b, b_lines, p, k, st);
 }
 
 bool vector_rows(const void* p, int64_t ld_bytes) {
@@ -418,7 +483,12 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
     return run<2, 256>(a, b, b_lines, p, k, st);
   if ((int64_t)((m + 127) / 128) * ((n + 127) / 128) * 2 > sms)
     return run<1, 128>(a, b, b_lines, p, k, st);
-  return run<1, 64>(a, b, b_lines, p, k, st);
+  const int64_t tiles = (int64_t)((m + 127) / 128) * ((n + 63) / 64);
+  // (clusters of four and eight do not fill every multiprocessor of a graphics cluster)
+  int split = (int)std::min<int64_t>(sms / std::max<int64_t>(tiles, 1), p.blocks / 2);
+  if (split >= 4 && tiles * split > sms * 7 / 8) split /= 2;
+  return m <= 64 ? run_split<64>(split, a, b, b_lines, p, k, st)
+                 : run_split<128>(split, a, b, b_lines, p, k, st);
 }
 
 // Reads and clears this translation unit's device error word (synchronising).

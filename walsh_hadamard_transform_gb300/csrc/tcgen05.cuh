@@ -55,6 +55,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+__device__ __forceinline__ float load_cluster(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar))
                : "memory");
@@ -207,6 +213,18 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 
 // ---- waits ---------------------------------------------------------------------------
 
+// Whether the phase is complete, without waiting (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -221,8 +239,11 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
 
 // A wait of a whole warp: at most about a second, and over at once when another role of the
 // CTA has given up.  false, in every lane: leave the role's loop.
-__device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  bool done = mbar_poll(bar, parity);
+// `seen`: what an earlier mbar_test of the same phase said (asked ahead, its answer is there
+// by now).
+__device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int* gave_up,
+                                              bool seen = false) {
+  bool done = seen || mbar_poll(bar, parity);
   for (int i = 0; i < 32 && !done; ++i) done = mbar_poll(bar, parity);
   if (!done) {  // the timer is slow to read: not before it is needed
     const unsigned long long t0 = global_ns();

@@ -18,45 +18,55 @@ from __future__ import annotations
 import walsh_hadamard_transform_gb300 as _fwt
 
 _ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
-_REALS = None
-_E4M3 = None
+_torch = _REALS = _E4M3 = _F32 = _lib = _device = None
 
 
-def _reals():
-    global _REALS, _E4M3
-    if _REALS is None:
-        torch = _fwt._torch_mod()
-        _E4M3 = torch.float8_e4m3fn
-        _REALS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    return _REALS
+def _load():
+    """torch and the C library, on first use."""
+    global _torch, _REALS, _E4M3, _F32, _lib, _device
+    torch = _fwt._torch_mod()
+    _E4M3, _F32 = torch.float8_e4m3fn, torch.float32
+    _REALS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    _torch = torch
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _lib = _fwt.library()
 
 
 def _matrix(t, name, device, dtype=None, shape=None):
     """Row stride of a 2-D CUDA tensor with contiguous rows."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
-    if t.device != device or device.type != "cuda":
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError(f"{name}: expected a matrix, got {len(size)} dimensions")
+    if not t.is_cuda or t.device != device:
         raise ValueError(f"{name}: every tensor must be on one CUDA device")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {(rows, cols)}")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(size)}")
+    rows, cols = size
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    if rows <= 1:
-        return max(cols + -cols % 16, row if row >= cols else 0)
+    if rows <= 1:  # no second row: any stride will do
+        return cols + -cols % 16
     return row
 
 
 def _empty(rows, cols, dtype, device, multiple):
     """A new rows x cols tensor, its rows a multiple of ``multiple`` elements apart."""
-    torch = _fwt._torch_mod()
-    wide = -cols % multiple
-    t = torch.empty((rows, cols + wide), dtype=dtype, device=device)
-    return t[:, :cols] if wide else t
+    over = cols % multiple
+    if over:
+        return _torch.empty_strided((rows, cols), (cols + multiple - over, 1), dtype=dtype,
+                                    device=device)
+    return _torch.empty((rows, cols), dtype=dtype, device=device)
 
+
+def _run(device, entry, *args):
+    """Calls the C entry with ``device`` current."""
+    if device.index == _device():
+        return entry(*args)
+    with _torch.cuda.device(device):
+        return entry(*args)
 
 
 def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None, stream=None):
@@ -73,9 +83,9 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     (codes, scale): float8_e4m3fn (lines of codes, L) and float32 of a row for each
     ``lines`` lines and a column for each block.
     """
-    torch = _fwt._torch_mod()
-    reals = _REALS or _reals()
-    kind, device = reals.get(x.dtype), x.device
+    if _lib is None:
+        _load()
+    kind, device = _REALS.get(x.dtype), x.device
     if kind is None:
         raise TypeError(f"unsupported dtype {x.dtype}: use float32, bfloat16 or float16")
     if axis not in (0, 1) or lines not in (1, 128) or not 0 <= rotate <= 7:
@@ -87,15 +97,15 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     shape = (-(-across // lines), -(-length // 128))
     if out is None:
         q = _empty(across, length, _E4M3, device, 16)
-        scale = _empty(*shape, torch.float32, device, 4)
+        scale = _empty(*shape, _F32, device, 4)
+        ld_q, ld_s = q.stride(0), scale.stride(0)
     else:
         q, scale = out
-    ld_q = _matrix(q, "codes", device, _E4M3, (across, length))
-    ld_s = _matrix(scale, "scale", device, torch.float32, shape)
-    handle = _fwt._stream_handle(stream, device)
-    st = _fwt._on_device(device, lambda: _fwt.library().fwt_quantize_blocks(
-        x.data_ptr(), kind, rows, cols, ld, rotate, axis, lines, q.data_ptr(), ld_q,
-        scale.data_ptr(), ld_s, handle))
+        ld_q = _matrix(q, "codes", device, _E4M3, (across, length))
+        ld_s = _matrix(scale, "scale", device, _F32, shape)
+    st = _run(device, _lib.fwt_quantize_blocks, x.data_ptr(), kind, rows, cols, ld, rotate, axis,
+              lines, q.data_ptr(), ld_q, scale.data_ptr(), ld_s,
+              _fwt._stream_handle(stream, device))
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_quantize_blocks({rows} x {cols}, axis={axis})")
     return q, scale
@@ -108,8 +118,8 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
     ``b_scale`` a row for each line, (n, ceil(k / 128)), or for each 128 of them.  C is
     (m, n) of ``out_dtype`` (bfloat16 by default, float16 or float32), or ``out``.
     """
-    torch = _fwt._torch_mod()
-    reals = _REALS or _reals()
+    if _lib is None:
+        _load()
     device = a.device
     ld_a = _matrix(a, "a", device, _E4M3)
     m, k = a.shape
@@ -118,28 +128,33 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
     if b.shape[1] != k:
         raise ValueError(f"a and b have {k} and {b.shape[1]} elements along the contraction")
     blocks = -(-k // 128)
-    ld_as = _matrix(a_scale, "a_scale", device, torch.float32, (m, blocks))
-    lines = 1 if b_scale.dim() == 2 and b_scale.shape[0] == n else 128
-    ld_bs = _matrix(b_scale, "b_scale", device, torch.float32, (-(-n // lines), blocks))
+    ld_as = _matrix(a_scale, "a_scale", device, _F32, (m, blocks))
+    lines = 1 if len(b_scale.shape) == 2 and b_scale.shape[0] == n else 128
+    ld_bs = _matrix(b_scale, "b_scale", device, _F32, (-(-n // lines), blocks))
     if out is None:
-        out_dtype = out_dtype or torch.bfloat16
-        if out_dtype not in reals:
+        out_dtype = out_dtype or _torch.bfloat16
+        kind = _REALS.get(out_dtype)
+        if kind is None:
             raise TypeError(f"unsupported dtype {out_dtype}: use float32, bfloat16 or float16")
-        out = _empty(m, n, out_dtype, device, 16 // out_dtype.itemsize)
-    elif out.dtype not in reals or (out_dtype is not None and out.dtype != out_dtype):
-        raise TypeError(f"out: unsupported dtype {out.dtype}")
-    ld_c = _matrix(out, "out", device, None, (m, n))
-    handle = _fwt._stream_handle(stream, device)
-    st = _fwt._on_device(device, lambda: _fwt.library().fwt_matmul_blocks(
-        a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as, b.data_ptr(), ld_b, b_scale.data_ptr(),
-        ld_bs, lines, out.data_ptr(), reals[out.dtype], ld_c, m, n, k, handle))
+        out = _empty(m, n, out_dtype, device, 4 if kind == 0 else 8)
+        ld_c = out.stride(0)
+    else:
+        kind = _REALS.get(out.dtype)
+        if kind is None or (out_dtype is not None and out.dtype != out_dtype):
+            raise TypeError(f"out: unsupported dtype {out.dtype}")
+        ld_c = _matrix(out, "out", device, None, (m, n))
+    st = _run(device, _lib.fwt_matmul_blocks, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as,
+              b.data_ptr(), ld_b, b_scale.data_ptr(), ld_bs, lines, out.data_ptr(), kind, ld_c, m, n,
+              k, _fwt._stream_handle(stream, device))
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_matmul_blocks(m={m}, n={n}, k={k})")
     return out
 
 
 def _gated_arguments(x, w_gate, w_up, activation):
-    kind, device = (_REALS or _reals()).get(x.dtype), x.device
+    if _lib is None:
+        _load()
+    kind, device = _REALS.get(x.dtype), x.device
     if kind not in (1, 2):
         raise TypeError(f"unsupported dtype {x.dtype}: use bfloat16 or float16")
     act = _ACTIVATIONS.get(activation)
@@ -162,11 +177,11 @@ def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
     kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up, activation)
     if out is None:
         out = _empty(m, f, x.dtype, device, 8)
-    ld_h = _matrix(out, "out", device, x.dtype, (m, f))
-    handle = _fwt._stream_handle(stream, device)
-    st = _fwt._on_device(device, lambda: _fwt.library().fwt_gated(
-        x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, out.data_ptr(), ld_h,
-        kind, act, m, f, d, handle))
+        ld_h = out.stride(0)
+    else:
+        ld_h = _matrix(out, "out", device, x.dtype, (m, f))
+    st = _run(device, _lib.fwt_gated, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(),
+              ld_u, out.data_ptr(), ld_h, kind, act, m, f, d, _fwt._stream_handle(stream, device))
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_gated(m={m}, f={f}, d={d})")
     return out
@@ -181,7 +196,6 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
     three tensors to write to.  ``workspace``: a CUDA tensor of at least
     ``fwt_gated_backward_workspace_bytes(m, f)`` bytes for the gradients of the two
     products (allocated here when None)."""
-    torch = _fwt._torch_mod()
     kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up, activation)
     ld_dy = _matrix(grad, "grad", device, x.dtype, (m, f))
     want_x, want_w = "x" in want, "w" in want
@@ -196,20 +210,19 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
     ld_dg = _matrix(dw_gate, "dw_gate", device, x.dtype, (f, d)) if want_w else 0
     ld_du = _matrix(dw_up, "dw_up", device, x.dtype, (f, d)) if want_w else 0
     if workspace is None:
-        workspace = torch.empty(fwt_gated_backward_workspace_bytes(m, f), dtype=torch.uint8,
-                                device=device)
+        workspace = _torch.empty(_lib.fwt_gated_backward_workspace_bytes(m, f), dtype=_torch.uint8,
+                                 device=device)
         if stream is not None:
             # the allocator must not hand the memory on before `stream` is done with it
             workspace.record_stream(stream if hasattr(stream, "cuda_stream")
-                                    else torch.cuda.ExternalStream(int(stream), device=device))
+                                    else _torch.cuda.ExternalStream(int(stream), device=device))
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    handle = _fwt._stream_handle(stream, device)
     pointer = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    st = _fwt._on_device(device, lambda: _fwt.library().fwt_gated_backward(
-        grad.data_ptr(), ld_dy, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u,
-        pointer(dx), ld_dx, pointer(dw_gate), ld_dg, pointer(dw_up), ld_du, kind, act, m, f, d,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+    st = _run(device, _lib.fwt_gated_backward, grad.data_ptr(), ld_dy, x.data_ptr(), ld_x,
+              w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, pointer(dx), ld_dx, pointer(dw_gate),
+              ld_dg, pointer(dw_up), ld_du, kind, act, m, f, d, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _fwt._stream_handle(stream, device))
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_gated_backward(m={m}, f={f}, d={d})")
     return dx, dw_gate, dw_up
