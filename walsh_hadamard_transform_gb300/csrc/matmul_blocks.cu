@@ -162,8 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kHalf = BN / 2;  // columns of a warp
 
   extern __shared__ uint8_t dynamic[];
-  __shared__ uint64_t full[C::kStages], empty[C::kStages], slot_full[C::kSlots],
-      slot_empty[C::kSlots], scales_full[2], scales_empty[2];
+  // done: a stage's products are, so its slot is there to read and its memory free again
+  __shared__ uint64_t full[C::kStages], done[C::kStages], slot_empty[C::kSlots], scales_full[2],
+      scales_empty[2];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
 
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < C::kSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], 8 * CG);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&done[i], 1);
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(&slot_empty[i], 8 * CG);
     for (int i = 0; i < 2; ++i) mbar_init(&scales_full[i], 2), mbar_init(&scales_empty[i], 8);
     gave_up = 0;
     prefetch_map(&maps.a), prefetch_map(&maps.b);
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int m0, n0;
           place(index, m0, n0);
           for (int t = begin; t < end; ++t) {
-            if (!wait_or_leave(&empty[stage], parity, &gave_up)) return;
+            if (!wait_or_leave(&done[stage], parity, &gave_up)) return;
             const uint32_t a = ring + stage * C::kStage;
             const uint32_t bar = bars + 8 * stage;
             if (elect_one()) {
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t a = ring + stage * C::kStage;
             const uint64_t da = operand(a, 16), db = operand(a + C::kABytes, 16);
             const uint32_t d = tmem + slot * BN;
-            uint64_t *emptied = &empty[stage], *summed = &slot_full[slot];
+            uint64_t* summed = &done[stage];
             if (++stage == C::kStages) stage = 0, parity ^= 1;
             if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
             filled = mbar_test(&full[stage], parity);
@@ -259,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kBlock / 32; ++kk)  // 32 bytes of a swizzle row each
                 mma_tile<CG, 1>(d, da + 2 * kk, db + 2 * kk, kIdesc, kk > 0);
-              mma_commit<CG>(emptied);
               mma_commit<CG>(summed);
             }
             __syncwarp();
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegisters));
     // sums: warp w reads lanes 32 (w mod 4) on, a row of the tile each, and half its columns
     [&] {
-      int slot = 0, buffer = 0;
-      uint32_t slot_parity = 0, parity = 0;
+      int stage = 0, slot = 0, buffer = 0;
+      uint32_t done_parity = 0, parity = 0;
       const int quarter = warp & 3, half = (warp - 4) >> 2;
       uint32_t release = smem_u32(&slot_empty[0]);
       if constexpr (CG == 2) release = map_to_rank(release, 0);
@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[3] = fmaf(__uint_as_float(x[i + 3]), f.w, sum[3]);
             }
           };
-          if (!wait_or_leave(&slot_full[slot], slot_parity, &gave_up)) return;
+          if (!wait_or_leave(&done[stage], done_parity, &gave_up)) return;
+          if (++stage == C::kStages) stage = 0, done_parity ^= 1;
           tmem_fence_after();
           const uint32_t at = lanes + slot * BN;
           tmem_load32(at, v[0]);
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else mbar_arrive(&slot_empty[slot]);
           }
           __syncwarp();
-          if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
+          if (++slot == C::kSlots) slot = 0;
           add(kHalf == 128 ? 64 : 0, v[0]);
           if constexpr (kHalf >= 64) add(kHalf == 128 ? 96 : 32, v[1]);
           if (turn == 3 || t + 1 == end) {
