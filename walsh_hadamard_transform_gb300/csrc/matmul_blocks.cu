@@ -59,7 +59,13 @@ template <int CG, int BN, int LINES, int ROWS, int SPLIT>
 struct Config {
   static constexpr int kABytes = ROWS * 128, kBBytes = BN / CG * 128;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kSlots = 512 / BN > 4 ? 4 : 512 / BN;
+  // A tile of 256 columns is multiplied in two halves, each by a warp of its own into slots of
+  // its own, which four of the eight summing warps read: from the issue of a block's products
+  // to its slot's return is some 1500 clocks (of which the products take 512), too long for
+  // the two slots that whole blocks leave room for.
+  static constexpr int kParts = BN == 256 ? 2 : 1;
+  static constexpr int kCols = BN / kParts;         // columns of a slot
+  static constexpr int kSlots = BN == 256 ? 2 : 4;  // of each part
   // scales of four blocks: one of a for each row; of b for each column, or each 128
   static constexpr int kBScales = LINES == 1 ? BN : BN == 256 ? 2 : 1;
   static constexpr int kScales = 4 * (128 + kBScales);  // floats
@@ -158,13 +164,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     blocks_kernel(const __grid_constant__ BlocksMaps maps, const BlocksParams p) {
   using C = Config<CG, BN, LINES, ROWS, SPLIT>;
   static_assert(CG == 1 || SPLIT == 1, "a pair shares the tile, not its blocks");
-  constexpr uint32_t kIdesc = instruction(0, false, false, 128 * CG, BN);
+  constexpr uint32_t kIdesc = instruction(0, false, false, 128 * CG, C::kCols);
   constexpr int kHalf = BN / 2;  // columns of a warp
 
   extern __shared__ uint8_t dynamic[];
-  // done: a stage's products are, so its slot is there to read and its memory free again
-  __shared__ uint64_t full[C::kStages], done[C::kStages], slot_empty[C::kSlots], scales_full[2],
-      scales_empty[2];
+  // done: a stage's products (of a part) are, so the slot is there to read, and with both
+  // parts the stage's memory free again
+  __shared__ uint64_t full[C::kStages], done[C::kParts][C::kStages], slot_empty[C::kParts][C::kSlots],
+      scales_full[2], scales_empty[2];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
 
@@ -198,13 +205,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&done[i], 1);
-    for (int i = 0; i < C::kSlots; ++i) mbar_init(&slot_empty[i], 8 * CG);
-    for (int i = 0; i < 2; ++i) mbar_init(&scales_full[i], 2), mbar_init(&scales_empty[i], 8);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
+    for (int part = 0; part < C::kParts; ++part) {
+      for (int i = 0; i < C::kStages; ++i) mbar_init(&done[part][i], 1);
+      for (int i = 0; i < C::kSlots; ++i) mbar_init(&slot_empty[part][i], 8 / C::kParts * CG);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&scales_full[i], 1), mbar_init(&scales_empty[i], 8);
     gave_up = 0;
     prefetch_map(&maps.a), prefetch_map(&maps.b);
   }
-  if (warp == 1) tmem_alloc<CG>(&tmem_base, C::kSlots * BN);
+  if (warp == 1) tmem_alloc<CG>(&tmem_base, C::kParts * C::kSlots * C::kCols);
   tmem_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
@@ -224,38 +234,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           int m0, n0;
           place(index, m0, n0);
           for (int t = begin; t < end; ++t) {
-            if (!wait_or_leave(&done[stage], parity, &gave_up)) return;
+#pragma unroll
+            for (int part = 0; part < C::kParts; ++part)
+              if (!wait_or_leave(&done[part][stage], parity, &gave_up)) return;
             const uint32_t a = ring + stage * C::kStage;
             const uint32_t bar = bars + 8 * stage;
             if (elect_one()) {
               if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::kStage * CG);
               tma_load_tile<CG>(a, &maps.a, t * kBlock, m0 + (int)rank * 128, bar);
-              tma_load_tile<CG>(a + C::kABytes, &maps.b, t * kBlock, n0 + (int)rank * (BN / CG), bar);
+              // each part's lines together, half of them in each CTA of a pair
+#pragma unroll
+              for (int part = 0; part < C::kParts; ++part)
+                tma_load_tile<CG>(a + C::kABytes + part * (C::kBBytes / C::kParts), &maps.b,
+                                  t * kBlock, n0 + part * C::kCols + (int)rank * (C::kCols / CG), bar);
             }
             __syncwarp();
             if (++stage == C::kStages) stage = 0, parity ^= 1;
           }
         }
       }();
-    } else if (warp == 1 && rank == 0) {
-      // products
+    } else if (warp <= C::kParts) {
+      // products (of the pair's first CTA for both): warp 1, and 2 for the second part
+      if (rank == 0)
       [&] {
+        const int part = warp - 1;
         int stage = 0, slot = 0;
         uint32_t parity = 0, slot_parity = 1;
         bool filled = false, returned = false;  // asked one block ahead
         for (int index = first; index < tiles; index += stride) {
           for (int t = begin; t < end; ++t) {
             if (!wait_or_leave(&full[stage], parity, &gave_up, filled)) return;
-            if (!wait_or_leave(&slot_empty[slot], slot_parity, &gave_up, returned)) return;
+            if (!wait_or_leave(&slot_empty[part][slot], slot_parity, &gave_up, returned)) return;
             tmem_fence_after();
             const uint32_t a = ring + stage * C::kStage;
-            const uint64_t da = operand(a, 16), db = operand(a + C::kABytes, 16);
-            const uint32_t d = tmem + slot * BN;
-            uint64_t* summed = &done[stage];
+            const uint64_t da = operand(a, 16);
+            const uint64_t db = operand(a + C::kABytes + part * (C::kBBytes / C::kParts), 16);
+            const uint32_t d = tmem + (part * C::kSlots + slot) * C::kCols;
+            uint64_t* summed = &done[part][stage];
             if (++stage == C::kStages) stage = 0, parity ^= 1;
             if (++slot == C::kSlots) slot = 0, slot_parity ^= 1;
             filled = mbar_test(&full[stage], parity);
-            returned = mbar_test(&slot_empty[slot], slot_parity);
+            returned = mbar_test(&slot_empty[part][slot], slot_parity);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kBlock / 32; ++kk)  // 32 bytes of a swizzle row each
@@ -266,30 +285,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }();
-    } else if (warp >= 2) {
-      // scales: two warps bring those of four blocks at a time to shared memory, a row of
-      // kScales / 4 floats for each block
+    } else if (warp == 3) {
+      // scales: those of four blocks at a time to shared memory, a row of kScales / 4 floats
+      // for each block
       [&] {
         int buffer = 0;
         uint32_t parity = 1;
-        const int thread = threadIdx.x - 64;
         constexpr int kRow = C::kScales / 4;
         const bool vec_as = p.vec_as && begin % 4 == 0, vec_bs = p.vec_bs && begin % 4 == 0;
         for (int index = first; index < tiles; index += stride) {
           int m0, n0;
           place(index, m0, n0);
           for (int t = begin; t < end; t += 4) {
-            float4 a[2], b[LINES == 1 ? BN / 64 : 1];
+            float4 a[4], b[LINES == 1 ? BN / 32 : 1];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              a[i] = scales4(p.a_scale, p.ld_as, m0 + (int)rank * 128 + thread + 64 * i, p.m, t,
+            for (int i = 0; i < 4; ++i)
+              a[i] = scales4(p.a_scale, p.ld_as, m0 + (int)rank * 128 + lane + 32 * i, p.m, t,
                              p.blocks, vec_as);
             if constexpr (LINES == 1) {
 #pragma unroll
-              for (int i = 0; i < BN / 64; ++i)
-                b[i] = scales4(p.b_scale, p.ld_bs, n0 + thread + 64 * i, p.n, t, p.blocks, vec_bs);
-            } else if (thread < C::kBScales) {
-              b[0] = scales4(p.b_scale, p.ld_bs, n0 / 128 + thread, (p.n + 127) / 128, t, p.blocks,
+              for (int i = 0; i < BN / 32; ++i)
+                b[i] = scales4(p.b_scale, p.ld_bs, n0 + lane + 32 * i, p.n, t, p.blocks, vec_bs);
+            } else if (lane < C::kBScales) {
+              b[0] = scales4(p.b_scale, p.ld_bs, n0 / 128 + lane, (p.n + 127) / 128, t, p.blocks,
                              vec_bs);
             }
             if (!wait_or_leave(&scales_empty[buffer], parity, &gave_up)) return;
@@ -298,12 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               to[at] = v.x, to[at + kRow] = v.y, to[at + 2 * kRow] = v.z, to[at + 3 * kRow] = v.w;
             };
 #pragma unroll
-            for (int i = 0; i < 2; ++i) put(thread + 64 * i, a[i]);
+            for (int i = 0; i < 4; ++i) put(lane + 32 * i, a[i]);
             if constexpr (LINES == 1) {
 #pragma unroll
-              for (int i = 0; i < BN / 64; ++i) put(128 + thread + 64 * i, b[i]);
-            } else if (thread < C::kBScales) {
-              put(128 + thread, b[0]);
+              for (int i = 0; i < BN / 32; ++i) put(128 + lane + 32 * i, b[i]);
+            } else if (lane < C::kBScales) {
+              put(128 + lane, b[0]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&scales_full[buffer]);
@@ -321,70 +339,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, slot = 0, buffer = 0;
       uint32_t done_parity = 0, parity = 0;
       const int quarter = warp & 3, half = (warp - 4) >> 2;
-      uint32_t release = smem_u32(&slot_empty[0]);
+      const int part = C::kParts == 2 ? half : 0;
+      uint32_t release = smem_u32(&slot_empty[part][0]);
       if constexpr (CG == 2) release = map_to_rank(release, 0);
       uint8_t* piece = after_ring + (warp - 4) * 4096;
-      const uint32_t lanes = tmem + half * kHalf + ((uint32_t)quarter << 21);
+      const uint32_t lanes = tmem + part * (C::kSlots * C::kCols) +
+                             (C::kParts == 2 ? 0 : half * kHalf) + ((uint32_t)quarter << 21);
       for (int index = first; index < tiles; index += stride) {
         int m0, n0;
         place(index, m0, n0);
         float acc[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
-        for (int t = begin; t < end; ++t) {
-          const int turn = (t - begin) & 3;
-          if (turn == 0 && !wait_or_leave(&scales_full[buffer], parity, &gave_up)) return;
-          const float* row = scales + buffer * C::kScales + turn * (C::kScales / 4);
-          float s = row[quarter * 32 + lane];
-          if constexpr (LINES == 128) s *= row[128 + (BN == 256 ? half : 0)];
-          uint32_t v[2][32];
-          auto add = [&](int c, const uint32_t(&x)[32]) {
+        for (int t0 = begin; t0 < end; t0 += 4) {
+          // the scales of four blocks: the row's (times b's one, or b's row beside it)
+          if (!wait_or_leave(&scales_full[buffer], parity, &gave_up)) return;
+          const float* row = scales + buffer * C::kScales;
+          float s[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float4 f = make_float4(s, s, s, s);
-              if constexpr (LINES == 1) {
-                f = *(const float4*)&row[128 + half * kHalf + c + i];
-                f.x *= s, f.y *= s, f.z *= s, f.w *= s;
-              }
-              float* sum = &acc[c + i];
-              sum[0] = fmaf(__uint_as_float(x[i]), f.x, sum[0]);
-              sum[1] = fmaf(__uint_as_float(x[i + 1]), f.y, sum[1]);
-              sum[2] = fmaf(__uint_as_float(x[i + 2]), f.z, sum[2]);
-              sum[3] = fmaf(__uint_as_float(x[i + 3]), f.w, sum[3]);
-            }
-          };
-          if (!wait_or_leave(&done[stage], done_parity, &gave_up)) return;
-          if (++stage == C::kStages) stage = 0, done_parity ^= 1;
-          tmem_fence_after();
-          const uint32_t at = lanes + slot * BN;
-          tmem_load32(at, v[0]);
-          if constexpr (kHalf >= 64) tmem_load32(at + 32, v[1]);
-          tmem_wait_loads();
-          if constexpr (kHalf == 128) {
-            add(0, v[0]);
-            tmem_load32(at + 64, v[0]);
-            add(32, v[1]);
-            tmem_load32(at + 96, v[1]);
-            tmem_wait_loads();
+          for (int u = 0; u < 4; ++u) {
+            s[u] = row[u * (C::kScales / 4) + quarter * 32 + lane];
+            if constexpr (LINES == 128) s[u] *= row[u * (C::kScales / 4) + 128 + (BN == 256 ? half : 0)];
           }
-          // the slot is read: it goes back before the last sums, as the next block's products
-          // but one wait for it
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2) mbar_arrive_cluster(release + 8 * slot);
-            else mbar_arrive(&slot_empty[slot]);
-          }
-          __syncwarp();
-          if (++slot == C::kSlots) slot = 0;
-          add(kHalf == 128 ? 64 : 0, v[0]);
-          if constexpr (kHalf >= 64) add(kHalf == 128 ? 96 : 32, v[1]);
-          if (turn == 3 || t + 1 == end) {
+          if constexpr (LINES == 128) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&scales_empty[buffer]);
-            buffer ^= 1;
-            if (buffer == 0) parity ^= 1;
+            mbar_arrive(&scales_empty[buffer], lane == 0);
           }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (t0 + u >= end) break;
+            uint32_t v[2][32];
+            auto add = [&](int c, const uint32_t(&x)[32]) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float4 f = make_float4(s[u], s[u], s[u], s[u]);
+                if constexpr (LINES == 1) {
+                  f = *(const float4*)&row[u * (C::kScales / 4) + 128 + half * kHalf + c + i];
+                  f.x *= s[u], f.y *= s[u], f.z *= s[u], f.w *= s[u];
+                }
+                float* sum = &acc[c + i];
+                sum[0] = fmaf(__uint_as_float(x[i]), f.x, sum[0]);
+                sum[1] = fmaf(__uint_as_float(x[i + 1]), f.y, sum[1]);
+                sum[2] = fmaf(__uint_as_float(x[i + 2]), f.z, sum[2]);
+                sum[3] = fmaf(__uint_as_float(x[i + 3]), f.w, sum[3]);
+              }
+            };
+            if (!wait_or_leave(&done[part][stage], done_parity, &gave_up)) return;
+            if (++stage == C::kStages) stage = 0, done_parity ^= 1;
+            tmem_fence_after();
+            const uint32_t at = lanes + slot * C::kCols;
+            tmem_load32(at, v[0]);
+            if constexpr (kHalf >= 64) tmem_load32(at + 32, v[1]);
+            tmem_wait_loads();
+            if constexpr (kHalf == 128) {
+              add(0, v[0]);
+              tmem_load32(at + 64, v[0]);
+              add(32, v[1]);
+              tmem_load32(at + 96, v[1]);
+              tmem_wait_loads();
+            }
+            // the slot is read: it goes back before the last sums, as products may wait for it
+            tmem_fence_before();
+            if constexpr (CG == 2) mbar_arrive_cluster(release + 8 * slot, lane == 0);
+            else mbar_arrive(&slot_empty[part][slot], lane == 0);
+            if (++slot == C::kSlots) slot = 0;
+            add(kHalf == 128 ? 64 : 0, v[0]);
+            if constexpr (kHalf >= 64) add(kHalf == 128 ? 96 : 32, v[1]);
+          }
+          if constexpr (LINES == 1) {
+            __syncwarp();
+            mbar_arrive(&scales_empty[buffer], lane == 0);
+          }
+          if (++buffer == 2) buffer = 0, parity ^= 1;
         }
         const int row0 = m0 + (int)rank * 128 + quarter * 32, col = n0 + half * kHalf;
         if constexpr (SPLIT == 1) {
@@ -425,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (gave_up) drain();
   if constexpr (CG == 2) cluster_sync();
   tmem_fence_after();
-  if (warp == 1) tmem_free<CG>(tmem, C::kSlots * BN);
+  if (warp == 1) tmem_free<CG>(tmem, C::kParts * C::kSlots * C::kCols);
 }
 
 template <int CG, int BN, int LINES, int ROWS, int SPLIT>
@@ -444,7 +470,8 @@ template <int CG, int BN, int ROWS = 128, int SPLIT = 1>
 cudaError_t run(CMat a, CMat b, int b_lines, const BlocksParams& p, int k, cudaStream_t st) {
   BlocksMaps maps;
   if (!swizzled_map(&maps.a, a.p, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.m, k, a.ld, ROWS) ||
-      !swizzled_map(&maps.b, b.p, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.n, k, b.ld, BN / CG))
+      !swizzled_map(&maps.b, b.p, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.n, k, b.ld,
+                    Config<CG, BN, 128, ROWS, SPLIT>::kCols / CG))
     return cudaErrorInvalidValue;
   return b_lines == 1 ? launch_config<CG, BN, 1, ROWS, SPLIT>(maps, p, st)
                       : launch_config<CG, BN, 128, ROWS, SPLIT>(maps, p, st);

@@ -50,9 +50,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 
 // Says that reads of tensor memory are done (after tmem_fence_before()); orders no other
 // memory, as a release at cluster scope would (measured: a thousand clocks).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr, bool one = true) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+      "r"((uint32_t)one)
+      : "memory");
 }
 
 __device__ __forceinline__ float load_cluster(uint32_t cluster_addr) {
@@ -61,9 +64,13 @@ __device__ __forceinline__ float load_cluster(uint32_t cluster_addr) {
   return v;
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+// (`one`: only the threads for which it is true arrive, without a branch.)
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar, bool one = true) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)one)
+      : "memory");
 }
 
 // A box of `map` at (x, y) into this CTA's shared memory; its bytes are counted by `bar`, a
