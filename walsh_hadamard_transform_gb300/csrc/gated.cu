@@ -53,7 +53,8 @@ struct GemmMaps {
 
 constexpr int kTileK = 64;  // elements of the contraction in a stage: one swizzle row
 constexpr int kRingBytes = 196608;
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;  // a warp each for copies and products, eight for the epilogue
+constexpr int kPieceBytes = 32 * 64;  // 32 columns of a warp's 32 rows, see store_rows
 
 // CG: CTAs that share a tile.  BN: columns of its accumulator.  Each CTA holds 128 rows of
 // the first operand and BN / CG lines of the second.
@@ -62,7 +63,7 @@ struct Config {
   static constexpr int kABytes = 128 * 128, kBBytes = BN / CG * 128;
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kStages = kRingBytes / kStage;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + 8 * kPieceBytes + 1024;
 };
 
 struct Tile {
@@ -99,39 +100,77 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
   else return __bfloat1622float2(*(const __nv_bfloat162*)&v);
 }
 
-// 32 values of a row to columns [col, col + 32) of `out`, those below n.
-template <typename T>
-__device__ __forceinline__ void store32(T* row, int col, int n, bool vec, const uint32_t (&v)[16]) {
-  if (vec && col + 32 <= n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *(uint4*)(row + col + 8 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (col + i < n)
-      *(unsigned short*)(row + col + i) = (unsigned short)(v[i / 2] >> (16 * (i & 1)));
+// A warp's 32 rows from `row0` on, W columns from `col`, one row a thread as pairs: through
+// the warp's piece of shared memory (16-byte chunks, swizzled by row), so that global memory
+// sees whole runs of a row and not 16 bytes of each.  Outside m x n nothing is touched.
+template <int W>
+__device__ __forceinline__ uint4* piece_at(uint8_t* piece, int row, int chunk) {
+  constexpr int kChunks = W / 8;
+  return (uint4*)(piece + (row * kChunks + ((chunk ^ (row * kChunks / 8)) & (kChunks - 1))) * 16);
 }
-template <typename T>
-__device__ __forceinline__ void load32(const T* row, int col, int n, uint32_t (&v)[16]) {
-  if (col + 32 <= n) {
+template <typename T, int W>
+__device__ __forceinline__ void store_rows(T* out, int64_t ld, uint8_t* piece, int row0, int lane,
+                                           int m, int col, int n, bool vec, const uint32_t (&v)[W / 2]) {
+  constexpr int kChunks = W / 8;
+  static_assert(kChunks > 0, "whole 16-byte chunks");
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 q = __ldg((const uint4*)(row + col + 8 * i));
-      v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+  for (int i = 0; i < kChunks; ++i)
+    *piece_at<W>(piece, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int r = i * (32 / kChunks) + lane / kChunks, chunk = lane & (kChunks - 1);
+    const uint4 q = *piece_at<W>(piece, r, chunk);
+    const int at = col + 8 * chunk;
+    if (row0 + r < m && at < n) {
+      T* to = out + (int64_t)(row0 + r) * ld + at;
+      if (vec && at + 8 <= n) {
+        *(uint4*)to = q;
+      } else {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at + j < n) *(unsigned short*)(to + j) = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
+      }
     }
-    return;
   }
+}
+// (Rows of `in` start on 16-byte boundaries.)
+template <typename T, int W>
+__device__ __forceinline__ void load_rows(const T* in, int64_t ld, uint8_t* piece, int row0, int lane,
+                                          int m, int col, int n, uint32_t (&v)[W / 2]) {
+  constexpr int kChunks = W / 8;
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t lo = col + 2 * i < n ? __ldg((const unsigned short*)row + col + 2 * i) : 0;
-    const uint32_t hi = col + 2 * i + 1 < n ? __ldg((const unsigned short*)row + col + 2 * i + 1) : 0;
-    v[i] = lo | (hi << 16);
+  for (int i = 0; i < kChunks; ++i) {
+    const int r = i * (32 / kChunks) + lane / kChunks, chunk = lane & (kChunks - 1);
+    const int at = col + 8 * chunk;
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (row0 + r < m && at < n) {
+      const T* from = in + (int64_t)(row0 + r) * ld + at;
+      if (at + 8 <= n) {
+        q = __ldg((const uint4*)from);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at + j < n) w[j / 2] |= (uint32_t)__ldg((const unsigned short*)from + j) << (16 * (j & 1));
+        q = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *piece_at<W>(piece, r, chunk) = q;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const uint4 q = *piece_at<W>(piece, lane, i);
+    v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
   }
 }
 
-template <typename T, int MODE, int CG, int BN>
+// SPLIT: CTAs of a cluster that share out the contraction of a tile.
+template <typename T, int MODE, int CG, int BN, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
   using C = Config<CG, BN>;
@@ -149,13 +188,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
-  const int steps = p.k_blocks * p.phases;
+  static_assert(CG == 1 || SPLIT == 1, "a pair shares the tile, not its contraction");
   const int tiles = p.tiles_m * p.tiles_n * p.outputs;
-  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int first = blockIdx.x / (CG * SPLIT), stride = gridDim.x / (CG * SPLIT);
+  // the CTA's stages of the contraction: all, or its share of them
+  const int all = p.k_blocks * p.phases, share = (all + SPLIT - 1) / SPLIT;
+  const int begin = SPLIT == 1 ? 0 : min(all, (int)cluster_rank() * share);
+  const int end = SPLIT == 1 ? all : min(all, begin + share);
+  bool met = false;  // whether the warp is past the cluster's first barrier
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4 * CG);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 8 * CG);
     gave_up = 0;
     for (int i = 0; i < 2; ++i) prefetch_map(&maps.a[i]), prefetch_map(&maps.b[i]);
   }
@@ -174,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (CG == 2) bars = map_to_rank(bars, 0);
       for (int index = first; index < tiles; index += stride) {
         const Tile t = tile_at(p, index, 128 * CG, kCols);
-        for (int s = 0; s < steps; ++s) {
+        for (int s = begin; s < end; ++s) {
           if (!wait_or_leave(&empty[stage], parity, &gave_up)) return;
           const uint32_t bar = bars + 8 * stage;
           const int phase = MODE == kDx ? s / p.k_blocks : 0;
@@ -217,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int index = first; index < tiles; index += stride) {
         if (!wait_or_leave(&acc_empty[acc], acc_parity, &gave_up)) return;
         tmem_fence_after();
-        for (int s = 0; s < steps; ++s) {
+        for (int s = begin; s < end; ++s) {
           if (!wait_or_leave(&full[stage], parity, &gave_up)) return;
           tmem_fence_after();
           const uint32_t a = ring + stage * C::kStage, b = a + C::kABytes;
@@ -227,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < kTileK / 16; ++kk)  // 16 along the contraction: 32 bytes of a
               mma_tile<CG, 2>(tmem + acc * BN,        // swizzle row, or 16 rows (units of 16)
                               da + kk * (kAcrossA ? 128 : 2), db + kk * (kAcrossB ? 128 : 2),
-                              kIdesc, s + kk > 0);
+                              kIdesc, s - begin + kk > 0);
             mma_commit<CG>(&empty[stage]);
           }
           __syncwarp();
@@ -239,75 +283,131 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }();
   } else if (warp >= 2) {
-    // epilogue: warp w reads lanes 32 (w mod 4) on, a row of the tile each
+    // epilogue: warp w reads lanes 32 (w mod 4) on, a row of the tile each, and half the columns
     [&] {
       int acc = 0;
       uint32_t acc_parity = 0;
-      const int quarter = warp & 3;
-      uint32_t release[2];
-      for (int i = 0; i < 2; ++i)
-        release[i] = CG == 2 ? map_to_rank(smem_u32(&acc_empty[i]), 0) : smem_u32(&acc_empty[i]);
+      constexpr int kHalf = kCols / 2, kChunk = 32;
+      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      uint32_t release = smem_u32(&acc_empty[0]);
+      if constexpr (CG == 2) release = map_to_rank(release, 0);
+      uint8_t* ring_memory = dynamic + (ring - smem_u32(dynamic));
+      uint8_t* piece = ring_memory + C::kStages * C::kStage + (warp - 2) * kPieceBytes;
       for (int index = first; index < tiles; index += stride) {
         const Tile t = tile_at(p, index, 128 * CG, kCols);
-        const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
-        const bool live = row < p.m;
+        const int row0 = t.m0 + (int)rank * 128 + quarter * 32;
         const uint32_t at = tmem + acc * BN + ((uint32_t)quarter << 21);
-        if (!wait_or_leave(&acc_full[acc], acc_parity, &gave_up)) return;
-        tmem_fence_after();
-        T* out0 = (T*)p.out[MODE == kDw ? t.output : 0] +
-                  (int64_t)row * p.ld_out[MODE == kDw ? t.output : 0];
-#pragma unroll 1
-        for (int c = 0; c < kCols; c += 32) {
+        // W columns of the output from the tile's column c: v, and u beside it for two weights;
+        // dh: the gradients' share of `grad`, overwritten
+        auto emit = [&](int c, auto& v, auto& u, auto& dh) {
+          constexpr int W = sizeof(v) / 4;
+          uint32_t packed[W / 2];
           const int col = t.n0 + c;
-          if (col >= p.n) break;
-          uint32_t v[32], packed[16];
-          tmem_load32(at + c, v);
-          if constexpr (kPairedWeights) {
-            uint32_t u[32], second[16];
-            tmem_load32(at + BN / 2 + c, u);
-            if constexpr (MODE == kGradients) {
-              if (live) load32((const T*)p.grad + (int64_t)row * p.ld_grad, col, p.n, second);
-              __syncwarp();
-            }
-            tmem_wait_loads();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < W / 2; ++i) {
+            const float a0 = __uint_as_float(v[2 * i]), a1 = __uint_as_float(v[2 * i + 1]);
+            if constexpr (kPairedWeights) {
               float v0, v1, s0, s1;
-              activate(p.act, __uint_as_float(v[2 * i]), v0, s0);
-              activate(p.act, __uint_as_float(v[2 * i + 1]), v1, s1);
+              activate(p.act, a0, v0, s0);
+              activate(p.act, a1, v1, s1);
               const float u0 = __uint_as_float(u[2 * i]), u1 = __uint_as_float(u[2 * i + 1]);
               if constexpr (MODE == kForward) {
                 packed[i] = pack2<T>(v0 * u0, v1 * u1);
               } else {
-                const float2 dh = unpack2<T>(second[i]);
-                packed[i] = pack2<T>(dh.x * u0 * s0, dh.y * u1 * s1);
-                second[i] = pack2<T>(dh.x * v0, dh.y * v1);
+                const float2 g = unpack2<T>(dh[i]);
+                packed[i] = pack2<T>(g.x * u0 * s0, g.y * u1 * s1);
+                dh[i] = pack2<T>(g.x * v0, g.y * v1);
               }
+            } else {
+              packed[i] = pack2<T>(a0, a1);
             }
-            if constexpr (MODE == kGradients) {
-              if (live) store32((T*)p.out[1] + (int64_t)row * p.ld_out[1], col, p.n, p.vec, second);
-            }
-          } else {
+          }
+          const int o = MODE == kDw ? t.output : 0;
+          store_rows<T, W>((T*)p.out[o], p.ld_out[o], piece, row0, lane, p.m, col, p.n, p.vec, packed);
+          if constexpr (MODE == kGradients)
+            store_rows<T, W>((T*)p.out[1], p.ld_out[1], piece, row0, lane, p.m, col, p.n, p.vec, dh);
+        };
+        auto load_grad = [&](int c, auto& dh) {
+          if constexpr (MODE == kGradients)
+            load_rows<T, sizeof(dh) / 2>((const T*)p.grad, p.ld_grad, piece, row0, lane, p.m, t.n0 + c,
+                                         p.n, dh);
+        };
+        uint32_t dh[2][kChunk / 2];  // on their way while the products run
+        if constexpr (SPLIT == 1 && MODE == kGradients) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (i * kChunk < kHalf) load_grad(half * kHalf + i * kChunk, dh[i]);
+        }
+        if (!wait_or_leave(&acc_full[acc], acc_parity, &gave_up)) return;
+        tmem_fence_after();
+        if constexpr (SPLIT == 1) {
+#pragma unroll
+          for (int i = 0; i < kHalf / kChunk; ++i) {
+            const int c = half * kHalf + i * kChunk;
+            if (t.n0 + c >= p.n) break;
+            uint32_t v[32], u[32];
+            tmem_load32(at + c, v);
+            if constexpr (kPairedWeights) tmem_load32(at + BN / 2 + c, u);
+            tmem_wait_loads();
+            emit(c, v, u, dh[i & 1]);
+          }
+          __syncwarp();
+        } else {
+          // Every CTA of the cluster leaves its sums in its own ring, which its products are
+          // done with, and adds up and emits a share of the columns, in the order of ranks.
+          float* mine = (float*)ring_memory + quarter * BN * 32 + lane;
+          const bool some = begin < end;
+#pragma unroll 1
+          for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+            uint32_t v[32];
+            tmem_load32(at + c, v);
             tmem_wait_loads();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              packed[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            for (int i = 0; i < 32; ++i) mine[(c + i) * 32] = some ? __uint_as_float(v[i]) : 0.f;
           }
-          if (live) store32(out0, col, p.n, p.vec, packed);
           __syncwarp();
+          cluster_sync();
+          met = true;
+          constexpr int kShare = kHalf / SPLIT, W = kShare < 32 ? kShare : 32;
+          const int from = half * kHalf + (int)cluster_rank() * kShare;
+          const uint32_t there = smem_u32(mine);
+#pragma unroll 1
+          for (int c = from; c < from + kShare; c += W) {
+            uint32_t v[W], u[W];
+            auto gather = [&](int c0, uint32_t(&x)[W]) {
+              float sum[W];
+#pragma unroll
+              for (int i = 0; i < W; ++i) sum[i] = 0.f;
+#pragma unroll
+              for (int r = 0; r < SPLIT; ++r) {
+                const uint32_t peer = map_to_rank(there, r) + c0 * 128;
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum[i] += load_cluster(peer + i * 128);
+              }
+#pragma unroll
+              for (int i = 0; i < W; ++i) x[i] = __float_as_uint(sum[i]);
+            };
+            gather(c, v);
+            if constexpr (kPairedWeights) gather(BN / 2 + c, u);
+            uint32_t dh[W / 2];
+            load_grad(c, dh);
+            emit(c, v, u, dh);
+          }
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2) mbar_arrive_cluster(release[acc]);
-          else mbar_arrive(&acc_empty[acc]);
-        }
+        if constexpr (CG == 2) mbar_arrive_cluster(release + 8 * acc, lane == 0);
+        else mbar_arrive(&acc_empty[acc], lane == 0);
         if (++acc == 2) acc = 0, acc_parity ^= 1;
       }
     }();
   }
 
   __syncwarp();
+  if constexpr (SPLIT > 1) {
+    if (!met) cluster_sync();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
   tmem_fence_before();
   __syncthreads();
   if (gave_up) drain();
@@ -316,17 +416,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_free<CG>(tmem, 2 * BN);
 }
 
-template <typename T, int MODE, int CG, int BN>
-cudaError_t launch_config(const GemmMaps& maps, GemmParams p, cudaStream_t st) {
+template <typename T, int MODE, int CG, int BN, int SPLIT>
+cudaError_t launch_config(const GemmMaps& maps, const GemmParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  constexpr int cols = MODE == kForward || MODE == kGradients ? BN / 2 : BN;
-  p.tiles_m = (p.m + 128 * CG - 1) / (128 * CG);
-  p.tiles_n = (p.n + cols - 1) / cols;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outputs;
-  if (tiles > 0x7fffff00) return cudaErrorInvalidConfiguration;
-  const int64_t grid = std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
-  return launch_cluster(gemm_kernel<T, MODE, CG, BN>, ready, (unsigned)grid, kThreads,
-                        Config<CG, BN>::kSmem, CG, st, maps, p);
+  if (tiles > 0x7fffff00 / SPLIT) return cudaErrorInvalidConfiguration;
+  const int64_t grid =
+      SPLIT > 1 ? tiles * SPLIT : std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
+  return launch_cluster(gemm_kernel<T, MODE, CG, BN, SPLIT>, ready, (unsigned)grid, kThreads,
+                        Config<CG, BN>::kSmem, CG * SPLIT, st, maps, p);
+}
+
+template <typename T, int MODE>
+cudaError_t launch_mode(bool wide, const GemmMaps& maps, GemmParams p, cudaStream_t st) {
+  constexpr int halves = MODE == kForward || MODE == kGradients ? 2 : 1;
+  const int rows = wide ? 256 : 128, cols = (wide ? 256 : 128) / halves;
+  p.tiles_m = (p.m + rows - 1) / rows;
+  p.tiles_n = (p.n + cols - 1) / cols;
+  if (wide) return launch_config<T, MODE, 2, 256, 1>(maps, p, st);
+  // Where the tiles leave multiprocessors idle, clusters share out the contraction, four
+  // stages a CTA at least.  (Clusters of four and eight do not fill every multiprocessor of a
+  // graphics cluster.)
+  const int sms = multiprocessors();
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outputs;
+  int64_t split = std::min<int64_t>(sms / tiles, (int64_t)p.k_blocks * p.phases / 4);
+  if (split >= 4 && tiles * split > sms * 7 / 8) split /= 2;
+  if constexpr (halves == 1)  // two weights' shares of an eighth would be narrower than a store
+    if (split >= 8) return launch_config<T, MODE, 1, 128, 8>(maps, p, st);
+  if (split >= 4) return launch_config<T, MODE, 1, 128, 4>(maps, p, st);
+  if (split >= 2) return launch_config<T, MODE, 1, 128, 2>(maps, p, st);
+  return launch_config<T, MODE, 1, 128, 1>(maps, p, st);
 }
 
 // Whether pairs of CTAs on 256 x 256 tiles fill the device: else smaller tiles.
@@ -362,8 +481,7 @@ cudaError_t run_paired(CMat x, CMat w_gate, CMat w_up, GemmParams p, int d, cuda
   maps.a[1] = maps.a[0];
   p.k_blocks = (d + kTileK - 1) / kTileK;
   p.phases = p.outputs = 1;
-  return wide ? launch_config<T, MODE, 2, 256>(maps, p, st)
-              : launch_config<T, MODE, 1, 128>(maps, p, st);
+  return launch_mode<T, MODE>(wide, maps, p, st);
 }
 
 template <typename T>
@@ -377,8 +495,7 @@ cudaError_t run_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, int m, int 
   GemmParams p{};
   p.m = m, p.n = d, p.k_blocks = (f + kTileK - 1) / kTileK, p.phases = 2, p.outputs = 1;
   p.out[0] = dx.p, p.ld_out[0] = dx.ld, p.vec = vector_rows(dx);
-  return wide_tiles(m, d, 1) ? launch_config<T, kDx, 2, 256>(maps, p, st)
-                             : launch_config<T, kDx, 1, 128>(maps, p, st);
+  return launch_mode<T, kDx>(wide_tiles(m, d, 1), maps, p, st);
 }
 
 template <typename T>
@@ -394,8 +511,7 @@ cudaError_t run_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int m, int 
   p.out[0] = dw_gate.p, p.ld_out[0] = dw_gate.ld;
   p.out[1] = dw_up.p, p.ld_out[1] = dw_up.ld;
   p.vec = vector_rows(dw_gate) && vector_rows(dw_up);
-  return wide_tiles(f, d, 2) ? launch_config<T, kDw, 2, 256>(maps, p, st)
-                             : launch_config<T, kDw, 1, 128>(maps, p, st);
+  return launch_mode<T, kDw>(wide_tiles(f, d, 2), maps, p, st);
 }
 
 }  // namespace
