@@ -14,6 +14,8 @@ namespace fwt {
 
 // The driver's tensor-map encoder, resolved once at run time (nullptr if absent).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+// Whether kernels are launched with programmatic stream serialisation (fwt_set_pdl).
+int pdl_mode();
 
 namespace ff {
 
@@ -44,8 +46,35 @@ inline int multiprocessors() {
   return n;
 }
 
-// Launches `kernel` in clusters of `cluster` CTAs; its shared-memory limit is raised by the
-// first launch on each device.
+// Launches `kernel` in clusters of `cluster` CTAs.  On grids of up to 2048 CTAs it may be
+// scheduled while the previous kernel on the stream finishes: every kernel launched here
+// waits for that one (pdl_begin) before it touches global memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(KArgs...), unsigned grid, unsigned threads, size_t smem,
+                              unsigned cluster, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (pdl_mode() && grid <= 2048) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The same for kernels with dynamic shared memory, whose limit the first launch on each
+// device raises.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), std::atomic<uint64_t>& ready, unsigned grid,
                            unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
@@ -60,18 +89,7 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), std::atomic<uint64_t>& read
     if (err != cudaSuccess) return err;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch_overlapped(kernel, grid, threads, smem, cluster, st, args...);
 }
 
 }  // namespace ff

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = tmem_base;
+  pdl_begin();
 
   if (warp == 0) {
     // copies
@@ -440,6 +441,7 @@ cudaError_t launch_mode(bool wide, const GemmMaps& maps, GemmParams p, cudaStrea
   const int sms = multiprocessors();
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outputs;
   int64_t split = std::min<int64_t>(sms / tiles, (int64_t)p.k_blocks * p.phases / 4);
+  split = split >= 8 ? 8 : split >= 4 ? 4 : split;
   if (split >= 4 && tiles * split > sms * 7 / 8) split /= 2;
   if constexpr (halves == 1)  // two weights' shares of an eighth would be narrower than a store
     if (split >= 8) return launch_config<T, MODE, 1, 128, 8>(maps, p, st);

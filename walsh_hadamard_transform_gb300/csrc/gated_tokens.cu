@@ -10,7 +10,9 @@
 
 #include "activation.cuh"
 #include "feed_forward.cuh"
+#include "ff_host.cuh"
 #include "fwt.h"
+#include "tma.cuh"
 #include "tokens.cuh"
 
 namespace fwt {
@@ -66,6 +68,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) gated_tokens_kernel(const Ga
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[s][i][e] = 0.f;
 
+  pdl_begin();
   for (int first = warp; first < p.stretches; first += kTokenWarps * U) {
     uint4 wv[U][2][2][2], xv[U][NT][2];
 #pragma unroll
@@ -125,8 +128,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32) gated_tokens_kernel(const Ga
 
 template <typename T, int NT, int U>
 cudaError_t launch(const GatedTokenParams& p, cudaStream_t st) {
-  gated_tokens_kernel<T, NT, U><<<(unsigned)((p.f + 15) / 16), kTokenWarps * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(gated_tokens_kernel<T, NT, U>, (unsigned)((p.f + 15) / 16),
+                           kTokenWarps * 32, 0, 1, st, p);
 }
 template <typename T>
 cudaError_t run(const GatedTokenParams& p, cudaStream_t st) {

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = tmem_base;
+  pdl_begin();
 
   if (warp < 4) {
     if constexpr (BN == 256)
@@ -514,6 +515,7 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
   const int64_t tiles = (int64_t)((m + 127) / 128) * ((n + 63) / 64);
   // (clusters of four and eight do not fill every multiprocessor of a graphics cluster)
   int split = (int)std::min<int64_t>(sms / std::max<int64_t>(tiles, 1), p.blocks / 2);
+  split = split >= 8 ? 8 : split >= 4 ? 4 : split;
   if (split >= 4 && tiles * split > sms * 7 / 8) split /= 2;
   return m <= 64 ? run_split<64>(split, a, b, b_lines, p, k, st)
                  : run_split<128>(split, a, b, b_lines, p, k, st);

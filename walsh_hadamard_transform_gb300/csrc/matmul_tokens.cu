@@ -2,6 +2,12 @@
 // tokens.cuh for the scheme.  A CTA owns 16 lines of b; its warps take blocks of 128 of the
 // contraction in turn.  The sums of one block stay in the matrix products' fp32 accumulators
 // and are then added up in fp32, times both scales.  Bound: HBM (the bytes of b).
+//
+// Each warp has a ring of its own in shared memory that asynchronous copies fill: the bytes on
+// their way then cost no registers, and an SM holds enough of them.  (Loading straight to
+// registers measured 12.6 us for one token by 4096 x 8192: 163 registers a thread left one
+// CTA an SM, and two waves.)
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -9,8 +15,9 @@
 #include <cuda_runtime.h>
 
 #include "feed_forward.cuh"
+#include "ff_host.cuh"
 #include "fwt.h"
-#include "tokens.cuh"
+#include "tma.cuh"
 
 namespace fwt {
 namespace ff {
@@ -35,84 +42,119 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: groups of 8 tokens.  U: blocks whose loads a warp has in flight together.
-template <int NT, int U, int LINES>
-__global__ void __launch_bounds__(kTokenWarps * 32) tokens_kernel(const TokenParams p) {
-  __shared__ float sums[kTokenWarps][NT][32][4];
+// 16 (or 4) bytes to shared memory, `valid` of them from `from`, zeros after.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int valid) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(valid)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, int valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(valid)
+               : "memory");
+}
+
+// NT: groups of 8 tokens.  W: warps.  S: stages of a warp's ring, a block of 128 each.
+template <int NT, int W, int S>
+struct Ring {
+  static constexpr int kTokens = 2048, kScales = kTokens + NT * 1024;  // after 16 lines of b
+  static constexpr int kStage = kScales + (8 * NT + 16) * 4;
+  static constexpr int kBytes = S * W * kStage;
+};
+
+template <int NT, int W, int S, int LINES>
+__global__ void __launch_bounds__(W * 32) tokens_kernel(const TokenParams p) {
+  using R = Ring<NT, W, S>;
+  extern __shared__ __align__(16) uint8_t rings[];
+  __shared__ float sums[W][NT][32][4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int j0 = blockIdx.x * 16;
-  const uint8_t* w[2];
-  const float* ws[2];
+  uint8_t* ring = rings + warp * (S * R::kStage);
+  const uint32_t ring_at = smem_u32(ring);
+  pdl_begin();
+
+  // Rows of 128 bytes, the halves of odd ones swapped, so that the fragments' reads (64 bytes
+  // of two rows at a time) meet all banks.
+  auto fill = [&](int stage, int block) {
+    const uint32_t at = ring_at + stage * R::kStage;
+    if (block < p.blocks) {
+      const int chunk = lane & 7;
+      const int64_t k = (int64_t)block * 128 + 16 * chunk;
+      const int valid = (int)min((int64_t)16, max((int64_t)0, p.k - k));
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int j = j0 + g + 8 * r;
-    w[r] = j < p.n ? p.b + (int64_t)j * p.ld_b : nullptr;
-    ws[r] = j < p.n ? p.b_scale + (int64_t)(LINES == 1 ? j : j / 128) * p.ld_bs : nullptr;
-  }
+      for (int i = 0; i < 4 + 2 * NT; ++i) {  // of b, then of the tokens
+        const int row = (i < 4 ? i : i - 4) * 4 + (lane >> 3);
+        const bool in = i < 4 ? j0 + row < p.n : row < p.m;
+        const uint8_t* from = i < 4 ? p.b + (int64_t)(j0 + row) * p.ld_b : p.a + (int64_t)row * p.ld_a;
+        copy16(at + (i < 4 ? 0 : R::kTokens) + row * 128 + ((chunk ^ ((row & 1) << 2)) << 4),
+               in && valid ? from + k : p.b, in ? valid : 0);
+      }
+      if (lane < 8 * NT)
+        copy4(at + R::kScales + lane * 4, lane < p.m ? p.a_scale + lane * p.ld_as + block : p.a_scale,
+              lane < p.m ? 4 : 0);
+      if (lane < (LINES == 1 ? 16 : 1)) {
+        const int line = LINES == 1 ? j0 + lane : j0 / 128;
+        const bool in = LINES == 128 || line < p.n;
+        copy4(at + R::kScales + (8 * NT + lane) * 4,
+              in ? p.b_scale + (int64_t)line * p.ld_bs + block : p.b_scale, in ? 4 : 0);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < S; ++s) fill(s, warp + s * W);
+
   float sum[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
-
-  for (int first = warp; first < p.blocks; first += kTokenWarps * U) {
-    uint4 wv[U][2][2], xv[U][NT][2];
-    float sw[U][2], sx[U][NT][2];
+  int stage = 0;
+  for (int block = warp; block < p.blocks; block += W) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    __syncwarp();
+    const uint8_t* at = ring + stage * R::kStage;
+    const float* scales = (const float*)(at + R::kScales);
+    uint4 w[2][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int block = first + u * kTokenWarps;
-      const bool in = block < p.blocks;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int h = 0; h < 2; ++h)
+        w[r][h] = *(const uint4*)(at + (g + 8 * r) * 128 + (((4 * h + t) ^ ((g & 1) << 2)) << 4));
+    const float sw[2] = {scales[8 * NT + (LINES == 1 ? g : 0)], scales[8 * NT + (LINES == 1 ? g + 8 : 0)]};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          wv[u][r][h] = load16_once<1>(w[r], (int64_t)block * 128 + 64 * h + 16 * t, p.k);
+    for (int i = 0; i < NT; ++i) {
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) sw[u][r] = in && ws[r] ? __ldg(ws[r] + block) : 0.f;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int token = 8 * i + g;
-        const uint8_t* x = token < p.m ? p.a + token * p.ld_a : nullptr;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          xv[u][i][h] = load16<1>(x, (int64_t)block * 128 + 64 * h + 16 * t, p.k);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          sx[u][i][e] = in && 8 * i + 2 * t + e < p.m
-                            ? __ldg(p.a_scale + (8 * i + 2 * t + e) * p.ld_as + block) : 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = *(const uint4*)(at + R::kTokens + (8 * i + g) * 128 +
+                                        (((4 * h + t) ^ ((g & 1) << 2)) << 4));
+        const uint4 lo = w[0][h], hi = w[1][h];
+        mma_e4m3(part, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+        mma_e4m3(part, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
       }
+      const float2 sx = *(const float2*)&scales[8 * i + 2 * t];
+      sum[i][0] = fmaf(part[0], sw[0] * sx.x, sum[i][0]);
+      sum[i][1] = fmaf(part[1], sw[0] * sx.y, sum[i][1]);
+      sum[i][2] = fmaf(part[2], sw[1] * sx.x, sum[i][2]);
+      sum[i][3] = fmaf(part[3], sw[1] * sx.y, sum[i][3]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (first + u * kTokenWarps >= p.blocks) break;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 lo = wv[u][0][h], hi = wv[u][1][h], x = xv[u][i][h];
-          mma_e4m3(part, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
-          mma_e4m3(part, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sum[i][e] = fmaf(part[e], sw[u][e >> 1] * sx[u][i][e & 1], sum[i][e]);
-      }
-    }
+    __syncwarp();
+    fill(stage, block + S * W);
+    if (++stage == S) stage = 0;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 
 #pragma unroll
   for (int i = 0; i < NT; ++i)
     *(float4*)sums[warp][i][lane] = make_float4(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
   __syncthreads();
   // thread -> (token, line): 16 consecutive lines of a token's row of C
-  for (int o = threadIdx.x; o < NT * 128; o += kTokenWarps * 32) {
+  for (int o = threadIdx.x; o < NT * 128; o += W * 32) {
     const int token = o >> 4, line = o & 15;
     if (token >= p.m || j0 + line >= p.n) continue;
     const int from = 4 * (line & 7) + ((token & 7) >> 1), e = (line >> 3) * 2 + (token & 1);
     float v = 0.f;
 #pragma unroll
-    for (int s = 0; s < kTokenWarps; ++s) v += sums[s][token >> 3][from][e];
+    for (int s = 0; s < W; ++s) v += sums[s][token >> 3][from][e];
     const int64_t at = token * p.ld_c + j0 + line;
     if (p.c_type == FWT_F32) ((float*)p.c)[at] = v;
     else if (p.c_type == FWT_BF16) ((__nv_bfloat16*)p.c)[at] = __float2bfloat16_rn(v);
@@ -120,12 +162,21 @@ __global__ void __launch_bounds__(kTokenWarps * 32) tokens_kernel(const TokenPar
   }
 }
 
-template <int NT, int U>
+template <int NT, int W, int S, int LINES>
+cudaError_t launch(const TokenParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  return launch_cluster(tokens_kernel<NT, W, S, LINES>, ready, (unsigned)((p.n + 15) / 16), W * 32,
+                        Ring<NT, W, S>::kBytes, 1, st, p);
+}
+template <int NT, int W, int S>
 cudaError_t launch(const TokenParams& p, int lines, cudaStream_t st) {
-  const unsigned grid = (unsigned)((p.n + 15) / 16);
-  if (lines == 1) tokens_kernel<NT, U, 1><<<grid, kTokenWarps * 32, 0, st>>>(p);
-  else tokens_kernel<NT, U, 128><<<grid, kTokenWarps * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  return lines == 1 ? launch<NT, W, S, 1>(p, st) : launch<NT, W, S, 128>(p, st);
+}
+// Eight warps to 16 lines of b, or four where that many CTAs would come in a second wave.
+template <int NT, int S8, int S4>
+cudaError_t launch_few(const TokenParams& p, int lines, cudaStream_t st) {
+  return (p.n + 15) / 16 <= 2 * multiprocessors() ? launch<NT, 8, S8>(p, lines, st)
+                                                  : launch<NT, 4, S4>(p, lines, st);
 }
 
 }  // namespace
@@ -135,9 +186,9 @@ cudaError_t launch_matmul_tokens(CMat a, CMat a_scale, CMat b, CMat b_scale, int
   const TokenParams p{(const uint8_t*)a.p, (const uint8_t*)b.p, a.ld, b.ld,
                       (const float*)a_scale.p, (const float*)b_scale.p, a_scale.ld, b_scale.ld,
                       c.p, c.ld, c_type, m, n, k, (int)(((int64_t)k + 127) / 128)};
-  if (m <= 8) return launch<1, 4>(p, b_lines, st);
-  if (m <= 16) return launch<2, 2>(p, b_lines, st);
-  return launch<4, 1>(p, b_lines, st);
+  if (m <= 8) return launch_few<1, 4, 4>(p, b_lines, st);
+  if (m <= 16) return launch_few<2, 3, 4>(p, b_lines, st);
+  return launch_few<4, 2, 3>(p, b_lines, st);
 }
 
 }  // namespace ff

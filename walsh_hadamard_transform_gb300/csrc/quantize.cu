@@ -28,6 +28,7 @@
 #include "feed_forward.cuh"
 #include "ff_host.cuh"
 #include "fwt.h"
+#include "tma.cuh"
 
 namespace fwt {
 namespace ff {
@@ -215,7 +216,10 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
   int strip = blockIdx.x / per;
   if constexpr (kStep == W) block += warp;
   else strip = strip * W + warp;
-  if (LINES == 1 && (block >= p.blocks || strip >= p.strips)) return;
+  if (LINES == 1 && (block >= p.blocks || strip >= p.strips)) {
+    pdl_begin();
+    return;
+  }
   const int end = min(p.blocks, block + kStep * p.rounds);
 
   uint32_t b[2][2];
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
   const int lines[2] = {Block<T, AXIS>::line(strip, g, 0), Block<T, AXIS>::line(strip, g, 1)};
 
   Block<T, AXIS> x;
+  pdl_begin();
   x.load(p, strip, block, g, t);
   for (int round = 0; block < end; block += kStep, ++round) {
     float y[4][2][2][4];  // group of 32, bit 2, bit 1, (line, bit 0)
@@ -347,8 +352,7 @@ cudaError_t launch(QuantizeParams p, cudaStream_t st) {
   p.rounds = (int)std::max<int64_t>(1, std::min<int64_t>(4, across * steps / (8 * multiprocessors())));
   const int64_t grid = (steps + p.rounds - 1) / p.rounds * across;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  quantize_kernel<T, AXIS, LINES><<<(unsigned)grid, W * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(quantize_kernel<T, AXIS, LINES>, (unsigned)grid, W * 32, 0, 1, st, p);
 }
 
 template <typename T>
