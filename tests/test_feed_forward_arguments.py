@@ -90,7 +90,7 @@ def test_empty_calls_need_no_gpu(lib):
 
 def test_workspace_size(lib):
     size = lib.fwt_gated_backward_workspace_bytes
-    assert size(10, 100) == 10 * 104 * 2 * 2 and size(1, 1) == 32
+    assert size(10, 100) == 10 * 104 * 2 * 2 and size(1, 1) == size(8, 8) == 8 * 64
     assert size(0, 5) == 0 and size(5, 0) == 0 and size(-1, 5) == 0 and size(1 << 31, 1) == 0
     assert size(1 << 20, 1 << 14) == 1 << 36
 

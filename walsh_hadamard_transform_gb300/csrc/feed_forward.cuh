@@ -29,12 +29,19 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
 cudaError_t launch_gated(CMat x, CMat w_gate, CMat w_up, Mat h, int type, int activation, int m,
                          int f, int d, cudaStream_t st);
 
-// The same for at most kMostTokens lines of the first operand.
+// The same for a few lines of the first operand, at most kMostTokens.
 constexpr int kMostTokens = 32;
 cudaError_t launch_matmul_tokens(CMat a, CMat a_scale, CMat b, CMat b_scale, int b_lines, Mat c,
                                  int c_type, int m, int n, int k, cudaStream_t st);
 cudaError_t launch_gated_tokens(CMat x, CMat w_gate, CMat w_up, Mat h, int type, int activation,
                                 int m, int f, int d, cudaStream_t st);
+
+// The gradients for at most kMostGradientTokens lines, all in fp32 up to their one rounding.
+// `work`: 64 bytes for each of f.  dx, or dw_gate and dw_up, may be null.
+constexpr int kMostGradientTokens = 8;
+cudaError_t launch_gated_token_gradients(CMat grad, CMat x, CMat w_gate, CMat w_up, Mat dx,
+                                         Mat dw_gate, Mat dw_up, void* work, int type,
+                                         int activation, int m, int f, int d, cudaStream_t st);
 
 // dg and du into the workspace matrices, rows of ld elements (a multiple of 8).
 cudaError_t launch_gated_gradients(CMat grad, CMat x, CMat w_gate, CMat w_up, Mat dg, Mat du,

@@ -146,7 +146,9 @@ int fwt_gated(const void* x, int64_t ld_x, const void* w_gate, int64_t ld_gate, 
 
 size_t fwt_gated_backward_workspace_bytes(int64_t m, int64_t f) {
   if (m <= 0 || f <= 0 || m > kMaxExtent || f > kMaxExtent) return 0;
-  return (size_t)m * (size_t)((f + 7) / 8 * 8) * 4;  // dg and du, rows of a multiple of 8
+  const size_t line = (size_t)((f + 7) / 8 * 8);
+  if (m <= kMostGradientTokens) return line * 64;  // dg and du of 8 lines in fp32
+  return (size_t)m * line * 4;                     // dg and du, rows of a multiple of 8
 }
 
 int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t ld_x,
@@ -196,6 +198,11 @@ int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t
   for (int i = 0; i < 4; ++i)
     if (overlap(inputs[i], inputs[4])) return FWT_ERR_INVALID_ARG;
 
+  if (m <= kMostGradientTokens)
+    return done(launch_gated_token_gradients({grad, ld_grad}, {x, ld_x}, {w_gate, ld_gate},
+                                             {w_up, ld_up}, {dx, ld_dx}, {dw_gate, ld_dw_gate},
+                                             {dw_up, ld_dw_up}, workspace, type, activation, (int)m,
+                                             (int)f, (int)d, st));
   const int64_t ld = (f + 7) / 8 * 8;
   Mat dg{workspace, ld}, du{(char*)workspace + (size_t)m * (size_t)ld * 2, ld};
   const CMat cx{x, ld_x}, cg{w_gate, ld_gate}, cu{w_up, ld_up}, cdg{dg.p, ld}, cdu{du.p, ld};
