@@ -18,33 +18,36 @@ from __future__ import annotations
 import walsh_hadamard_transform_gb300 as _fwt
 
 _ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
-_torch = _REALS = _E4M3 = _F32 = _lib = _device = None
+_torch = _REALS = _E4M3 = _F32 = _lib = _device = _raw_stream = None
 
 
 def _load():
     """torch and the C library, on first use."""
-    global _torch, _REALS, _E4M3, _F32, _lib, _device
+    global _torch, _REALS, _E4M3, _F32, _lib, _device, _raw_stream
     torch = _fwt._torch_mod()
     _E4M3, _F32 = torch.float8_e4m3fn, torch.float32
     _REALS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     _torch = torch
     _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
     _lib = _fwt.library()
 
 
 def _matrix(t, name, device, dtype=None, shape=None):
-    """Row stride of a 2-D CUDA tensor with contiguous rows."""
+    """Row stride of a 2-D tensor with contiguous rows on CUDA device number ``device``."""
     size = t.shape
-    if len(size) != 2:
-        raise ValueError(f"{name}: expected a matrix, got {len(size)} dimensions")
-    if not t.is_cuda or t.device != device:
+    if size != shape:
+        if len(size) != 2:
+            raise ValueError(f"{name}: expected a matrix, got {len(size)} dimensions")
+        if shape is not None:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(size)}")
+    if device < 0 or t.get_device() != device:
         raise ValueError(f"{name}: every tensor must be on one CUDA device")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(size)}")
-    rows, cols = size
     row, col = t.stride()
+    rows, cols = size
     if col != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous")
     if rows <= 1:  # no second row: any stride will do
@@ -61,12 +64,16 @@ def _empty(rows, cols, dtype, device, multiple):
     return _torch.empty((rows, cols), dtype=dtype, device=device)
 
 
-def _run(device, entry, *args):
-    """Calls the C entry with ``device`` current."""
-    if device.index == _device():
-        return entry(*args)
+def _run(device, stream, entry, *args):
+    """Calls the C entry on ``stream`` (default: the current one) with the device current."""
+    if stream is not None:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    else:
+        handle = _raw_stream(device)
+    if device == _device():
+        return entry(*args, handle)
     with _torch.cuda.device(device):
-        return entry(*args)
+        return entry(*args, handle)
 
 
 def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None, stream=None):
@@ -85,7 +92,7 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     """
     if _lib is None:
         _load()
-    kind, device = _REALS.get(x.dtype), x.device
+    kind, device = _REALS.get(x.dtype), x.get_device()
     if kind is None:
         raise TypeError(f"unsupported dtype {x.dtype}: use float32, bfloat16 or float16")
     if axis not in (0, 1) or lines not in (1, 128) or not 0 <= rotate <= 7:
@@ -96,16 +103,15 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     length += -length % (1 << rotate)
     shape = (-(-across // lines), -(-length // 128))
     if out is None:
-        q = _empty(across, length, _E4M3, device, 16)
-        scale = _empty(*shape, _F32, device, 4)
+        q = _empty(across, length, _E4M3, x.device, 16)
+        scale = _empty(*shape, _F32, x.device, 4)
         ld_q, ld_s = q.stride(0), scale.stride(0)
     else:
         q, scale = out
         ld_q = _matrix(q, "codes", device, _E4M3, (across, length))
         ld_s = _matrix(scale, "scale", device, _F32, shape)
-    st = _run(device, _lib.fwt_quantize_blocks, x.data_ptr(), kind, rows, cols, ld, rotate, axis,
-              lines, q.data_ptr(), ld_q, scale.data_ptr(), ld_s,
-              _fwt._stream_handle(stream, device))
+    st = _run(device, stream, _lib.fwt_quantize_blocks, x.data_ptr(), kind, rows, cols, ld, rotate,
+              axis, lines, q.data_ptr(), ld_q, scale.data_ptr(), ld_s)
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_quantize_blocks({rows} x {cols}, axis={axis})")
     return q, scale
@@ -120,32 +126,32 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
     """
     if _lib is None:
         _load()
-    device = a.device
+    device = a.get_device()
     ld_a = _matrix(a, "a", device, _E4M3)
-    m, k = a.shape
     ld_b = _matrix(b, "b", device, _E4M3)
-    n = b.shape[0]
-    if b.shape[1] != k:
-        raise ValueError(f"a and b have {k} and {b.shape[1]} elements along the contraction")
+    m, k = a.shape
+    n, k_b = b.shape
+    if k_b != k:
+        raise ValueError(f"a and b have {k} and {k_b} elements along the contraction")
     blocks = -(-k // 128)
     ld_as = _matrix(a_scale, "a_scale", device, _F32, (m, blocks))
-    lines = 1 if len(b_scale.shape) == 2 and b_scale.shape[0] == n else 128
+    lines = 1 if b_scale.shape[:1] == (n,) else 128
     ld_bs = _matrix(b_scale, "b_scale", device, _F32, (-(-n // lines), blocks))
     if out is None:
         out_dtype = out_dtype or _torch.bfloat16
         kind = _REALS.get(out_dtype)
         if kind is None:
             raise TypeError(f"unsupported dtype {out_dtype}: use float32, bfloat16 or float16")
-        out = _empty(m, n, out_dtype, device, 4 if kind == 0 else 8)
+        out = _empty(m, n, out_dtype, a.device, 4 if kind == 0 else 8)
         ld_c = out.stride(0)
     else:
         kind = _REALS.get(out.dtype)
         if kind is None or (out_dtype is not None and out.dtype != out_dtype):
             raise TypeError(f"out: unsupported dtype {out.dtype}")
         ld_c = _matrix(out, "out", device, None, (m, n))
-    st = _run(device, _lib.fwt_matmul_blocks, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as,
+    st = _run(device, stream, _lib.fwt_matmul_blocks, a.data_ptr(), ld_a, a_scale.data_ptr(), ld_as,
               b.data_ptr(), ld_b, b_scale.data_ptr(), ld_bs, lines, out.data_ptr(), kind, ld_c, m, n,
-              k, _fwt._stream_handle(stream, device))
+              k)
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_matmul_blocks(m={m}, n={n}, k={k})")
     return out
@@ -154,18 +160,19 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
 def _gated_arguments(x, w_gate, w_up, activation):
     if _lib is None:
         _load()
-    kind, device = _REALS.get(x.dtype), x.device
-    if kind not in (1, 2):
-        raise TypeError(f"unsupported dtype {x.dtype}: use bfloat16 or float16")
+    dtype, device = x.dtype, x.get_device()
+    kind = _REALS.get(dtype)
+    if kind != 1 and kind != 2:
+        raise TypeError(f"unsupported dtype {dtype}: use bfloat16 or float16")
     act = _ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation {activation!r}: use one of {sorted(_ACTIVATIONS)}")
-    ld_x = _matrix(x, "x", device, x.dtype)
-    d = x.shape[1]
-    f = w_gate.shape[0]
-    ld_g = _matrix(w_gate, "w_gate", device, x.dtype, (f, d))
-    ld_u = _matrix(w_up, "w_up", device, x.dtype, (f, d))
-    return kind, act, device, x.shape[0], f, d, ld_x, ld_g, ld_u
+    ld_x = _matrix(x, "x", device)
+    m, d = x.shape
+    shape = (w_gate.shape[0], d)
+    ld_g = _matrix(w_gate, "w_gate", device, dtype, shape)
+    ld_u = _matrix(w_up, "w_up", device, dtype, shape)
+    return dtype, kind, act, device, m, shape[0], d, ld_x, ld_g, ld_u
 
 
 def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
@@ -174,14 +181,15 @@ def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
 
     ``x`` (m, d), ``w_gate`` and ``w_up`` (f, d): bfloat16 or float16, all of one type.
     ``activation``: "silu", "gelu" (the tanh form) or "relu".  Returns h (m, f)."""
-    kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up, activation)
+    dtype, kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up,
+                                                                           activation)
     if out is None:
-        out = _empty(m, f, x.dtype, device, 8)
+        out = _empty(m, f, dtype, x.device, 8)
         ld_h = out.stride(0)
     else:
-        ld_h = _matrix(out, "out", device, x.dtype, (m, f))
-    st = _run(device, _lib.fwt_gated, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(),
-              ld_u, out.data_ptr(), ld_h, kind, act, m, f, d, _fwt._stream_handle(stream, device))
+        ld_h = _matrix(out, "out", device, dtype, (m, f))
+    st = _run(device, stream, _lib.fwt_gated, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g,
+              w_up.data_ptr(), ld_u, out.data_ptr(), ld_h, kind, act, m, f, d)
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_gated(m={m}, f={f}, d={d})")
     return out
@@ -196,33 +204,48 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
     three tensors to write to.  ``workspace``: a CUDA tensor of at least
     ``fwt_gated_backward_workspace_bytes(m, f)`` bytes for the gradients of the two
     products (allocated here when None)."""
-    kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up, activation)
-    ld_dy = _matrix(grad, "grad", device, x.dtype, (m, f))
+    dtype, kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up,
+                                                                           activation)
+    ld_dy = _matrix(grad, "grad", device, dtype, (m, f))
     want_x, want_w = "x" in want, "w" in want
-    if out is None:
-        out = (_empty(m, d, x.dtype, device, 8) if want_x else None,
-               _empty(f, d, x.dtype, device, 8) if want_w else None,
-               _empty(f, d, x.dtype, device, 8) if want_w else None)
-    dx, dw_gate, dw_up = out
-    if want_x != (dx is not None) or want_w != (dw_gate is not None) or want_w != (dw_up is not None):
-        raise ValueError("out must hold the gradients named in want, and no other")
-    ld_dx = _matrix(dx, "dx", device, x.dtype, (m, d)) if want_x else 0
-    ld_dg = _matrix(dw_gate, "dw_gate", device, x.dtype, (f, d)) if want_w else 0
-    ld_du = _matrix(dw_up, "dw_up", device, x.dtype, (f, d)) if want_w else 0
+    dx = dw_gate = dw_up = None
+    p_dx = p_dg = p_du = None
+    ld_dx = ld_dg = ld_du = 0
+    if out is not None:
+        dx, dw_gate, dw_up = out
+        if (want_x != (dx is not None) or want_w != (dw_gate is not None)
+                or want_w != (dw_up is not None)):
+            raise ValueError("out must hold the gradients named in want, and no other")
+    if want_x:
+        if dx is None:
+            dx = _empty(m, d, dtype, x.device, 8)
+            ld_dx = dx.stride(0)
+        else:
+            ld_dx = _matrix(dx, "dx", device, dtype, (m, d))
+        p_dx = dx.data_ptr()
+    if want_w:
+        if dw_gate is None:
+            dw_gate = _empty(f, d, dtype, x.device, 8)
+            dw_up = _empty(f, d, dtype, x.device, 8)
+            ld_dg = ld_du = dw_gate.stride(0)
+        else:
+            ld_dg = _matrix(dw_gate, "dw_gate", device, dtype, (f, d))
+            ld_du = _matrix(dw_up, "dw_up", device, dtype, (f, d))
+        p_dg, p_du = dw_gate.data_ptr(), dw_up.data_ptr()
     if workspace is None:
-        workspace = _torch.empty(_lib.fwt_gated_backward_workspace_bytes(m, f), dtype=_torch.uint8,
-                                 device=device)
+        size = _lib.fwt_gated_backward_workspace_bytes(m, f)
+        workspace = _torch.empty(size, dtype=_torch.uint8, device=x.device)
         if stream is not None:
             # the allocator must not hand the memory on before `stream` is done with it
             workspace.record_stream(stream if hasattr(stream, "cuda_stream")
-                                    else _torch.cuda.ExternalStream(int(stream), device=device))
-    elif workspace.device != device or not workspace.is_contiguous():
+                                    else _torch.cuda.ExternalStream(int(stream), device=x.device))
+    elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    pointer = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    st = _run(device, _lib.fwt_gated_backward, grad.data_ptr(), ld_dy, x.data_ptr(), ld_x,
-              w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, pointer(dx), ld_dx, pointer(dw_gate),
-              ld_dg, pointer(dw_up), ld_du, kind, act, m, f, d, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), _fwt._stream_handle(stream, device))
+    else:
+        size = workspace.numel() * workspace.element_size()
+    st = _run(device, stream, _lib.fwt_gated_backward, grad.data_ptr(), ld_dy, x.data_ptr(), ld_x,
+              w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, p_dx, ld_dx, p_dg, ld_dg, p_du, ld_du,
+              kind, act, m, f, d, workspace.data_ptr(), size)
     if st != _fwt.FWT_OK:
         raise _fwt.FwtError(st, f"fwt_gated_backward(m={m}, f={f}, d={d})")
     return dx, dw_gate, dw_up
