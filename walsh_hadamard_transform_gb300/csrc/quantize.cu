@@ -47,6 +47,7 @@ struct QuantizeParams {
   float norm;  // 2^(-r/2)
   int rounds;  // blocks a warp goes through
   int vec;     // rows of x start on 16-byte boundaries (axis 0: on two elements')
+  int vec16;   // on 16-byte boundaries, whichever axis
 };
 
 template <typename T>
@@ -197,6 +198,32 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// 16-bit inputs along the rows with 16-byte aligned rows take another way in: 128 rows of the
+// CTA's lines (16 a warp) come to shared memory by asynchronous 16-byte copies, a block ahead,
+// and go into the product's slots transposed.  Rows lie 32 W bytes apart, their chunks
+// swizzled so that the eight rows that one 8 x 8 matrix takes (0, 1, 8, 9, 16, ...) meet
+// different banks.
+template <int W>
+__device__ __forceinline__ uint32_t staged_at(int pos, int chunk) {
+  return (uint32_t)(pos * 2 * W + (chunk ^ ((pos & 1) | ((pos >> 2) & 6)))) * 16;
+}
+template <int W>
+__device__ __forceinline__ void stage_block(const QuantizeParams& p, uint32_t to, int line0, int block) {
+  constexpr int kChunks = 2 * W;
+  const int chunk = threadIdx.x % kChunks, line = line0 + 8 * chunk;
+  const int bytes = min(16, max(0, (p.nl - line) * 2));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int pos = i * 16 + threadIdx.x / kChunks, row = block * 128 + pos;
+    const int valid = row < p.length ? bytes : 0;
+    const uint8_t* from = (const uint8_t*)p.x + (valid ? ((int64_t)row * p.ld_x + line) * 2 : 0);
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
+                     to + staged_at<W>(pos, chunk)), "l"(from), "r"(valid)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
 // Warps of a CTA: consecutive blocks of one strip (axis 1) or consecutive strips (axis 0), so
 // that a CTA reads long runs of rows; with 128 lines to a scale, the eight strips of one tile.
 // Each then goes on along the axis, `rounds` blocks in all, the loads of the next block on
@@ -204,10 +231,12 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 template <int LINES>
 constexpr int kWarps = LINES == 1 ? 4 : 8;
 
-template <typename T, int AXIS, int LINES>
+template <typename T, int AXIS, int LINES, bool STAGED>
 __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizeParams p) {
   constexpr int W = kWarps<LINES>;
-  constexpr bool kAhead = sizeof(T) == 2;  // fp32 blocks take twice the registers
+  constexpr bool kAhead = sizeof(T) == 2 && !STAGED;  // fp32 blocks take twice the registers
+  constexpr int kStaged = 128 * 32 * W;               // bytes of a staged block
+  extern __shared__ __align__(128) uint8_t staged[];
   constexpr int kStep = AXIS == 1 && LINES == 1 ? W : 1;
   using M = typename Input<T>::Mma;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -216,7 +245,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
   int strip = blockIdx.x / per;
   if constexpr (kStep == W) block += warp;
   else strip = strip * W + warp;
-  if (LINES == 1 && (block >= p.blocks || strip >= p.strips)) {
+  if (!STAGED && LINES == 1 && (block >= p.blocks || strip >= p.strips)) {
     pdl_begin();
     return;
   }
@@ -230,13 +259,27 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
     for (int h = 0; h < 2; ++h)
       b[n][h] = sign16<M>(8 * t + 2 * h, en, p.r) | (sign16<M>(8 * t + 2 * h + 1, en, p.r) << 16);
   }
-  const int lines[2] = {Block<T, AXIS>::line(strip, g, 0), Block<T, AXIS>::line(strip, g, 1)};
+  const int lines[2] = {STAGED ? strip * 16 + g : Block<T, AXIS>::line(strip, g, 0),
+                        STAGED ? strip * 16 + g + 8 : Block<T, AXIS>::line(strip, g, 1)};
 
   Block<T, AXIS> x;
   pdl_begin();
-  x.load(p, strip, block, g, t);
+  const uint32_t buffers = STAGED ? smem_u32(staged) : 0;
+  const int line0 = (strip - warp) * 16;
+  if constexpr (STAGED) stage_block<W>(p, buffers, line0, block);
+  else x.load(p, strip, block, g, t);
   for (int round = 0; block < end; block += kStep, ++round) {
     float y[4][2][2][4];  // group of 32, bit 2, bit 1, (line, bit 0)
+    const uint32_t now = buffers + (round & 1) * kStaged;
+    if constexpr (STAGED) {
+      if (block + kStep < end) {
+        stage_block<W>(p, buffers + ((round & 1) ^ 1) * kStaged, line0, block + kStep);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      __syncthreads();
+    }
 #pragma unroll
     for (int grp = 0; grp < 4; ++grp)
 #pragma unroll
@@ -247,12 +290,24 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
           for (int i = 0; i < 4; ++i) y[grp][h][n][i] = 0.f;
 #pragma unroll
         for (int k = 0; k < Input<T>::kPieces; ++k) {
-          const uint32_t a[4] = {x.pair(grp, 2 * h, 0), x.pair(grp, 2 * h, 1),
-                                 x.pair(grp, 2 * h + 1, 0), x.pair(grp, 2 * h + 1, 1)};
+          uint32_t a[4];
+          if constexpr (STAGED) {
+            // lane -> a row of one of four 8 x 8 matrices: elements 0, 1 or 2, 3 (lanes 16 on)
+            // of each thread's four, lines 0..7 or 8..15 (odd eights of lanes)
+            const int pos = 32 * grp + 4 * h + 8 * ((lane & 7) >> 1) + 2 * (lane >> 4) + (lane & 1);
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                         : "r"(now + staged_at<W>(pos, 2 * warp + ((lane >> 3) & 1)))
+                         : "memory");
+          } else {
+            a[0] = x.pair(grp, 2 * h, 0), a[1] = x.pair(grp, 2 * h, 1);
+            a[2] = x.pair(grp, 2 * h + 1, 0), a[3] = x.pair(grp, 2 * h + 1, 1);
+          }
           mma16<M>(y[grp][h][0], a, b[0]);
           mma16<M>(y[grp][h][1], a, b[1]);
         }
       }
+    if (STAGED) __syncthreads();  // the next round's copies may overwrite the block
     if (kAhead && block + kStep < end) x.load(p, strip, block + kStep, g, t);
 
     if (p.r > 2) {
@@ -338,11 +393,11 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
       }
       __syncwarp();
     }
-    if (!kAhead && block + kStep < end) x.load(p, strip, block + kStep, g, t);
+    if (!kAhead && !STAGED && block + kStep < end) x.load(p, strip, block + kStep, g, t);
   }
 }
 
-template <typename T, int AXIS, int LINES>
+template <typename T, int AXIS, int LINES, bool STAGED>
 cudaError_t launch(QuantizeParams p, cudaStream_t st) {
   constexpr int W = kWarps<LINES>;
   constexpr int kStep = AXIS == 1 && LINES == 1 ? W : 1;
@@ -352,13 +407,22 @@ cudaError_t launch(QuantizeParams p, cudaStream_t st) {
   p.rounds = (int)std::max<int64_t>(1, std::min<int64_t>(4, across * steps / (8 * multiprocessors())));
   const int64_t grid = (steps + p.rounds - 1) / p.rounds * across;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_overlapped(quantize_kernel<T, AXIS, LINES>, (unsigned)grid, W * 32, 0, 1, st, p);
+  if constexpr (STAGED) {
+    static std::atomic<uint64_t> ready{0};
+    return launch_cluster(quantize_kernel<T, AXIS, LINES, true>, ready, (unsigned)grid, W * 32,
+                          2 * 128 * 32 * W, 1, st, p);
+  } else {
+    return launch_overlapped(quantize_kernel<T, AXIS, LINES, false>, (unsigned)grid, W * 32, 0, 1, st, p);
+  }
 }
 
 template <typename T>
 cudaError_t launch(const QuantizeParams& p, int axis, int lines, cudaStream_t st) {
-  if (axis == 1) return lines == 1 ? launch<T, 1, 1>(p, st) : launch<T, 1, 128>(p, st);
-  return lines == 1 ? launch<T, 0, 1>(p, st) : launch<T, 0, 128>(p, st);
+  if (axis == 1)
+    return lines == 1 ? launch<T, 1, 1, false>(p, st) : launch<T, 1, 128, false>(p, st);
+  if constexpr (sizeof(T) == 2)
+    if (p.vec16) return lines == 1 ? launch<T, 0, 1, true>(p, st) : launch<T, 0, 128, true>(p, st);
+  return lines == 1 ? launch<T, 0, 1, false>(p, st) : launch<T, 0, 128, false>(p, st);
 }
 
 }  // namespace
@@ -382,6 +446,7 @@ cudaError_t launch_quantize(CMat x, int x_type, int rows, int cols, int rot_bits
   const int size = x_type == FWT_F32 ? 4 : 2;
   const int unit = axis ? 16 : 2 * size;
   p.vec = (uintptr_t)x.p % (unsigned)unit == 0 && (x.ld * size) % unit == 0;
+  p.vec16 = (uintptr_t)x.p % 16 == 0 && (x.ld * size) % 16 == 0;
   if (x_type == FWT_F32) return launch<float>(p, axis, lines, st);
   if (x_type == FWT_BF16) return launch<__nv_bfloat16>(p, axis, lines, st);
   return launch<__half>(p, axis, lines, st);
