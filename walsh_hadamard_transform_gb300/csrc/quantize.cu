@@ -198,30 +198,47 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// 16-bit inputs along the rows with 16-byte aligned rows take another way in: 128 rows of the
-// CTA's lines (16 a warp) come to shared memory by asynchronous 16-byte copies, a block ahead,
-// and go into the product's slots transposed.  Rows lie 32 W bytes apart, their chunks
-// swizzled so that the eight rows that one 8 x 8 matrix takes (0, 1, 8, 9, 16, ...) meet
-// different banks.
+// 16-bit inputs whose rows are 16-byte aligned take another way in: asynchronous 16-byte copies
+// bring blocks ahead to shared memory, where they cost no registers (loaded to registers, a
+// block ahead, the warps an SM holds had too few bytes on their way: 8192 x 8192 took 42.9 us
+// along the columns and 53 down the rows).
+//
+// Along the columns each warp has its own stages: 16 rows of 256 bytes, the halves of every 128
+// swapped in odd rows so that the reads (64 bytes of two rows at a time) meet all banks.
+__device__ __forceinline__ uint32_t row_at(int row, int chunk) {
+  return (uint32_t)(row * 256 + ((chunk ^ ((row & 1) << 2)) << 4));
+}
+__device__ __forceinline__ void copy16(uint32_t to, const QuantizeParams& p, int64_t element, int valid) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to),
+               "l"((const uint8_t*)p.x + (valid ? element * 2 : 0)), "r"(valid)
+               : "memory");
+}
+__device__ __forceinline__ void stage_rows(const QuantizeParams& p, uint32_t to, int strip, int block) {
+  const int lane = threadIdx.x & 31, chunk = lane & 15, col = block * 128 + 8 * chunk;
+  const int bytes = min(16, max(0, (p.length - col) * 2));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 2 * i + (lane >> 4), line = strip * 16 + row;
+    copy16(to + row_at(row, chunk), p, (int64_t)line * p.ld_x + col, line < p.nl ? bytes : 0);
+  }
+}
+// Down the rows the CTA has stages in common: 128 rows of its lines (16 a warp), 32 W bytes
+// apart, which go into the product's slots transposed.  The chunks are swizzled so that the
+// eight rows that one 8 x 8 matrix takes (0, 1, 8, 9, 16, ...) meet different banks.
 template <int W>
-__device__ __forceinline__ uint32_t staged_at(int pos, int chunk) {
+__device__ __forceinline__ uint32_t column_at(int pos, int chunk) {
   return (uint32_t)(pos * 2 * W + (chunk ^ ((pos & 1) | ((pos >> 2) & 6)))) * 16;
 }
 template <int W>
-__device__ __forceinline__ void stage_block(const QuantizeParams& p, uint32_t to, int line0, int block) {
+__device__ __forceinline__ void stage_columns(const QuantizeParams& p, uint32_t to, int line0, int block) {
   constexpr int kChunks = 2 * W;
   const int chunk = threadIdx.x % kChunks, line = line0 + 8 * chunk;
   const int bytes = min(16, max(0, (p.nl - line) * 2));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int pos = i * 16 + threadIdx.x / kChunks, row = block * 128 + pos;
-    const int valid = row < p.length ? bytes : 0;
-    const uint8_t* from = (const uint8_t*)p.x + (valid ? ((int64_t)row * p.ld_x + line) * 2 : 0);
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
-                     to + staged_at<W>(pos, chunk)), "l"(from), "r"(valid)
-                 : "memory");
+    copy16(to + column_at<W>(pos, chunk), p, (int64_t)row * p.ld_x + line, row < p.length ? bytes : 0);
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // Warps of a CTA: consecutive blocks of one strip (axis 1) or consecutive strips (axis 0), so
@@ -231,11 +248,18 @@ __device__ __forceinline__ void stage_block(const QuantizeParams& p, uint32_t to
 template <int LINES>
 constexpr int kWarps = LINES == 1 ? 4 : 8;
 
+template <int AXIS, int LINES>
+struct Stages {
+  static constexpr int kCount = AXIS == 1 && LINES == 1 ? 3 : 2;
+  static constexpr size_t kBytes = (size_t)kCount * kWarps<LINES> * 4096;
+};
+
 template <typename T, int AXIS, int LINES, bool STAGED>
 __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizeParams p) {
   constexpr int W = kWarps<LINES>;
   constexpr bool kAhead = sizeof(T) == 2 && !STAGED;  // fp32 blocks take twice the registers
-  constexpr int kStaged = 128 * 32 * W;               // bytes of a staged block
+  constexpr int kStaged = AXIS == 1 ? 4096 : 128 * 32 * W;  // bytes of a stage (axis 1: a warp's)
+  constexpr int kStages = Stages<AXIS, LINES>::kCount;
   extern __shared__ __align__(128) uint8_t staged[];
   constexpr int kStep = AXIS == 1 && LINES == 1 ? W : 1;
   using M = typename Input<T>::Mma;
@@ -245,7 +269,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
   int strip = blockIdx.x / per;
   if constexpr (kStep == W) block += warp;
   else strip = strip * W + warp;
-  if (!STAGED && LINES == 1 && (block >= p.blocks || strip >= p.strips)) {
+  if (!(STAGED && AXIS == 0) && LINES == 1 && (block >= p.blocks || strip >= p.strips)) {
     pdl_begin();
     return;
   }
@@ -264,21 +288,29 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
 
   Block<T, AXIS> x;
   pdl_begin();
-  const uint32_t buffers = STAGED ? smem_u32(staged) : 0;
-  const int line0 = (strip - warp) * 16;
-  if constexpr (STAGED) stage_block<W>(p, buffers, line0, block);
-  else x.load(p, strip, block, g, t);
+  const uint32_t buffers = STAGED ? smem_u32(staged) + (AXIS == 1 ? warp * kStages * kStaged : 0) : 0;
+  auto stage = [&](int round, int at) {
+    if (at < end) {
+      const uint32_t to = buffers + round % kStages * kStaged;
+      if constexpr (AXIS == 1) stage_rows(p, to, strip, at);
+      else stage_columns<W>(p, to, (strip - warp) * 16, at);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (STAGED) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) stage(i, block + i * kStep);
+  } else {
+    x.load(p, strip, block, g, t);
+  }
   for (int round = 0; block < end; block += kStep, ++round) {
     float y[4][2][2][4];  // group of 32, bit 2, bit 1, (line, bit 0)
-    const uint32_t now = buffers + (round & 1) * kStaged;
+    const int now = round % kStages * kStaged;
     if constexpr (STAGED) {
-      if (block + kStep < end) {
-        stage_block<W>(p, buffers + ((round & 1) ^ 1) * kStaged, line0, block + kStep);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
-      __syncthreads();
+      stage(round + kStages - 1, block + (kStages - 1) * kStep);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      if constexpr (AXIS == 1) __syncwarp();
+      else __syncthreads();
     }
 #pragma unroll
     for (int grp = 0; grp < 4; ++grp)
@@ -291,13 +323,18 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
 #pragma unroll
         for (int k = 0; k < Input<T>::kPieces; ++k) {
           uint32_t a[4];
-          if constexpr (STAGED) {
+          if constexpr (STAGED && AXIS == 1) {
+            const uint8_t* from = staged + (buffers - smem_u32(staged)) + now + 8 * h;
+            const uint2 lo = *(const uint2*)(from + row_at(g, 4 * grp + t));
+            const uint2 hi = *(const uint2*)(from + row_at(g + 8, 4 * grp + t));
+            a[0] = lo.x, a[1] = hi.x, a[2] = lo.y, a[3] = hi.y;
+          } else if constexpr (STAGED) {
             // lane -> a row of one of four 8 x 8 matrices: elements 0, 1 or 2, 3 (lanes 16 on)
             // of each thread's four, lines 0..7 or 8..15 (odd eights of lanes)
             const int pos = 32 * grp + 4 * h + 8 * ((lane & 7) >> 1) + 2 * (lane >> 4) + (lane & 1);
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                         : "r"(now + staged_at<W>(pos, 2 * warp + ((lane >> 3) & 1)))
+                         : "r"(buffers + now + column_at<W>(pos, 2 * warp + ((lane >> 3) & 1)))
                          : "memory");
           } else {
             a[0] = x.pair(grp, 2 * h, 0), a[1] = x.pair(grp, 2 * h, 1);
@@ -307,7 +344,9 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32) quantize_kernel(QuantizePa
           mma16<M>(y[grp][h][1], a, b[1]);
         }
       }
-    if (STAGED) __syncthreads();  // the next round's copies may overwrite the block
+    // the next round's copies overwrite the stage that was read the longest ago: this one
+    if constexpr (STAGED && AXIS == 1) __syncwarp();
+    else if constexpr (STAGED) __syncthreads();
     if (kAhead && block + kStep < end) x.load(p, strip, block + kStep, g, t);
 
     if (p.r > 2) {
@@ -410,19 +449,23 @@ cudaError_t launch(QuantizeParams p, cudaStream_t st) {
   if constexpr (STAGED) {
     static std::atomic<uint64_t> ready{0};
     return launch_cluster(quantize_kernel<T, AXIS, LINES, true>, ready, (unsigned)grid, W * 32,
-                          2 * 128 * 32 * W, 1, st, p);
+                          Stages<AXIS, LINES>::kBytes, 1, st, p);
   } else {
     return launch_overlapped(quantize_kernel<T, AXIS, LINES, false>, (unsigned)grid, W * 32, 0, 1, st, p);
   }
 }
 
+template <typename T, bool STAGED>
+cudaError_t launch(const QuantizeParams& p, int axis, int lines, cudaStream_t st) {
+  if (axis == 1) return lines == 1 ? launch<T, 1, 1, STAGED>(p, st) : launch<T, 1, 128, STAGED>(p, st);
+  return lines == 1 ? launch<T, 0, 1, STAGED>(p, st) : launch<T, 0, 128, STAGED>(p, st);
+}
+
 template <typename T>
 cudaError_t launch(const QuantizeParams& p, int axis, int lines, cudaStream_t st) {
-  if (axis == 1)
-    return lines == 1 ? launch<T, 1, 1, false>(p, st) : launch<T, 1, 128, false>(p, st);
   if constexpr (sizeof(T) == 2)
-    if (p.vec16) return lines == 1 ? launch<T, 0, 1, true>(p, st) : launch<T, 0, 128, true>(p, st);
-  return lines == 1 ? launch<T, 0, 1, false>(p, st) : launch<T, 0, 128, false>(p, st);
+    if (p.vec16) return launch<T, true>(p, axis, lines, st);
+  return launch<T, false>(p, axis, lines, st);
 }
 
 }  // namespace
