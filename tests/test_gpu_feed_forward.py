@@ -323,6 +323,7 @@ BACKWARD = [
     (517, 333, 401, "f16", "gelu"), (600, 1024, 900, "bf16", "silu"), (1025, 128, 260, "bf16", "relu"),
     (1, 1500, 300, "f16", "silu"), (2, 2048, 70, "bf16", "relu"), (5, 1001, 900, "bf16", "gelu"),
     (8, 260, 2057, "f16", "silu"), (9, 700, 520, "f16", "relu"),
+    (40, 300, 1100, "bf16", "gelu"),
     (1500, 1303, 2105, "bf16", "silu"), (2307, 2500, 300, "f16", "gelu"),
 ]
 

@@ -428,31 +428,41 @@ cudaError_t launch_config(const GemmMaps& maps, const GemmParams& p, cudaStream_
                         Config<CG, BN>::kSmem, CG * SPLIT, st, maps, p);
 }
 
-template <typename T, int MODE>
-cudaError_t launch_mode(bool wide, const GemmMaps& maps, GemmParams p, cudaStream_t st) {
-  constexpr int halves = MODE == kForward || MODE == kGradients ? 2 : 1;
-  const int rows = wide ? 256 : 128, cols = (wide ? 256 : 128) / halves;
-  p.tiles_m = (p.m + rows - 1) / rows;
-  p.tiles_n = (p.n + cols - 1) / cols;
-  if (wide) return launch_config<T, MODE, 2, 256, 1>(maps, p, st);
-  // Where the tiles leave multiprocessors idle, clusters share out the contraction, four
-  // stages a CTA at least.  (Clusters of four and eight do not fill every multiprocessor of a
-  // graphics cluster.)
-  const int sms = multiprocessors();
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outputs;
-  int64_t split = std::min<int64_t>(sms / tiles, (int64_t)p.k_blocks * p.phases / 4);
-  split = split >= 8 ? 8 : split >= 4 ? 4 : split;
-  if (split >= 4 && tiles * split > sms * 7 / 8) split /= 2;
-  if constexpr (halves == 1)  // two weights' shares of an eighth would be narrower than a store
-    if (split >= 8) return launch_config<T, MODE, 1, 128, 8>(maps, p, st);
-  if (split >= 4) return launch_config<T, MODE, 1, 128, 4>(maps, p, st);
-  if (split >= 2) return launch_config<T, MODE, 1, 128, 2>(maps, p, st);
-  return launch_config<T, MODE, 1, 128, 1>(maps, p, st);
+// How a product is cut: pairs of CTAs on 256 x 256 tiles, or single ones on 128 x 128 whose
+// contraction a cluster of `split` shares out where the tiles leave multiprocessors idle.
+struct Cut {
+  bool wide;
+  int split;
+};
+
+// A stage costs a CTA about the same either way (it moves 32 KB), so what counts is the stages
+// that one CTA after the other goes through: waves of tiles times stages a tile.
+Cut choose_cut(int64_t m, int64_t n, int outputs, int64_t stages, int most_split) {
+  const int64_t sms = multiprocessors();
+  const auto tiles = [&](int64_t size) { return ((m + size - 1) / size) * ((n + size - 1) / size) * outputs; };
+  const int64_t wide = (tiles(256) + sms / 2 - 1) / (sms / 2) * stages, small = tiles(128);
+  // (four stages a CTA at least; clusters of four and eight do not fill every multiprocessor
+  // of a graphics cluster)
+  int split = 1;
+  while (2 * split <= most_split && 2 * split * small <= (split >= 2 ? sms * 7 / 8 : sms) &&
+         2 * split * 4 <= stages)
+    split *= 2;
+  const int64_t rest = (small * split + sms - 1) / sms * ((stages + split - 1) / split);
+  return wide < rest ? Cut{true, 1} : Cut{false, split};
 }
 
-// Whether pairs of CTAs on 256 x 256 tiles fill the device: else smaller tiles.
-bool wide_tiles(int m, int n, int outputs) {
-  return (int64_t)((m + 255) / 256) * ((n + 255) / 256) * outputs * 2 >= multiprocessors();
+template <typename T, int MODE>
+cudaError_t launch_mode(Cut cut, const GemmMaps& maps, GemmParams p, cudaStream_t st) {
+  constexpr int halves = MODE == kForward || MODE == kGradients ? 2 : 1;
+  const int rows = cut.wide ? 256 : 128, cols = (cut.wide ? 256 : 128) / halves;
+  p.tiles_m = (p.m + rows - 1) / rows;
+  p.tiles_n = (p.n + cols - 1) / cols;
+  if (cut.wide) return launch_config<T, MODE, 2, 256, 1>(maps, p, st);
+  if constexpr (halves == 1)
+    if (cut.split == 8) return launch_config<T, MODE, 1, 128, 8>(maps, p, st);
+  if (cut.split == 4) return launch_config<T, MODE, 1, 128, 4>(maps, p, st);
+  if (cut.split == 2) return launch_config<T, MODE, 1, 128, 2>(maps, p, st);
+  return launch_config<T, MODE, 1, 128, 1>(maps, p, st);
 }
 
 struct Operand {
@@ -473,17 +483,18 @@ bool vector_rows(Mat m) { return ((uintptr_t)m.p & 15u) == 0 && m.ld % 8 == 0; }
 
 template <typename T, int MODE>
 cudaError_t run_paired(CMat x, CMat w_gate, CMat w_up, GemmParams p, int d, cudaStream_t st) {
-  const bool wide = wide_tiles(p.m, 2 * p.n, 1);
-  const int box = wide ? 128 : 64;  // lines of each weight in a stage
+  p.k_blocks = (d + kTileK - 1) / kTileK;
+  p.phases = p.outputs = 1;
+  // (both weights' columns count; an eighth of them would be narrower than a store)
+  const Cut cut = choose_cut(p.m, 2 * (int64_t)p.n, 1, p.k_blocks, 4);
+  const int box = cut.wide ? 128 : 64;  // lines of each weight in a stage
   GemmMaps maps;
   if (!make_map<T>(&maps.a[0], {x, p.m, d, 128}) ||
       !make_map<T>(&maps.b[0], {w_gate, p.n, d, box}) ||
       !make_map<T>(&maps.b[1], {w_up, p.n, d, box}))
     return cudaErrorInvalidValue;
   maps.a[1] = maps.a[0];
-  p.k_blocks = (d + kTileK - 1) / kTileK;
-  p.phases = p.outputs = 1;
-  return launch_mode<T, MODE>(wide, maps, p, st);
+  return launch_mode<T, MODE>(cut, maps, p, st);
 }
 
 template <typename T>
@@ -497,7 +508,7 @@ cudaError_t run_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, int m, int 
   GemmParams p{};
   p.m = m, p.n = d, p.k_blocks = (f + kTileK - 1) / kTileK, p.phases = 2, p.outputs = 1;
   p.out[0] = dx.p, p.ld_out[0] = dx.ld, p.vec = vector_rows(dx);
-  return launch_mode<T, kDx>(wide_tiles(m, d, 1), maps, p, st);
+  return launch_mode<T, kDx>(choose_cut(m, d, 1, 2 * (int64_t)p.k_blocks, 8), maps, p, st);
 }
 
 template <typename T>
@@ -513,7 +524,7 @@ cudaError_t run_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int m, int 
   p.out[0] = dw_gate.p, p.ld_out[0] = dw_gate.ld;
   p.out[1] = dw_up.p, p.ld_out[1] = dw_up.ld;
   p.vec = vector_rows(dw_gate) && vector_rows(dw_up);
-  return launch_mode<T, kDw>(wide_tiles(f, d, 2), maps, p, st);
+  return launch_mode<T, kDw>(choose_cut(f, d, 2, p.k_blocks, 8), maps, p, st);
 }
 
 }  // namespace

@@ -107,13 +107,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 template <typename C, int N>
 __device__ __forceinline__ void store_rows(const BlocksParams& p, uint8_t* piece, int row0, int lane,
                                            int col, const float (&acc)[N]) {
-  if constexpr (N * sizeof(C) < 16) {  // less than a chunk a row
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (row0 + lane < p.m && col + i < p.n)
-        ((C*)p.c)[(int64_t)(row0 + lane) * p.ld_c + col + i] = (C)acc[i];
-    return;
-  } else {
   constexpr int kPiece = 128 / sizeof(C) < N ? 128 / sizeof(C) : N;  // columns
   constexpr int kChunks = kPiece * sizeof(C) / 16, kPer = 16 / sizeof(C);
   const bool vec = p.vec_c != 0;
@@ -155,7 +148,6 @@ __device__ __forceinline__ void store_rows(const BlocksParams& p, uint8_t* piece
       }
     }
     __syncwarp();
-  }
   }
 }
 
@@ -478,14 +470,14 @@ cudaError_t run(CMat a, CMat b, int b_lines, const BlocksParams& p, int k, cudaS
                       : launch_config<CG, BN, 128, ROWS, SPLIT>(maps, p, st);
 }
 
-// Tiles of 64 columns, each shared out over `split` CTAs.
+// Tiles of 128 columns, each shared out over `split` CTAs.
 template <int ROWS>
 cudaError_t run_split(int split, CMat a, CMat b, int b_lines, const BlocksParams& p, int k,
                       cudaStream_t st) {
-  if (split >= 8) return run<1, 64, ROWS, 8>(a, b, b_lines, p, k, st);
-  if (split >= 4) return run<1, 64, ROWS, 4>(a, b, b_lines, p, k, st);
-  if (split >= 2) return run<1, 64, ROWS, 2>(a, b, b_lines, p, k, st);
-  return run<1, 64, ROWS, 1>(a, b, b_lines, p, k, st);
+  if (split >= 8) return run<1, 128, ROWS, 8>(a, b, b_lines, p, k, st);
+  if (split >= 4) return run<1, 128, ROWS, 4>(a, b, b_lines, p, k, st);
+  if (split >= 2) return run<1, 128, ROWS, 2>(a, b, b_lines, p, k, st);
+  return run<1, 128, ROWS, 1>(a, b, b_lines, p, k, st);
 }
 
 bool vector_rows(const void* p, int64_t ld_bytes) {
@@ -509,17 +501,19 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
   p.vec_c = vector_rows(c.p, c.ld * (c_type == FWT_F32 ? 4 : 2));
   p.vec_as = vector_rows(a_scale.p, a_scale.ld * 4);
   p.vec_bs = vector_rows(b_scale.p, b_scale.ld * 4);
-  // Pairs of CTAs on 256 x 256 tiles where these fill the device, else smaller tiles.
-  const int sms = multiprocessors();
-  if ((int64_t)((m + 255) / 256) * ((n + 255) / 256) * 2 >= sms)
-    return run<2, 256>(a, b, b_lines, p, k, st);
-  if ((int64_t)((m + 127) / 128) * ((n + 127) / 128) * 2 > sms)
-    return run<1, 128>(a, b, b_lines, p, k, st);
-  const int64_t tiles = (int64_t)((m + 127) / 128) * ((n + 63) / 64);
-  // (clusters of four and eight do not fill every multiprocessor of a graphics cluster)
-  int split = (int)std::min<int64_t>(sms / std::max<int64_t>(tiles, 1), p.blocks / 2);
-  split = split >= 8 ? 8 : split >= 4 ? 4 : split;
-  if (split >= 4 && tiles * split > sms * 7 / 8) split /= 2;
+  // Pairs of CTAs on 256 x 256 tiles, or single ones on 128 x 128 whose blocks a cluster shares
+  // out where the tiles leave multiprocessors idle.  A block costs a CTA about the same either
+  // way (it moves 32 KB), so what counts is the blocks that one CTA after the other goes
+  // through: waves of tiles times blocks a tile.  (Two blocks a CTA at least; clusters of four
+  // and eight do not fill every multiprocessor of a graphics cluster.)
+  const int64_t sms = multiprocessors();
+  const auto tiles = [&](int64_t size) { return ((m + size - 1) / size) * ((n + size - 1) / size); };
+  const int64_t wide = (tiles(256) + sms / 2 - 1) / (sms / 2) * p.blocks, small = tiles(128);
+  int split = 1;
+  while (split < 8 && 2 * split * small <= (split >= 2 ? sms * 7 / 8 : sms) && 4 * split <= p.blocks)
+    split *= 2;
+  const int64_t rest = (small * split + sms - 1) / sms * ((p.blocks + split - 1) / split);
+  if (wide < rest) return run<2, 256>(a, b, b_lines, p, k, st);
   return m <= 64 ? run_split<64>(split, a, b, b_lines, p, k, st)
                  : run_split<128>(split, a, b, b_lines, p, k, st);
 }
