@@ -318,8 +318,8 @@ int fwt_quantize_blocks(const void* x, int x_type, int64_t rows, int64_t cols, i
  * scale per block of 128 along k by b_lines (1 or 128) lines.  C: m x n of c_type.  Both
  * operands run along the contraction, as fwt_quantize_blocks writes them (for the
  * gradient products, along either axis).  Products and sums are fp32, in an order that
- * depends on the sizes alone, with one rounding to c_type.  m or n = 0: nothing is
- * written; k = 0: C is zero.
+ * depends on the sizes and the device alone, with one rounding to c_type; the product of two
+ * scales is rounded to fp32 first.  m or n = 0: nothing is written; k = 0: C is zero.
  */
 int fwt_matmul_blocks(const void* a, int64_t ld_a, const float* a_scale, int64_t ld_a_scale,
                       const void* b, int64_t ld_b, const float* b_scale, int64_t ld_b_scale,
@@ -343,8 +343,9 @@ int fwt_gated(const void* x, int64_t ld_x, const void* w_gate, int64_t ld_gate, 
  *     dg = grad * u * act'(g),  du = grad * act(g)
  *     dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.
  *
- * dg and du are rounded to `type` once, in the workspace, as the operands of the second
- * products; sums are fp32.  dx (m x d) may be NULL, and dw_gate and dw_up (f x d) both
+ * Sums are fp32.  For m > 8, dg and du are rounded to `type` once, in the workspace, as the
+ * operands of the second products (16-bit tensor-core operands; that rounding is as large as
+ * the outputs' own); for m <= 8 they stay in fp32.  dx (m x d) may be NULL, and dw_gate and dw_up (f x d) both
  * NULL, where they are not wanted.  Outputs are written, not added to.  workspace: DEVICE
  * memory, 16-byte aligned, of at least fwt_gated_backward_workspace_bytes(m, f) bytes.
  */
