@@ -171,6 +171,7 @@ MATMUL = [  # m, n, k, lines, out
     (300, 513, 2049, 128, "bf16"), (1024, 1024, 1024, 128, "f32"), (1500, 3000, 640, 128, "bf16"),
     (3, 50000, 160, 128, "bf16"), (4000, 5, 200, 1, "f32"), (640, 384, 1, 128, "f32"),
     (2307, 2500, 400, 128, "bf16"), (2500, 2307, 261, 1, "f32"), (2049, 2560, 640, 128, "f16"),
+    (150, 2500, 900, 128, "bf16"), (129, 1290, 1700, 1, "f32"), (50, 2600, 1600, 128, "f16"),
 ]
 
 
@@ -323,7 +324,7 @@ BACKWARD = [
     (517, 333, 401, "f16", "gelu"), (600, 1024, 900, "bf16", "silu"), (1025, 128, 260, "bf16", "relu"),
     (1, 1500, 300, "f16", "silu"), (2, 2048, 70, "bf16", "relu"), (5, 1001, 900, "bf16", "gelu"),
     (8, 260, 2057, "f16", "silu"), (9, 700, 520, "f16", "relu"),
-    (40, 300, 1100, "bf16", "gelu"),
+    (40, 300, 1100, "bf16", "gelu"), (300, 1700, 400, "f16", "silu"), (250, 1200, 1000, "bf16", "silu"),
     (1500, 1303, 2105, "bf16", "silu"), (2307, 2500, 300, "f16", "gelu"),
 ]
 

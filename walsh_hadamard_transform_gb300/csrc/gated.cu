@@ -369,11 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           cluster_sync();
           met = true;
-          constexpr int kShare = kHalf / SPLIT, W = kShare < 32 ? kShare : 32;
-          const int from = half * kHalf + (int)cluster_rank() * kShare;
+          // whole 16-byte chunks of the warp's columns, the last CTAs' shares smaller or empty
+          constexpr int kShare = (kHalf / 8 + SPLIT - 1) / SPLIT * 8;
+          constexpr int W = kShare % 32 == 0 ? 32 : kShare % 16 == 0 ? 16 : 8;
+          const int from = (int)cluster_rank() * kShare;
           const uint32_t there = smem_u32(mine);
 #pragma unroll 1
-          for (int c = from; c < from + kShare; c += W) {
+          for (int at = from; at < min(from + kShare, kHalf); at += W) {
+            const int c = half * kHalf + at;
             uint32_t v[W], u[W];
             auto gather = [&](int c0, uint32_t(&x)[W]) {
               float sum[W];
@@ -441,12 +444,11 @@ Cut choose_cut(int64_t m, int64_t n, int outputs, int64_t stages, int most_split
   const int64_t sms = multiprocessors();
   const auto tiles = [&](int64_t size) { return ((m + size - 1) / size) * ((n + size - 1) / size) * outputs; };
   const int64_t wide = (tiles(256) + sms / 2 - 1) / (sms / 2) * stages, small = tiles(128);
-  // (four stages a CTA at least; clusters of four and eight do not fill every multiprocessor
+  // (four stages a CTA at least; clusters of three and more do not fill every multiprocessor
   // of a graphics cluster)
   int split = 1;
-  while (2 * split <= most_split && 2 * split * small <= (split >= 2 ? sms * 7 / 8 : sms) &&
-         2 * split * 4 <= stages)
-    split *= 2;
+  for (int s : {2, 3, 4, 6, 8})
+    if (s <= most_split && s * small <= (s > 2 ? sms * 7 / 8 : sms) && s * 4 <= stages) split = s;
   const int64_t rest = (small * split + sms - 1) / sms * ((stages + split - 1) / split);
   return wide < rest ? Cut{true, 1} : Cut{false, split};
 }
@@ -458,9 +460,12 @@ cudaError_t launch_mode(Cut cut, const GemmMaps& maps, GemmParams p, cudaStream_
   p.tiles_m = (p.m + rows - 1) / rows;
   p.tiles_n = (p.n + cols - 1) / cols;
   if (cut.wide) return launch_config<T, MODE, 2, 256, 1>(maps, p, st);
-  if constexpr (halves == 1)
+  if constexpr (halves == 1) {
     if (cut.split == 8) return launch_config<T, MODE, 1, 128, 8>(maps, p, st);
+    if (cut.split == 6) return launch_config<T, MODE, 1, 128, 6>(maps, p, st);
+  }
   if (cut.split == 4) return launch_config<T, MODE, 1, 128, 4>(maps, p, st);
+  if (cut.split == 3) return launch_config<T, MODE, 1, 128, 3>(maps, p, st);
   if (cut.split == 2) return launch_config<T, MODE, 1, 128, 2>(maps, p, st);
   return launch_config<T, MODE, 1, 128, 1>(maps, p, st);
 }

@@ -411,24 +411,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // Every CTA of the cluster leaves its sums in its own ring, which its products are
           // done with, and adds up and stores a share of the columns, in the order of ranks.
-          constexpr int kShare = kHalf / SPLIT;
+          // whole eights of the warp's columns, the last CTAs' shares smaller or empty
+          constexpr int kShare = (kHalf / 8 + SPLIT - 1) / SPLIT * 8;
+          constexpr int W = kShare % 32 == 0 ? 32 : kShare % 16 == 0 ? 16 : 8;
           float* mine = (float*)(dynamic + (ring - smem_u32(dynamic))) + (warp - 4) * kHalf * 32 + lane;
 #pragma unroll
           for (int i = 0; i < kHalf; ++i) mine[i * 32] = acc[i];
           cluster_sync();
           met = true;
           const int from = (int)cluster_rank() * kShare;
-          float sum[kShare];
+#pragma unroll 1
+          for (int c = from; c < min(from + kShare, kHalf); c += W) {
+            float sum[W];
 #pragma unroll
-          for (int i = 0; i < kShare; ++i) sum[i] = 0.f;
-          const uint32_t there = smem_u32(mine) + from * 128;
+            for (int i = 0; i < W; ++i) sum[i] = 0.f;
+            const uint32_t there = smem_u32(mine) + c * 128;
 #pragma unroll
-          for (int r = 0; r < SPLIT; ++r) {
-            const uint32_t peer = map_to_rank(there, r);
+            for (int r = 0; r < SPLIT; ++r) {
+              const uint32_t peer = map_to_rank(there, r);
 #pragma unroll
-            for (int i = 0; i < kShare; ++i) sum[i] += load_cluster(peer + i * 128);
+              for (int i = 0; i < W; ++i) sum[i] += load_cluster(peer + i * 128);
+            }
+            store(piece, row0, col + c, sum);
           }
-          store(piece, row0, col + from, sum);
         }
       }
     }();
@@ -474,9 +479,11 @@ cudaError_t run(CMat a, CMat b, int b_lines, const BlocksParams& p, int k, cudaS
 template <int ROWS>
 cudaError_t run_split(int split, CMat a, CMat b, int b_lines, const BlocksParams& p, int k,
                       cudaStream_t st) {
-  if (split >= 8) return run<1, 128, ROWS, 8>(a, b, b_lines, p, k, st);
-  if (split >= 4) return run<1, 128, ROWS, 4>(a, b, b_lines, p, k, st);
-  if (split >= 2) return run<1, 128, ROWS, 2>(a, b, b_lines, p, k, st);
+  if (split == 8) return run<1, 128, ROWS, 8>(a, b, b_lines, p, k, st);
+  if (split == 6) return run<1, 128, ROWS, 6>(a, b, b_lines, p, k, st);
+  if (split == 4) return run<1, 128, ROWS, 4>(a, b, b_lines, p, k, st);
+  if (split == 3) return run<1, 128, ROWS, 3>(a, b, b_lines, p, k, st);
+  if (split == 2) return run<1, 128, ROWS, 2>(a, b, b_lines, p, k, st);
   return run<1, 128, ROWS, 1>(a, b, b_lines, p, k, st);
 }
 
@@ -504,14 +511,14 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
   // Pairs of CTAs on 256 x 256 tiles, or single ones on 128 x 128 whose blocks a cluster shares
   // out where the tiles leave multiprocessors idle.  A block costs a CTA about the same either
   // way (it moves 32 KB), so what counts is the blocks that one CTA after the other goes
-  // through: waves of tiles times blocks a tile.  (Two blocks a CTA at least; clusters of four
-  // and eight do not fill every multiprocessor of a graphics cluster.)
+  // through: waves of tiles times blocks a tile.  (Two blocks a CTA at least; clusters of three
+  // and more do not fill every multiprocessor of a graphics cluster.)
   const int64_t sms = multiprocessors();
   const auto tiles = [&](int64_t size) { return ((m + size - 1) / size) * ((n + size - 1) / size); };
   const int64_t wide = (tiles(256) + sms / 2 - 1) / (sms / 2) * p.blocks, small = tiles(128);
   int split = 1;
-  while (split < 8 && 2 * split * small <= (split >= 2 ? sms * 7 / 8 : sms) && 4 * split <= p.blocks)
-    split *= 2;
+  for (int s : {2, 3, 4, 6, 8})
+    if (s * small <= (s > 2 ? sms * 7 / 8 : sms) && s * 2 <= p.blocks) split = s;
   const int64_t rest = (small * split + sms - 1) / sms * ((p.blocks + split - 1) / split);
   if (wide < rest) return run<2, 256>(a, b, b_lines, p, k, st);
   return m <= 64 ? run_split<64>(split, a, b, b_lines, p, k, st)
