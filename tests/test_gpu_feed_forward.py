@@ -172,6 +172,8 @@ MATMUL = [  # m, n, k, lines, out
     (3, 50000, 160, 128, "bf16"), (4000, 5, 200, 1, "f32"), (640, 384, 1, 128, "f32"),
     (2307, 2500, 400, 128, "bf16"), (2500, 2307, 261, 1, "f32"), (2049, 2560, 640, 128, "f16"),
     (150, 2500, 900, 128, "bf16"), (129, 1290, 1700, 1, "f32"), (50, 2600, 1600, 128, "f16"),
+    (200, 3800, 2500, 1, "bf16"), (300, 1700, 2600, 128, "f32"), (130, 1900, 2000, 128, "f16"),
+    (40, 7000, 2600, 128, "bf16"),
 ]
 
 
@@ -246,6 +248,7 @@ GATED = [  # m, d, f, dtype, act
     (40, 640, 384, "bf16", "silu"), (64, 1000, 1000, "f16", "silu"), (128, 64, 128, "bf16", "gelu"),
     (129, 1001, 531, "f16", "gelu"), (333, 200, 1031, "bf16", "silu"), (700, 513, 900, "bf16", "relu"),
     (1030, 1024, 1024, "f16", "silu"), (3, 1, 5, "bf16", "silu"), (130, 3, 70, "f16", "silu"),
+    (100, 1500, 2000, "bf16", "gelu"), (200, 1800, 1500, "f16", "silu"), (129, 1600, 1200, "bf16", "silu"),
     (1500, 200, 2105, "bf16", "gelu"), (1281, 513, 3000, "f16", "silu"),
 ]
 
@@ -325,6 +328,8 @@ BACKWARD = [
     (1, 1500, 300, "f16", "silu"), (2, 2048, 70, "bf16", "relu"), (5, 1001, 900, "bf16", "gelu"),
     (8, 260, 2057, "f16", "silu"), (9, 700, 520, "f16", "relu"),
     (40, 300, 1100, "bf16", "gelu"), (300, 1700, 400, "f16", "silu"), (250, 1200, 1000, "bf16", "silu"),
+    (256, 1900, 800, "bf16", "silu"), (500, 2000, 700, "f16", "gelu"), (2000, 300, 500, "bf16", "silu"),
+    (1500, 500, 700, "f16", "silu"), (1400, 640, 500, "bf16", "gelu"), (1800, 128, 128, "bf16", "silu"),
     (1500, 1303, 2105, "bf16", "silu"), (2307, 2500, 300, "f16", "gelu"),
 ]
 

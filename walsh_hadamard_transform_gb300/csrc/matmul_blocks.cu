@@ -511,16 +511,18 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
   // Pairs of CTAs on 256 x 256 tiles, or single ones on 128 x 128 whose blocks a cluster shares
   // out where the tiles leave multiprocessors idle.  A block costs a CTA about the same either
   // way (it moves 32 KB), so what counts is the blocks that one CTA after the other goes
-  // through: waves of tiles times blocks a tile.  (Two blocks a CTA at least; clusters of three
-  // and more do not fill every multiprocessor of a graphics cluster.)
+  // through, waves of tiles times blocks a tile; sharing out costs about as much as eight of
+  // them (measured: 1.7 us and more, at 0.25 us a block).
   const int64_t sms = multiprocessors();
   const auto tiles = [&](int64_t size) { return ((m + size - 1) / size) * ((n + size - 1) / size); };
   const int64_t wide = (tiles(256) + sms / 2 - 1) / (sms / 2) * p.blocks, small = tiles(128);
+  int64_t least = (small + sms - 1) / sms * p.blocks;
   int split = 1;
+  // (clusters of three and more do not fill every multiprocessor of a graphics cluster)
   for (int s : {2, 3, 4, 6, 8})
-    if (s * small <= (s > 2 ? sms * 7 / 8 : sms) && s * 2 <= p.blocks) split = s;
-  const int64_t rest = (small * split + sms - 1) / sms * ((p.blocks + split - 1) / split);
-  if (wide < rest) return run<2, 256>(a, b, b_lines, p, k, st);
+    if (s * small <= (s > 2 ? sms * 7 / 8 : sms) && (p.blocks + s - 1) / s + 8 < least)
+      split = s, least = (p.blocks + s - 1) / s + 8;
+  if (wide < least) return run<2, 256>(a, b, b_lines, p, k, st);
   return m <= 64 ? run_split<64>(split, a, b, b_lines, p, k, st)
                  : run_split<128>(split, a, b, b_lines, p, k, st);
 }
