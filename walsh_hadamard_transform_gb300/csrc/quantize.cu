@@ -15,7 +15,11 @@
 // (bits 5, 6), the lanes t = 0..3 of a quad being bits 3 and 4, for the lines g = lane / 4
 // and g + 8.  So inputs are 16-byte loads, codes 8-byte stores, and only the maximum of a
 // block crosses lanes (two shuffles a line, where butterflies across lanes would take four
-// shuffles an element and be bound by them).  Bound: HBM.
+// shuffles an element and be bound by them).
+//
+// Bound: HBM by its bytes, issue and the latency of dependent instructions as it stands (52% of
+// the issue slots, 12 to 16 warps an SM): 8192 x 8192 bf16 in 41.1 us along the columns and 37.7
+// down the rows, 4.9 and 5.3 TB/s; one line of 8192 2.4 us, the launch.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -2,11 +2,11 @@
 // kernels for single tokens and small batches share.
 //
 // With few tokens a product is bound by reading the weights once.  A warp reads 16 weight
-// lines straight from global memory into the fragments of 16 x 8 matrix products, 16 bytes a
-// thread: which elements of the contraction meet in which slot of a product is free as long
-// as both operands agree, so thread t of a quad takes 16 consecutive bytes of a line at
-// 64 c + 16 t, and the tokens' fragment the same bytes of its line.  The warps of a CTA split
-// the contraction and add their sums up in shared memory, in a fixed order.
+// lines into the fragments of 16 x 8 matrix products, 16 bytes a thread, without a tile that
+// the CTA would share: which elements of the contraction meet in which slot of a product is
+// free as long as both operands agree, so thread t of a quad takes 16 consecutive bytes of a
+// line at 64 c + 16 t, and the tokens' fragment the same bytes of its line.  The warps of a
+// CTA split the contraction and add their sums up in shared memory, in a fixed order.
 #pragma once
 
 #include <cstdint>
