@@ -378,8 +378,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; i += 4) {
                 float4 f = make_float4(s[u], s[u], s[u], s[u]);
                 if constexpr (LINES == 1) {
-                  f = *(const float4*)&row[u * (C::kScales / 4) + 128 + half * kHalf + c + i];
-                  f.x *= s[u], f.y *= s[u], f.z *= s[u], f.w *= s[u];
+                  // two scales of columns at a time by the row's
+                  const ulonglong2 pair = *(const ulonglong2*)&row[u * (C::kScales / 4) + 128 + half * kHalf + c + i];
+                  unsigned long long ss, lo, hi;
+                  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s[u]));
+                  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(lo) : "l"(pair.x), "l"(ss));
+                  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(hi) : "l"(pair.y), "l"(ss));
+                  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(lo));
+                  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.z), "=f"(f.w) : "l"(hi));
                 }
                 float* sum = &acc[c + i];
                 sum[0] = fmaf(__uint_as_float(x[i]), f.x, sum[0]);
