@@ -118,7 +118,7 @@ struct Block {
         for (int s = 0; s < 2; ++s) {
           const int l = line(strip, g, s);
           const T* from = x + (int64_t)l * p.ld_x + pos;
-          if (p.vec && l < p.nl && pos + 8 <= p.length) {
+          if (sizeof(T) == 4 && p.vec && l < p.nl && pos + 8 <= p.length) {  // (16 bits: staged)
 #pragma unroll
             for (int i = 0; i < kWords; i += 4) {
               const uint4 v = __ldg((const uint4*)from + i / 4);

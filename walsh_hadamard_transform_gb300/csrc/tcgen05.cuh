@@ -18,8 +18,7 @@
 namespace fwt {
 namespace ff {
 
-constexpr uint32_t kSwizzleRow = 128;   // bytes
-constexpr uint32_t kSwizzleAtom = 1024; // bytes, 8 rows
+constexpr uint32_t kSwizzleAtom = 1024;  // bytes, 8 rows
 
 // True in one thread of the (whole) warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
@@ -130,17 +129,8 @@ __device__ __forceinline__ void tmem_wait_loads() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 16 or 32 consecutive columns of the warp's 32 lanes, one lane a thread.  The values are
-// there after tmem_wait_loads().
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
-      " %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
-      : "r"(addr));
-}
+// 32 consecutive columns of the warp's 32 lanes, one lane a thread.  The values are there
+// after tmem_wait_loads().
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
