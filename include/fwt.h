@@ -297,7 +297,7 @@ enum fwt_activation {
  * is extended with zeros to L, a multiple of 2^r, for that.  Each block of 128 elements
  * along the axis by `lines` (1 or 128) lines across it gets
  *
- *     s = max(max |y| / 448, 2^-126),   q = e4m3(y * (1 / s))  (to nearest even).
+ *     s = max(max |y| / 448, 2^-126),   q = e4m3(y / s)  (to nearest even).
  *
  * q: lines-major, nl x L bytes (nl = rows for axis 1; cols for axis 0, that is
  * transposed), line i at q + i * ld_q, ld_q a multiple of 16, at least L.  scale:

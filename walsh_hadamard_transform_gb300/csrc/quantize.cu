@@ -424,8 +424,9 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float scale = fmaxf(__fdiv_rn(top[s] * p.norm, 448.f), 0x1p-126f);
-      if (!(top[s] < INFINITY)) scale = __uint_as_float(0x7fffffffu);
-      const float factor = __fdiv_rn(1.f, scale) * p.norm;
+      // norm / scale; above the least scale the norm cancels, which saves two roundings
+      float factor = scale > 0x1p-126f ? __fdiv_rn(448.f, top[s]) : p.norm * 0x1p126f;
+      if (!(top[s] < INFINITY)) scale = factor = __uint_as_float(0x7fffffffu);
       const int l = lines[s];
       if (LINES == 1 ? t == 0 && l < p.nl : threadIdx.x == 0 && s == 0)
         p.scale[(int64_t)(LINES == 1 ? l : l / 128) * p.ld_scale + block] = scale;
