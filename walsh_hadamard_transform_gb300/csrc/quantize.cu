@@ -18,8 +18,8 @@
 // shuffles an element and be bound by them).
 //
 // Bound: HBM by its bytes, issue and the latency of dependent instructions as it stands (52% of
-// the issue slots, 12 to 16 warps an SM): 8192 x 8192 bf16 in 41.1 us along the columns and 37.7
-// down the rows, 4.9 and 5.3 TB/s; one line of 8192 2.4 us, the launch.
+// the issue slots, 12 to 16 warps an SM): 8192 x 8192 bf16 in 39.4 us along the columns and 36.7
+// down the rows, 5.1 and 5.5 TB/s; one line of 8192 2.1 us, the launch.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -49,6 +49,7 @@ struct QuantizeParams {
   int blocks, strips;    // blocks of 128 along the axis, strips of 16 lines
   int r;
   float norm;  // 2^(-r/2)
+  float norm_448;  // 2^(-r/2) / 448
   int rounds;  // blocks a warp goes through
   int vec;     // rows of x start on 16-byte boundaries (axis 0: on two elements')
   int vec16;   // on 16-byte boundaries, whichever axis
@@ -216,8 +217,19 @@ __device__ __forceinline__ void copy16(uint32_t to, const QuantizeParams& p, int
                "l"((const uint8_t*)p.x + (valid ? element * 2 : 0)), "r"(valid)
                : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void stage_rows(const QuantizeParams& p, uint32_t to, int strip, int block) {
   const int lane = threadIdx.x & 31, chunk = lane & 15, col = block * 128 + 8 * chunk;
+  if (block * 128 + 128 <= p.length && strip * 16 + 16 <= p.nl) {  // all of it is there
+    const uint8_t* from = (const uint8_t*)p.x + ((strip * 16 + (lane >> 4)) * p.ld_x + col) * 2;
+    const int64_t step = p.ld_x * 4;
+    to += row_at(lane >> 4, chunk);
+#pragma unroll
+    for (int i = 0; i < 8; ++i, from += step) copy16(to + i * 512, from);
+    return;
+  }
   const int bytes = min(16, max(0, (p.length - col) * 2));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -236,6 +248,14 @@ template <int W>
 __device__ __forceinline__ void stage_columns(const QuantizeParams& p, uint32_t to, int line0, int block) {
   constexpr int kChunks = 2 * W;
   const int chunk = threadIdx.x % kChunks, line = line0 + 8 * chunk;
+  if (block * 128 + 128 <= p.length && line0 + 16 * W <= p.nl) {
+    const int pos = threadIdx.x / kChunks;
+    const uint8_t* from = (const uint8_t*)p.x + ((int64_t)(block * 128 + pos) * p.ld_x + line) * 2;
+    const int64_t step = p.ld_x * 32;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, from += step) copy16(to + column_at<W>(pos + 16 * i, chunk), from);
+    return;
+  }
   const int bytes = min(16, max(0, (p.nl - line) * 2));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -330,17 +350,20 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
       else __syncthreads();
     }
 #pragma unroll
-    for (int grp = 0; grp < 4; ++grp)
+    for (int grp = 0; grp < 4; ++grp) {
+      uint4 lo, hi;
+      if constexpr (STAGED && AXIS == 1) {
+        const uint8_t* from = staged + (buffers - smem_u32(staged)) + now;
+        lo = *(const uint4*)(from + row_at(g, 4 * grp + t));
+        hi = *(const uint4*)(from + row_at(g + 8, 4 * grp + t));
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int k = 0; k < Input<T>::kPieces; ++k) {
           uint32_t a[4];
           if constexpr (STAGED && AXIS == 1) {
-            const uint8_t* from = staged + (buffers - smem_u32(staged)) + now + 8 * h;
-            const uint2 lo = *(const uint2*)(from + row_at(g, 4 * grp + t));
-            const uint2 hi = *(const uint2*)(from + row_at(g + 8, 4 * grp + t));
-            a[0] = lo.x, a[1] = hi.x, a[2] = lo.y, a[3] = hi.y;
+            a[0] = h ? lo.z : lo.x, a[1] = h ? hi.z : hi.x, a[2] = h ? lo.w : lo.y, a[3] = h ? hi.w : hi.y;
           } else if constexpr (STAGED) {
             // lane -> a row of one of four 8 x 8 matrices: elements 0, 1 or 2, 3 (lanes 16 on)
             // of each thread's four, lines 0..7 or 8..15 (odd eights of lanes)
@@ -360,6 +383,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
           }
         }
       }
+    }
     // the next round's copies overwrite the stage that was read the longest ago: this one
     if constexpr (STAGED && AXIS == 1) __syncwarp();
     else if constexpr (STAGED) __syncthreads();
@@ -423,9 +447,13 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
 
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      float scale = fmaxf(__fdiv_rn(top[s] * p.norm, 448.f), 0x1p-126f);
-      // norm / scale; above the least scale the norm cancels, which saves two roundings
-      float factor = scale > 0x1p-126f ? __fdiv_rn(448.f, top[s]) : p.norm * 0x1p126f;
+      const bool whole = block * 128 + 128 <= p.full;
+      // s = top norm / 448, and norm / s: above the least scale the norm cancels.  448 / top comes
+      // from the reciprocal, corrected once by its remainder.
+      float scale = fmaxf(top[s] * p.norm_448, 0x1p-126f);
+      const float reciprocal = __frcp_rn(top[s]), rough = 448.f * reciprocal;
+      float factor = fmaf(fmaf(-rough, top[s], 448.f), reciprocal, rough);
+      if (scale <= 0x1p-126f) factor = p.norm * 0x1p126f;
       if (!(top[s] < INFINITY)) scale = factor = __uint_as_float(0x7fffffffu);
       const int l = lines[s];
       if (LINES == 1 ? t == 0 && l < p.nl : threadIdx.x == 0 && s == 0)
@@ -440,7 +468,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
           code.y = codes4(y[grp][1][0][2 * s] * factor, y[grp][1][0][2 * s + 1] * factor,
                           y[grp][1][1][2 * s] * factor, y[grp][1][1][2 * s + 1] * factor);
           const int at = block * 128 + 32 * grp + 8 * t;
-          if (at + 8 <= p.full) {
+          if (whole || at + 8 <= p.full) {
             *(uint2*)(q + at) = code;
           } else {
             for (int j = 0; j < 8 && at + j < p.full; ++j)
@@ -504,6 +532,7 @@ cudaError_t launch_quantize(CMat x, int x_type, int rows, int cols, int rot_bits
   p.strips = (p.nl + 15) / 16;
   p.r = rot_bits;
   p.norm = kNorm[rot_bits];
+  p.norm_448 = (float)((double)kNorm[rot_bits] / 448.0);
   const int size = x_type == FWT_F32 ? 4 : 2;
   const int unit = axis ? 16 : 2 * size;
   p.vec = (uintptr_t)x.p % (unsigned)unit == 0 && (x.ld * size) % unit == 0;
