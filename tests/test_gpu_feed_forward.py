@@ -144,6 +144,21 @@ def test_quantize_offsets_beyond_32_bits():
     check_quantized(x, q, s, 7, 1, 1)
 
 
+@pytest.mark.parametrize("axis,lines", [(1, 1), (1, 128), (0, 1), (0, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_large_calls_equal_their_parts(axis, lines, dtype):
+    """Large calls go through several blocks a warp, small ones through one: the same bits."""
+    rows, cols = (4099, 10250) if axis else (10250, 4099)
+    x = torch.randn(rows, cols + -cols % 8, device="cuda").to(REALS[dtype])[:, :cols]
+    q, s = fwt.quantize_blocks(x, rotate=5, axis=axis, lines=lines)
+    across = q.shape[0]
+    for start, size in ((0, 256), (1792, 128), (4096, across - 4096)):
+        part = x[start:start + size] if axis else x[:, start:start + size]
+        qp, sp = fwt.quantize_blocks(part, rotate=5, axis=axis, lines=lines)
+        assert torch.equal(qp.view(torch.uint8), q[start:start + size].view(torch.uint8))
+        assert torch.equal(sp, s[start // lines:start // lines + sp.shape[0]])
+
+
 # ---- matmul_blocks -----------------------------------------------------------------
 
 def operand(rows, k, lines, seed, extra=0):
@@ -173,7 +188,7 @@ MATMUL = [  # m, n, k, lines, out
     (2307, 2500, 400, 128, "bf16"), (2500, 2307, 261, 1, "f32"), (2049, 2560, 640, 128, "f16"),
     (150, 2500, 900, 128, "bf16"), (129, 1290, 1700, 1, "f32"), (50, 2600, 1600, 128, "f16"),
     (200, 3800, 2500, 1, "bf16"), (300, 1700, 2600, 128, "f32"), (130, 1900, 2000, 128, "f16"),
-    (40, 7000, 2600, 128, "bf16"),
+    (40, 7000, 2600, 128, "bf16"), (300, 9800, 200, 128, "bf16"), (300, 9800, 200, 1, "f16"),
 ]
 
 
@@ -249,6 +264,7 @@ GATED = [  # m, d, f, dtype, act
     (129, 1001, 531, "f16", "gelu"), (333, 200, 1031, "bf16", "silu"), (700, 513, 900, "bf16", "relu"),
     (1030, 1024, 1024, "f16", "silu"), (3, 1, 5, "bf16", "silu"), (130, 3, 70, "f16", "silu"),
     (100, 1500, 2000, "bf16", "gelu"), (200, 1800, 1500, "f16", "silu"), (129, 1600, 1200, "bf16", "silu"),
+    (300, 72, 4900, "bf16", "silu"),
     (1500, 200, 2105, "bf16", "gelu"), (1281, 513, 3000, "f16", "silu"),
 ]
 
@@ -329,7 +345,7 @@ BACKWARD = [
     (8, 260, 2057, "f16", "silu"), (9, 700, 520, "f16", "relu"),
     (40, 300, 1100, "bf16", "gelu"), (300, 1700, 400, "f16", "silu"), (250, 1200, 1000, "bf16", "silu"),
     (256, 1900, 800, "bf16", "silu"), (500, 2000, 700, "f16", "gelu"), (2000, 300, 500, "bf16", "silu"),
-    (1500, 500, 700, "f16", "silu"), (1400, 640, 500, "bf16", "gelu"), (1800, 128, 128, "bf16", "silu"),
+    (1500, 500, 700, "f16", "silu"), (1400, 640, 500, "bf16", "gelu"), (1800, 128, 128, "bf16", "silu"), (300, 72, 4900, "f16", "silu"), (70, 4900, 300, "bf16", "gelu"),
     (1500, 1303, 2105, "bf16", "silu"), (2307, 2500, 300, "f16", "gelu"),
 ]
 

@@ -56,12 +56,13 @@ def _matrix(t, name, device, dtype=None, shape=None):
 
 
 def _empty(rows, cols, dtype, device, multiple):
-    """A new rows x cols tensor, its rows a multiple of ``multiple`` elements apart."""
+    """A new rows x cols tensor, its rows a multiple of ``multiple`` elements apart, and that
+    distance."""
     over = cols % multiple
     if over:
-        return _torch.empty_strided((rows, cols), (cols + multiple - over, 1), dtype=dtype,
-                                    device=device)
-    return _torch.empty((rows, cols), dtype=dtype, device=device)
+        ld = cols + multiple - over
+        return _torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device), ld
+    return _torch.empty((rows, cols), dtype=dtype, device=device), cols
 
 
 def _run(device, stream, entry, *args):
@@ -103,9 +104,8 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     length += -length % (1 << rotate)
     shape = (-(-across // lines), -(-length // 128))
     if out is None:
-        q = _empty(across, length, _E4M3, x.device, 16)
-        scale = _empty(*shape, _F32, x.device, 4)
-        ld_q, ld_s = q.stride(0), scale.stride(0)
+        q, ld_q = _empty(across, length, _E4M3, x.device, 16)
+        scale, ld_s = _empty(*shape, _F32, x.device, 4)
     else:
         q, scale = out
         ld_q = _matrix(q, "codes", device, _E4M3, (across, length))
@@ -142,8 +142,7 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
         kind = _REALS.get(out_dtype)
         if kind is None:
             raise TypeError(f"unsupported dtype {out_dtype}: use float32, bfloat16 or float16")
-        out = _empty(m, n, out_dtype, a.device, 4 if kind == 0 else 8)
-        ld_c = out.stride(0)
+        out, ld_c = _empty(m, n, out_dtype, a.device, 4 if kind == 0 else 8)
     else:
         kind = _REALS.get(out.dtype)
         if kind is None or (out_dtype is not None and out.dtype != out_dtype):
@@ -184,8 +183,7 @@ def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
     dtype, kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up,
                                                                            activation)
     if out is None:
-        out = _empty(m, f, dtype, x.device, 8)
-        ld_h = out.stride(0)
+        out, ld_h = _empty(m, f, dtype, x.device, 8)
     else:
         ld_h = _matrix(out, "out", device, dtype, (m, f))
     st = _run(device, stream, _lib.fwt_gated, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g,
@@ -218,16 +216,14 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
             raise ValueError("out must hold the gradients named in want, and no other")
     if want_x:
         if dx is None:
-            dx = _empty(m, d, dtype, x.device, 8)
-            ld_dx = dx.stride(0)
+            dx, ld_dx = _empty(m, d, dtype, x.device, 8)
         else:
             ld_dx = _matrix(dx, "dx", device, dtype, (m, d))
         p_dx = dx.data_ptr()
     if want_w:
         if dw_gate is None:
-            dw_gate = _empty(f, d, dtype, x.device, 8)
-            dw_up = _empty(f, d, dtype, x.device, 8)
-            ld_dg = ld_du = dw_gate.stride(0)
+            dw_gate, ld_dg = _empty(f, d, dtype, x.device, 8)
+            dw_up, ld_du = _empty(f, d, dtype, x.device, 8)
         else:
             ld_dg = _matrix(dw_gate, "dw_gate", device, dtype, (f, d))
             ld_du = _matrix(dw_up, "dw_up", device, dtype, (f, d))
