@@ -78,16 +78,19 @@ struct Tile {
   int m0, n0, output;
 };
 
-// Tiles in groups of 8 rows of tiles, so that those in flight together share operands in L2.
+// Tiles in groups of 16 rows of tiles, so that those in flight together share operands in L2
+// (measured, us, at 8 and at 16: 4096 x 4096 x 8192 forward 306 and 290, 8192 x 4096 x 8192
+// the same).
+constexpr int kGroup = 16;
 __device__ __forceinline__ Tile tile_at(const GemmParams& p, int index, int rows, int cols) {
   const int area = p.tiles_m * p.tiles_n;
   Tile t;
   t.output = index / area;
   index -= t.output * area;
-  const int group = index / (8 * p.tiles_n);
-  const int height = min(8, p.tiles_m - group * 8);
-  index -= group * 8 * p.tiles_n;
-  t.m0 = (group * 8 + index % height) * rows;
+  const int group = index / (kGroup * p.tiles_n);
+  const int height = min(kGroup, p.tiles_m - group * kGroup);
+  index -= group * kGroup * p.tiles_n;
+  t.m0 = (group * kGroup + index % height) * rows;
   t.n0 = index / height * cols;
   return t;
 }

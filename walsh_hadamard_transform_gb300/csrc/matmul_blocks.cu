@@ -190,12 +190,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int begin = SPLIT == 1 ? 0 : min(p.blocks, (int)cluster_rank() * share);
   const int end = SPLIT == 1 ? p.blocks : min(p.blocks, begin + share);
 
-  // Tiles in groups of 8 rows of tiles, so that those in flight together share operands in L2.
+  // Tiles in groups of 16 rows of tiles, so that those in flight together share operands in L2
+  // (4096 x 8192 x 8192: 195 us, with 8 rows 200).
+  constexpr int kGroup = 16;
   auto place = [&](int index, int& m0, int& n0) {
-    const int group = index / (8 * p.tiles_n);
-    const int height = min(8, p.tiles_m - group * 8);
-    index -= group * 8 * p.tiles_n;
-    m0 = (group * 8 + index % height) * (128 * CG);
+    const int group = index / (kGroup * p.tiles_n);
+    const int height = min(kGroup, p.tiles_m - group * kGroup);
+    index -= group * kGroup * p.tiles_n;
+    m0 = (group * kGroup + index % height) * (128 * CG);
     n0 = index / height * BN;
   };
 
