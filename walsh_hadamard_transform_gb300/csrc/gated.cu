@@ -18,9 +18,9 @@
 // pair two CTAs on a tile of 256 x 256: each loads half of both operands, which halves the
 // shared-memory traffic of the second.
 //
-// Bound, large: the tensor cores under the power limit.  8192 x 4096 x 8192 bf16 forward: 533
-// to 600 us by the values' spread and the GPU, 1830 to 2060 TFLOP/s, the tensor pipe active
-// 92% of the cycles; 8192 x 2048 x 8192 backward: 0.90 to 1.03 ms, 1600 to 1830 TFLOP/s.
+// Bound, large: the tensor cores under the power limit.  8192 x 4096 x 8192 bf16 forward: 513
+// to 615 us by the values' spread and the GPU, 1790 to 2140 TFLOP/s, the tensor pipe active
+// 92% of the cycles; 8192 x 2048 x 8192 backward: 0.90 to 1.07 ms, 1540 to 1830 TFLOP/s.
 // Small: latency, some 3 us from launch to the last store and 0.2 to 0.3 us a stage; 333 x
 // 1008 x 2736 forward 7.1 us, 517 x 1008 x 2736 backward 38 us in three launches.
 #include <algorithm>
