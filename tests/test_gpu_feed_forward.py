@@ -466,3 +466,46 @@ def test_streams_and_graph_capture(m):
     torch.cuda.synchronize()
     assert torch.equal(kept[3], want) and all(torch.equal(a, b) for a, b in zip(grads, want_grads))
     assert fwt.device_status() == fwt.FWT_OK
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_allocations_belong_to_the_calls_stream(raw):
+    """Memory that a call on another stream allocates is not the current stream's to hand on:
+    a temporary of a chain on `side` may still be read there when its tensor is gone."""
+    m, d, f = 1024, 512, 4096  # 8 MB of h: blocks that the allocator keeps and hands on again
+    x, wg, wu, grad = gated_inputs(m, d, f, "bf16")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    stream = side.cuda_stream if raw else side
+
+    def outputs():
+        h = fwt.gated(x, wg, wu, stream=stream)
+        codes, scale = fwt.quantize_blocks(h, rotate=7, lines=128, stream=stream)
+        c = fwt.matmul_blocks(codes, fwt.quantize_blocks(h, stream=stream)[1], codes, scale,
+                              stream=stream)
+        return [h, codes, c, *fwt.gated_backward(grad, x, wg, wu, stream=stream)]
+
+    made = outputs()
+    side.synchronize()
+    freed = [(t.data_ptr(), t.numel() * t.element_size()) for t in made]
+    sizes = sorted({size for _, size in freed})
+    del made
+    taken = []  # as many blocks of each size on the current stream as were freed, and more
+    for size in sizes:
+        taken += [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(len(freed) + 1)]
+    for t in taken:
+        for at, size in freed:
+            assert t.data_ptr() >= at + size or at >= t.data_ptr() + t.numel()
+    assert fwt.device_status() == fwt.FWT_OK
+
+
+def test_the_default_stream_by_its_handle():
+    x, wg, wu, grad = gated_inputs(24, 256, 640, "f16")
+    want = [fwt.gated(x, wg, wu), *fwt.gated_backward(grad, x, wg, wu)]
+    torch.cuda.synchronize()
+    for handle in (0, 1):
+        got = [fwt.gated(x, wg, wu, stream=handle), *fwt.gated_backward(grad, x, wg, wu, stream=handle)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert fwt.device_status() == fwt.FWT_OK

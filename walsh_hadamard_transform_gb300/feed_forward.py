@@ -11,7 +11,8 @@ contraction leaves the product as it is.  Matrices are 2-D tensors whose rows ar
 contiguous (stride 1 along the columns) and may be a window of a larger matrix;
 operands of products start every row on a 16-byte boundary.  Outputs made here have
 such rows too (padded where the width asks for it).  Every call runs on ``stream``
-(default: the current PyTorch stream) and does not synchronise.
+(default: the current PyTorch stream) and does not synchronise; what it allocates belongs
+to that stream, as under ``torch.cuda.stream``.
 """
 from __future__ import annotations
 
@@ -55,14 +56,28 @@ def _matrix(t, name, device, dtype=None, shape=None):
     return row
 
 
-def _empty(rows, cols, dtype, device, multiple):
-    """A new rows x cols tensor, its rows a multiple of ``multiple`` elements apart, and that
-    distance."""
+def _empty(rows, cols, dtype, device, multiple, stream):
+    """A new rows x cols tensor for work on ``stream``, its rows a multiple of ``multiple``
+    elements apart, and that distance."""
+    if stream is not None:
+        with _allocations(device, stream):
+            return _empty(rows, cols, dtype, device, multiple, None)
     over = cols % multiple
     if over:
         ld = cols + multiple - over
         return _torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device), ld
     return _torch.empty((rows, cols), dtype=dtype, device=device), cols
+
+
+def _allocations(device, stream):
+    """A context in which new tensors belong to ``stream``, a PyTorch stream or a raw handle:
+    memory of the current stream may still be in use there, and may be handed out again there
+    before ``stream`` is done with it."""
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)  # (0 and 1 are names of the default stream)
+        stream = (_torch.cuda.ExternalStream(handle, device=device) if handle > 1
+                  else _torch.cuda.default_stream(device))
+    return _torch.cuda.stream(stream)
 
 
 def _run(device, stream, entry, *args):
@@ -104,8 +119,8 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     length += -length % (1 << rotate)
     shape = (-(-across // lines), -(-length // 128))
     if out is None:
-        q, ld_q = _empty(across, length, _E4M3, x.device, 16)
-        scale, ld_s = _empty(*shape, _F32, x.device, 4)
+        q, ld_q = _empty(across, length, _E4M3, x.device, 16, stream)
+        scale, ld_s = _empty(*shape, _F32, x.device, 4, stream)
     else:
         q, scale = out
         ld_q = _matrix(q, "codes", device, _E4M3, (across, length))
@@ -142,7 +157,7 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
         kind = _REALS.get(out_dtype)
         if kind is None:
             raise TypeError(f"unsupported dtype {out_dtype}: use float32, bfloat16 or float16")
-        out, ld_c = _empty(m, n, out_dtype, a.device, 4 if kind == 0 else 8)
+        out, ld_c = _empty(m, n, out_dtype, a.device, 4 if kind == 0 else 8, stream)
     else:
         kind = _REALS.get(out.dtype)
         if kind is None or (out_dtype is not None and out.dtype != out_dtype):
@@ -183,7 +198,7 @@ def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
     dtype, kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up,
                                                                            activation)
     if out is None:
-        out, ld_h = _empty(m, f, dtype, x.device, 8)
+        out, ld_h = _empty(m, f, dtype, x.device, 8, stream)
     else:
         ld_h = _matrix(out, "out", device, dtype, (m, f))
     st = _run(device, stream, _lib.fwt_gated, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g,
@@ -216,25 +231,21 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
             raise ValueError("out must hold the gradients named in want, and no other")
     if want_x:
         if dx is None:
-            dx, ld_dx = _empty(m, d, dtype, x.device, 8)
+            dx, ld_dx = _empty(m, d, dtype, x.device, 8, stream)
         else:
             ld_dx = _matrix(dx, "dx", device, dtype, (m, d))
         p_dx = dx.data_ptr()
     if want_w:
         if dw_gate is None:
-            dw_gate, ld_dg = _empty(f, d, dtype, x.device, 8)
-            dw_up, ld_du = _empty(f, d, dtype, x.device, 8)
+            dw_gate, ld_dg = _empty(f, d, dtype, x.device, 8, stream)
+            dw_up, ld_du = _empty(f, d, dtype, x.device, 8, stream)
         else:
             ld_dg = _matrix(dw_gate, "dw_gate", device, dtype, (f, d))
             ld_du = _matrix(dw_up, "dw_up", device, dtype, (f, d))
         p_dg, p_du = dw_gate.data_ptr(), dw_up.data_ptr()
     if workspace is None:
         size = _lib.fwt_gated_backward_workspace_bytes(m, f)
-        workspace = _torch.empty(size, dtype=_torch.uint8, device=x.device)
-        if stream is not None:
-            # the allocator must not hand the memory on before `stream` is done with it
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream")
-                                    else _torch.cuda.ExternalStream(int(stream), device=x.device))
+        workspace, _ = _empty(1, size, _torch.uint8, x.device, 1, stream)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     else:
