@@ -345,9 +345,17 @@ int fwt_gated(const void* x, int64_t ld_x, const void* w_gate, int64_t ld_gate, 
  *
  * Sums are fp32.  For m > 8, dg and du are rounded to `type` once, in the workspace, as the
  * operands of the second products (16-bit tensor-core operands; that rounding is as large as
- * the outputs' own); for m <= 8 they stay in fp32.  dx (m x d) may be NULL, and dw_gate and dw_up (f x d) both
+ * the outputs' own); for m <= 8 they stay in fp32.  For FWT_F16 and m > 8 both are held times one
+ * power of two, taken from a bound B on all of them, so that none leaves the range of float16:
+ *
+ *     B = 1.13 max_i (max_j |grad[i, j]| |x[i, :]|) max_j max(|w_gate[j, :]|, |w_up[j, :]|)
+ *
+ * with Euclidean norms of the rows; what is below 2^-28 B keeps fewer bits, in steps of at most
+ * 2^-38 B.  dx (m x d) may be NULL, and dw_gate and dw_up (f x d) both
  * NULL, where they are not wanted.  Outputs are written, not added to.  workspace: DEVICE
- * memory, 16-byte aligned, of at least fwt_gated_backward_workspace_bytes(m, f) bytes.
+ * memory, 16-byte aligned, of at least fwt_gated_backward_workspace_bytes_for(type, m, f) bytes.
+ * (fwt_gated_backward_workspace_bytes is that of FWT_BF16; FWT_F16 asks for 4096 more where
+ * m > 8, for B.)
  */
 int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t ld_x,
                        const void* w_gate, int64_t ld_gate, const void* w_up, int64_t ld_up,
@@ -355,6 +363,7 @@ int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t
                        int64_t ld_dw_up, int type, int activation, int64_t m, int64_t f,
                        int64_t d, void* workspace, size_t workspace_bytes, fwt_stream_t stream);
 size_t fwt_gated_backward_workspace_bytes(int64_t m, int64_t f);
+size_t fwt_gated_backward_workspace_bytes_for(int type, int64_t m, int64_t f);
 
 /* Static text for a status code (never NULL). */
 const char* fwt_status_string(int status);

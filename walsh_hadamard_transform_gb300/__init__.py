@@ -135,6 +135,8 @@ def library() -> ctypes.CDLL:
         lib.fwt_gated_backward.restype = ci
         lib.fwt_gated_backward_workspace_bytes.argtypes = [i64, i64]
         lib.fwt_gated_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.fwt_gated_backward_workspace_bytes_for.argtypes = [ci, i64, i64]
+        lib.fwt_gated_backward_workspace_bytes_for.restype = ctypes.c_size_t
         _lib = lib
     return _lib
 
@@ -599,4 +601,5 @@ def transform_host(re, im=None, out_re=None, out_im=None, normalize: bool = True
     return out_re, out_im
 
 
-from .feed_forward import gated, gated_backward, matmul_blocks, quantize_blocks  # noqa: E402,F401
+from .feed_forward import (fwt_gated_backward_workspace_bytes, gated, gated_backward,  # noqa: E402,F401
+                           matmul_blocks, quantize_blocks)

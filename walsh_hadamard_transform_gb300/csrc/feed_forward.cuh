@@ -43,16 +43,27 @@ cudaError_t launch_gated_token_gradients(CMat grad, CMat x, CMat w_gate, CMat w_
                                          Mat dw_gate, Mat dw_up, void* work, int type,
                                          int activation, int m, int f, int d, cudaStream_t st);
 
-// dg and du into the workspace matrices, rows of ld elements (a multiple of 8).
+// For float16, what dg and du are multiplied by to stay in its range: a power of two from a bound
+// on them all, which is the product of the largest first and the largest second of `parts` pairs.
+struct Bounds {
+  float* pairs;
+  int parts;
+};
+constexpr int kMostBounds = 512;
+cudaError_t launch_gated_bounds(CMat grad, CMat x, CMat w_gate, CMat w_up, Bounds& bounds, int m,
+                                int f, int d, cudaStream_t st);
+
+// dg and du into the workspace matrices, rows of ld elements (a multiple of 8).  (The bounds of
+// these three are read for float16 alone.)
 cudaError_t launch_gated_gradients(CMat grad, CMat x, CMat w_gate, CMat w_up, Mat dg, Mat du,
-                                   int type, int activation, int m, int f, int d,
+                                   Bounds bounds, int type, int activation, int m, int f, int d,
                                    cudaStream_t st);
 // dx = dg w_gate + du w_up.
-cudaError_t launch_gated_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, int type, int m,
-                            int f, int d, cudaStream_t st);
+cudaError_t launch_gated_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, Bounds bounds,
+                            int type, int m, int f, int d, cudaStream_t st);
 // dw_gate = dg^T x, dw_up = du^T x.
-cudaError_t launch_gated_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int type, int m,
-                            int f, int d, cudaStream_t st);
+cudaError_t launch_gated_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, Bounds bounds,
+                            int type, int m, int f, int d, cudaStream_t st);
 
 // Read and clear the device error words of the kernels that wait (synchronising).
 cudaError_t read_device_error_gated(unsigned int* out);

@@ -151,6 +151,12 @@ size_t fwt_gated_backward_workspace_bytes(int64_t m, int64_t f) {
   return (size_t)m * line * 4;                     // dg and du, rows of a multiple of 8
 }
 
+size_t fwt_gated_backward_workspace_bytes_for(int type, int64_t m, int64_t f) {
+  const size_t both = fwt_gated_backward_workspace_bytes(m, f);
+  if (type != FWT_BF16 && type != FWT_F16) return 0;
+  return both && type == FWT_F16 && m > kMostGradientTokens ? both + kMostBounds * 8 : both;
+}
+
 int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t ld_x,
                        const void* w_gate, int64_t ld_gate, const void* w_up, int64_t ld_up,
                        void* dx, int64_t ld_dx, void* dw_gate, int64_t ld_dw_gate, void* dw_up,
@@ -180,13 +186,13 @@ int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t
     if (want_dw && err == cudaSuccess) err = zero({dw_up, ld_dw_up}, 2, f, d, st);
     return done(err);
   }
-  if (!workspace || workspace_bytes < fwt_gated_backward_workspace_bytes(m, f))
+  if (!workspace || workspace_bytes < fwt_gated_backward_workspace_bytes_for(type, m, f))
     return FWT_ERR_INVALID_ARG;
   if (misaligned_rows(grad, ld_grad, 2) || misaligned_rows(x, ld_x, 2) ||
       misaligned_rows(w_gate, ld_gate, 2) || misaligned_rows(w_up, ld_up, 2) ||
       !aligned16(workspace))
     return FWT_ERR_MISALIGNED;
-  const int64_t ws_bytes = (int64_t)fwt_gated_backward_workspace_bytes(m, f);
+  const int64_t ws_bytes = (int64_t)fwt_gated_backward_workspace_bytes_for(type, m, f);
   const Window inputs[] = {wdy, wx, wg, wu, {(uintptr_t)workspace, 1, ws_bytes, ws_bytes}};
   const Window outputs[] = {wdx, wdg, wdu};
   for (int o = 0; o < 3; ++o) {
@@ -206,13 +212,18 @@ int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t
   const int64_t ld = (f + 7) / 8 * 8;
   Mat dg{workspace, ld}, du{(char*)workspace + (size_t)m * (size_t)ld * 2, ld};
   const CMat cx{x, ld_x}, cg{w_gate, ld_gate}, cu{w_up, ld_up}, cdg{dg.p, ld}, cdu{du.p, ld};
-  cudaError_t err = launch_gated_gradients({grad, ld_grad}, cx, cg, cu, dg, du, type, activation,
-                                           (int)m, (int)f, (int)d, st);
+  Bounds bounds{(float*)((char*)workspace + (size_t)m * (size_t)ld * 4), 0};
+  cudaError_t err = cudaSuccess;
+  if (type == FWT_F16)
+    err = launch_gated_bounds({grad, ld_grad}, cx, cg, cu, bounds, (int)m, (int)f, (int)d, st);
+  if (err == cudaSuccess)
+    err = launch_gated_gradients({grad, ld_grad}, cx, cg, cu, dg, du, bounds, type, activation,
+                                 (int)m, (int)f, (int)d, st);
   if (err == cudaSuccess && want_dx)
-    err = launch_gated_dx(cdg, cdu, cg, cu, {dx, ld_dx}, type, (int)m, (int)f, (int)d, st);
+    err = launch_gated_dx(cdg, cdu, cg, cu, {dx, ld_dx}, bounds, type, (int)m, (int)f, (int)d, st);
   if (err == cudaSuccess && want_dw)
-    err = launch_gated_dw(cdg, cdu, cx, {dw_gate, ld_dw_gate}, {dw_up, ld_dw_up}, type, (int)m,
-                          (int)f, (int)d, st);
+    err = launch_gated_dw(cdg, cdu, cx, {dw_gate, ld_dw_gate}, {dw_up, ld_dw_up}, bounds, type,
+                          (int)m, (int)f, (int)d, st);
   return done(err);
 }
 

@@ -53,6 +53,7 @@ struct GemmParams {
   int64_t ld_out[2];
   int act;
   int vec;                // output rows start on 16-byte boundaries
+  Bounds bounds;          // gradients, dx and dw in float16
 };
 
 struct GemmMaps {
@@ -180,6 +181,122 @@ __device__ __forceinline__ void load_rows(const T* in, int64_t ld, uint8_t* piec
   }
 }
 
+// ---- the range of dg and du in float16 -------------------------------------------------
+//
+// dg = dh u act'(g) and du = dh act(g) of a scaled loss pass 65504 long before the sums over them
+// do, and the gradients at the end of training fall below 2^-24.  |u| <= |x_m| |w_up_f| (Euclidean
+// norms), |act(g)| <= |g| <= |x_m| |w_gate_f| and |act'| < 1.13, so
+//
+//     |dg|, |du| <= 1.13 max_m (max_f |dh| |x_m|) max_f max(|w_gate_f|, |w_up_f|) = B,
+//
+// and both are held as 2^k dg and 2^k du with 2^14 <= 2^k B < 2^15 (kGradients), of which dx and
+// dw take 2^k away from their fp32 sums.  Powers of two change no rounding; what lies below
+// 2^-28 B is held in steps of 2^-38 B or less.  k is one for the whole call, as dx sums over the columns of dg and dw over its rows.  bfloat16 has fp32's range and needs
+// none of it.  Elements that are not finite count as zero here: their rows and columns are not
+// finite either way, and the others keep a scale of their own making.
+//
+// Bound: the latency of a row's few loads, then HBM, every input once: 9 us of the 50 that 517 x
+// 1001 x 2731 takes (17 MB), 20 us for 64 x 2048 x 8192 (69 MB), where 24 were with half the warps.
+
+// The largest magnitude (SQUARES: the sum of squares) of a row, over the lanes of a warp.
+// Elements that are not finite are left out, in a second pass where there are any: no finite
+// float16 takes either beyond fp32.
+template <bool SQUARES, bool CHECKED>
+__device__ __forceinline__ float row_pass(const __half* from, int cols, int lane) {
+  float sums[8] = {};  // independent of one another: the additions' latency bounds this
+  auto take = [](float& sum, float v) {
+    if (CHECKED && !(fabsf(v) < INFINITY)) return;
+    sum = SQUARES ? fmaf(v, v, sum) : fmaxf(sum, fabsf(v));
+  };
+  constexpr int kAhead = 4;
+  const int whole = cols & ~7;
+  for (int64_t c = 8 * lane; c < whole; c += 256 * kAhead) {
+    uint4 q[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      q[i] = c + 256 * i < whole ? *(const uint4*)(from + c + 256 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack2<__half>(w[j]);
+        take(sums[2 * j], v.x), take(sums[2 * j + 1], v.y);
+      }
+    }
+  }
+  if (whole + lane < cols) take(sums[0], __half2float(from[whole + lane]));
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = SQUARES ? sum + sums[j] : fmaxf(sum, sums[j]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float other = __shfl_xor_sync(~0u, sum, o);
+    sum = SQUARES ? sum + other : fmaxf(sum, other);
+  }
+  return sum;
+}
+template <bool SQUARES>
+__device__ __forceinline__ float row_magnitude(CMat mat, int row, int cols, int lane) {
+  const __half* from = (const __half*)mat.p + (int64_t)row * mat.ld;
+  const float sum = row_pass<SQUARES, false>(from, cols, lane);
+  return sum < INFINITY ? sum : row_pass<SQUARES, true>(from, cols, lane);
+}
+
+struct BoundParams {
+  CMat grad, x, w_gate, w_up;
+  float2* pairs;
+  int m, f, d;
+};
+constexpr int kBoundWarps = 16;
+
+__global__ void __launch_bounds__(kBoundWarps * 32, 3) bounds_kernel(const BoundParams p) {
+  __shared__ float2 tops[kBoundWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rows = (int64_t)p.m + p.f;
+  float2 most = make_float2(0.f, 0.f);
+  pdl_begin();
+  for (int64_t r = (int64_t)blockIdx.x * kBoundWarps + warp; r < rows; r += (int64_t)gridDim.x * kBoundWarps) {
+    if (r < p.m) {
+      const float dh = row_magnitude<false>(p.grad, (int)r, p.f, lane);
+      const float x = row_magnitude<true>(p.x, (int)r, p.d, lane);
+      most.x = fmaxf(most.x, dh * sqrtf(x));
+    } else {
+      const int j = (int)(r - p.m);
+      const float g = row_magnitude<true>(p.w_gate, j, p.d, lane);
+      const float u = row_magnitude<true>(p.w_up, j, p.d, lane);
+      most.y = fmaxf(most.y, sqrtf(fmaxf(g, u)));
+    }
+  }
+  if (lane == 0) tops[warp] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kBoundWarps; ++w)
+      most.x = fmaxf(most.x, tops[w].x), most.y = fmaxf(most.y, tops[w].y);
+    p.pairs[blockIdx.x] = most;
+  }
+}
+
+// 2^k (INVERSE: 2^-k) in every lane of a warp; 1 where the bound is zero.  Bounds of float16
+// operands lie between 2^-73 and 2^80, so both are normal numbers.
+template <bool INVERSE>
+__device__ __forceinline__ float range_scale(const Bounds& b, int lane) {
+  float2 most = make_float2(0.f, 0.f);
+  for (int i = lane; i < b.parts; i += 32) {
+    const float2 v = ((const float2*)b.pairs)[i];
+    most.x = fmaxf(most.x, v.x), most.y = fmaxf(most.y, v.y);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    most.x = fmaxf(most.x, __shfl_xor_sync(~0u, most.x, o));
+    most.y = fmaxf(most.y, __shfl_xor_sync(~0u, most.y, o));
+  }
+  const float bound = 1.13f * most.x * most.y;
+  if (!(bound > 0.f)) return 1.f;
+  const int e = (int)(__float_as_uint(bound) >> 23) - 127;  // 2^e <= bound < 2^(e + 1)
+  return __uint_as_float((uint32_t)(127 + (INVERSE ? e - 14 : 14 - e)) << 23);
+}
+
 // SPLIT: CTAs of a cluster that share out the contraction of a tile.
 template <typename T, int MODE, int CG, int BN, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -305,6 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (CG == 2) release = map_to_rank(release, 0);
       uint8_t* ring_memory = dynamic + (ring - smem_u32(dynamic));
       uint8_t* piece = ring_memory + C::kStages * C::kStage + (warp - 2) * kPieceBytes;
+      constexpr bool kScaled = std::is_same<T, __half>::value && MODE != kForward;
+      float scale = 1.f;
+      if constexpr (kScaled) scale = range_scale<MODE != kGradients>(p.bounds, lane);
       for (int index = first; index < tiles; index += stride) {
         const Tile t = tile_at(p, index, 128 * CG, kCols);
         const int row0 = t.m0 + (int)rank * 128 + quarter * 32;
@@ -326,12 +446,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (MODE == kForward) {
                 packed[i] = pack2<T>(v0 * u0, v1 * u1);
               } else {
-                const float2 g = unpack2<T>(dh[i]);
+                float2 g = unpack2<T>(dh[i]);
+                if constexpr (kScaled) g.x *= scale, g.y *= scale;
                 packed[i] = pack2<T>(g.x * u0 * s0, g.y * u1 * s1);
                 dh[i] = pack2<T>(g.x * v0, g.y * v1);
               }
             } else {
-              packed[i] = pack2<T>(a0, a1);
+              packed[i] = kScaled ? pack2<T>(a0 * scale, a1 * scale) : pack2<T>(a0, a1);
             }
           }
           const int o = MODE == kDw ? t.output : 0;
@@ -515,8 +636,8 @@ cudaError_t run_paired(CMat x, CMat w_gate, CMat w_up, GemmParams p, int d, cuda
 }
 
 template <typename T>
-cudaError_t run_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, int m, int f, int d,
-                   cudaStream_t st) {
+cudaError_t run_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, Bounds bounds, int m, int f,
+                   int d, cudaStream_t st) {
   GemmMaps maps;
   if (!make_map<T>(&maps.a[0], {dg, m, f, 128}) || !make_map<T>(&maps.a[1], {du, m, f, 128}) ||
       !make_map<T>(&maps.b[0], {w_gate, f, d, kTileK}) ||
@@ -524,13 +645,13 @@ cudaError_t run_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, int m, int 
     return cudaErrorInvalidValue;
   GemmParams p{};
   p.m = m, p.n = d, p.k_blocks = (f + kTileK - 1) / kTileK, p.phases = 2, p.outputs = 1;
-  p.out[0] = dx.p, p.ld_out[0] = dx.ld, p.vec = vector_rows(dx);
+  p.out[0] = dx.p, p.ld_out[0] = dx.ld, p.vec = vector_rows(dx), p.bounds = bounds;
   return launch_mode<T, kDx>(choose_cut(m, d, 1, 2 * (int64_t)p.k_blocks, 8), maps, p, st);
 }
 
 template <typename T>
-cudaError_t run_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int m, int f, int d,
-                   cudaStream_t st) {
+cudaError_t run_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, Bounds bounds, int m, int f,
+                   int d, cudaStream_t st) {
   GemmMaps maps;
   if (!make_map<T>(&maps.a[0], {dg, m, f, kTileK}) || !make_map<T>(&maps.a[1], {du, m, f, kTileK}) ||
       !make_map<T>(&maps.b[0], {x, m, d, kTileK}))
@@ -540,7 +661,7 @@ cudaError_t run_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int m, int 
   p.m = f, p.n = d, p.k_blocks = (m + kTileK - 1) / kTileK, p.phases = 1, p.outputs = 2;
   p.out[0] = dw_gate.p, p.ld_out[0] = dw_gate.ld;
   p.out[1] = dw_up.p, p.ld_out[1] = dw_up.ld;
-  p.vec = vector_rows(dw_gate) && vector_rows(dw_up);
+  p.vec = vector_rows(dw_gate) && vector_rows(dw_up), p.bounds = bounds;
   return launch_mode<T, kDw>(choose_cut(f, d, 2, p.k_blocks, 8), maps, p, st);
 }
 
@@ -562,9 +683,19 @@ cudaError_t launch_gated(CMat x, CMat w_gate, CMat w_up, Mat h, int type, int ac
                           : run_paired<__half, kForward>(x, w_gate, w_up, p, d, st);
 }
 
+cudaError_t launch_gated_bounds(CMat grad, CMat x, CMat w_gate, CMat w_up, Bounds& bounds, int m,
+                                int f, int d, cudaStream_t st) {
+  const int64_t rows = (int64_t)m + f, most = std::min(kMostBounds, 3 * multiprocessors());
+  bounds.parts = (int)std::min<int64_t>(most, (rows + kBoundWarps - 1) / kBoundWarps);
+  const BoundParams p{grad, x, w_gate, w_up, (float2*)bounds.pairs, m, f, d};
+  return launch_overlapped(bounds_kernel, (unsigned)bounds.parts, kBoundWarps * 32, 0, 1, st, p);
+}
+
 cudaError_t launch_gated_gradients(CMat grad, CMat x, CMat w_gate, CMat w_up, Mat dg, Mat du,
-                                   int type, int act, int m, int f, int d, cudaStream_t st) {
+                                   Bounds bounds, int type, int act, int m, int f, int d,
+                                   cudaStream_t st) {
   GemmParams p{};
+  p.bounds = bounds;
   p.m = m, p.n = f, p.act = act;
   p.grad = grad.p, p.ld_grad = grad.ld;
   p.out[0] = dg.p, p.ld_out[0] = dg.ld, p.out[1] = du.p, p.ld_out[1] = du.ld;
@@ -573,16 +704,16 @@ cudaError_t launch_gated_gradients(CMat grad, CMat x, CMat w_gate, CMat w_up, Ma
                           : run_paired<__half, kGradients>(x, w_gate, w_up, p, d, st);
 }
 
-cudaError_t launch_gated_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, int type, int m,
-                            int f, int d, cudaStream_t st) {
-  return type == FWT_BF16 ? run_dx<__nv_bfloat16>(dg, du, w_gate, w_up, dx, m, f, d, st)
-                          : run_dx<__half>(dg, du, w_gate, w_up, dx, m, f, d, st);
+cudaError_t launch_gated_dx(CMat dg, CMat du, CMat w_gate, CMat w_up, Mat dx, Bounds bounds,
+                            int type, int m, int f, int d, cudaStream_t st) {
+  return type == FWT_BF16 ? run_dx<__nv_bfloat16>(dg, du, w_gate, w_up, dx, bounds, m, f, d, st)
+                          : run_dx<__half>(dg, du, w_gate, w_up, dx, bounds, m, f, d, st);
 }
 
-cudaError_t launch_gated_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, int type, int m,
-                            int f, int d, cudaStream_t st) {
-  return type == FWT_BF16 ? run_dw<__nv_bfloat16>(dg, du, x, dw_gate, dw_up, m, f, d, st)
-                          : run_dw<__half>(dg, du, x, dw_gate, dw_up, m, f, d, st);
+cudaError_t launch_gated_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, Bounds bounds,
+                            int type, int m, int f, int d, cudaStream_t st) {
+  return type == FWT_BF16 ? run_dw<__nv_bfloat16>(dg, du, x, dw_gate, dw_up, bounds, m, f, d, st)
+                          : run_dw<__half>(dg, du, x, dw_gate, dw_up, bounds, m, f, d, st);
 }
 
 // Reads and clears this translation unit's device error word (synchronising).

@@ -215,8 +215,9 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
     Returns (dx, dw_gate, dw_up), of the inputs' shapes and type; those not named in
     ``want`` ("x", and "w" for both weights) are not computed and None.  ``out``: the
     three tensors to write to.  ``workspace``: a CUDA tensor of at least
-    ``fwt_gated_backward_workspace_bytes(m, f)`` bytes for the gradients of the two
-    products (allocated here when None)."""
+    ``fwt_gated_backward_workspace_bytes(m, f, dtype)`` bytes for the gradients of the two
+    products (allocated here when None, or when a float16 call is given one of the size for
+    bfloat16)."""
     dtype, kind, act, device, m, f, d, ld_x, ld_g, ld_u = _gated_arguments(x, w_gate, w_up,
                                                                            activation)
     ld_dy = _matrix(grad, "grad", device, dtype, (m, f))
@@ -243,13 +244,17 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
             ld_dg = _matrix(dw_gate, "dw_gate", device, dtype, (f, d))
             ld_du = _matrix(dw_up, "dw_up", device, dtype, (f, d))
         p_dg, p_du = dw_gate.data_ptr(), dw_up.data_ptr()
+    size = _lib.fwt_gated_backward_workspace_bytes_for(kind, m, f)
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        given = workspace.numel() * workspace.element_size()
+        if _lib.fwt_gated_backward_workspace_bytes(m, f) <= given < size:
+            workspace = None
+        else:
+            size = given
     if workspace is None:
-        size = _lib.fwt_gated_backward_workspace_bytes(m, f)
         workspace, _ = _empty(1, size, _torch.uint8, x.device, 1, stream)
-    elif workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    else:
-        size = workspace.numel() * workspace.element_size()
     st = _run(device, stream, _lib.fwt_gated_backward, grad.data_ptr(), ld_dy, x.data_ptr(), ld_x,
               w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, p_dx, ld_dx, p_dg, ld_dg, p_du, ld_du,
               kind, act, m, f, d, workspace.data_ptr(), size)
@@ -258,5 +263,15 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
     return dx, dw_gate, dw_up
 
 
-def fwt_gated_backward_workspace_bytes(m: int, f: int) -> int:
-    return int(_fwt.library().fwt_gated_backward_workspace_bytes(int(m), int(f)))
+def fwt_gated_backward_workspace_bytes(m: int, f: int, dtype=None) -> int:
+    """Bytes of the workspace of ``gated_backward`` for x of (m, d) and weights of (f, d) of
+    ``dtype``, bfloat16 (also None) or float16."""
+    lib = _fwt.library()
+    if dtype is None:
+        return int(lib.fwt_gated_backward_workspace_bytes(int(m), int(f)))
+    if _lib is None:
+        _load()
+    kind = _REALS.get(dtype)
+    if kind != 1 and kind != 2:
+        raise TypeError(f"unsupported dtype {dtype}: use bfloat16 or float16")
+    return int(lib.fwt_gated_backward_workspace_bytes_for(kind, int(m), int(f)))
