@@ -111,7 +111,7 @@ template <typename U>
 __device__ __forceinline__ typename Vec16<U>::type ldg16(const void* p, unsigned long long pol) {
   using V = typename Vec16<U>::type;
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p), "l"(pol));
   return *reinterpret_cast<V*>(&v);

@@ -162,12 +162,12 @@ __device__ __forceinline__ void load_rows(const T* in, int64_t ld, uint8_t* piec
     if (row0 + r < m && at < n) {
       const T* from = in + (int64_t)(row0 + r) * ld + at;
       if (at + 8 <= n) {
-        q = __ldg((const uint4*)from);
+        q = *(const uint4*)from;
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (at + j < n) w[j / 2] |= (uint32_t)__ldg((const unsigned short*)from + j) << (16 * (j & 1));
+          if (at + j < n) w[j / 2] |= (uint32_t)((const unsigned short*)from)[j] << (16 * (j & 1));
         q = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kDxWarps * 32, 2) token_dx_kernel(const TokenG
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const float4* from = (const float4*)(p.work + ((int64_t)s * p.f + j0 + line) * 8) + (threadIdx.x & 1);
-      const float4 v = j0 + line < end ? __ldg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 v = j0 + line < end ? *from : make_float4(0.f, 0.f, 0.f, 0.f);
       *((float4*)work[turn][s][line] + (threadIdx.x & 1)) = v;
     }
     __syncthreads();  // once a turn: the other half of `work` is read until the next
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kDwWarps * 32) token_dw_kernel(const TokenGrad
     const int s = i / (kDwWarps * kDwLines * 2), line = i / 2 % (kDwWarps * kDwLines);
     const float4* from = (const float4*)(p.work + ((int64_t)s * p.f + first + line) * 8) + (i & 1);
     *((float4*)work[s][line] + (i & 1)) =
-        first + line < p.f ? __ldg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+        first + line < p.f ? *from : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   if (col >= p.d) return;

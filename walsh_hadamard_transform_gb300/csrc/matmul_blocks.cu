@@ -92,11 +92,11 @@ __device__ __forceinline__ float4 scales4(const float* base, int64_t ld, int lin
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (line >= lines) return v;
   const float* row = base + line * ld + t;
-  if (vec && t + 4 <= blocks) return __ldg((const float4*)row);
-  v.x = __ldg(row);
-  if (t + 1 < blocks) v.y = __ldg(row + 1);
-  if (t + 2 < blocks) v.z = __ldg(row + 2);
-  if (t + 3 < blocks) v.w = __ldg(row + 3);
+  if (vec && t + 4 <= blocks) return *(const float4*)row;
+  v.x = *row;
+  if (t + 1 < blocks) v.y = row[1];
+  if (t + 2 < blocks) v.z = row[2];
+  if (t + 3 < blocks) v.w = row[3];
   return v;
 }
 

@@ -122,7 +122,7 @@ struct Block {
           if (sizeof(T) == 4 && p.vec && l < p.nl && pos + 8 <= p.length) {  // (16 bits: staged)
 #pragma unroll
             for (int i = 0; i < kWords; i += 4) {
-              const uint4 v = __ldg((const uint4*)from + i / 4);
+              const uint4 v = ((const uint4*)from)[i / 4];
               w[grp][i][s] = v.x, w[grp][i + 1][s] = v.y, w[grp][i + 2][s] = v.z, w[grp][i + 3][s] = v.w;
             }
           } else {
@@ -133,9 +133,9 @@ struct Block {
               for (int j = 0; j < 8; ++j)
                 if (pos + j < p.length) {
                   if constexpr (sizeof(T) == 2)
-                    w[grp][j / 2][s] |= (uint32_t)__ldg((const unsigned short*)from + j) << (16 * (j & 1));
+                    w[grp][j / 2][s] |= (uint32_t)((const unsigned short*)from)[j] << (16 * (j & 1));
                   else
-                    w[grp][j][s] = __ldg((const uint32_t*)from + j);
+                    w[grp][j][s] = ((const uint32_t*)from)[j];
                 }
             }
           }
@@ -150,19 +150,19 @@ struct Block {
           if constexpr (sizeof(T) == 2) {
             uint32_t v = 0;
             if (p.vec && in && l + 1 < p.nl) {
-              v = __ldg((const uint32_t*)from);
+              v = *(const uint32_t*)from;
             } else {
-              if (in && l < p.nl) v = __ldg((const unsigned short*)from);
-              if (in && l + 1 < p.nl) v |= (uint32_t)__ldg((const unsigned short*)from + 1) << 16;
+              if (in && l < p.nl) v = *(const unsigned short*)from;
+              if (in && l + 1 < p.nl) v |= (uint32_t)((const unsigned short*)from)[1] << 16;
             }
             w[grp][j / 2][j & 1] = v;
           } else {
             uint2 v = make_uint2(0, 0);
             if (p.vec && in && l + 1 < p.nl) {
-              v = __ldg((const uint2*)from);
+              v = *(const uint2*)from;
             } else {
-              if (in && l < p.nl) v.x = __ldg((const uint32_t*)from);
-              if (in && l + 1 < p.nl) v.y = __ldg((const uint32_t*)from + 1);
+              if (in && l < p.nl) v.x = *(const uint32_t*)from;
+              if (in && l + 1 < p.nl) v.y = ((const uint32_t*)from)[1];
             }
             w[grp][j][0] = v.x, w[grp][j][1] = v.y;
           }

@@ -29,6 +29,9 @@ constexpr unsigned int kErrTmaTimeout = 1u;
 // its writes are visible, and then lets the next kernel on the stream be scheduled
 // (it starts once every CTA of this grid has started, so nothing of this grid can
 // be left unscheduled behind it).  Without the launch attribute both are no-ops.
+// Loads after it go the ordinary way: the read-only path (ld.global.nc) is for data that nothing
+// writes while the kernel runs, and a kernel that starts early cannot say that of what the
+// previous one wrote.
 __device__ __forceinline__ void pdl_begin() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

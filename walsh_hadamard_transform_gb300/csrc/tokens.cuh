@@ -24,13 +24,13 @@ template <int SIZE>
 __device__ __forceinline__ uint4 load16(const uint8_t* line, int64_t at, int64_t bytes) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (!line || at >= bytes) return v;
-  if (at + 16 <= bytes) return __ldg((const uint4*)(line + at));
+  if (at + 16 <= bytes) return *(const uint4*)(line + at);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 16; i += SIZE)
     if (at + i < bytes) {
-      const uint32_t e = SIZE == 1 ? (uint32_t)__ldg(line + at + i)
-                                   : (uint32_t)__ldg((const unsigned short*)(line + at + i));
+      const uint32_t e = SIZE == 1 ? (uint32_t)line[at + i]
+                                   : (uint32_t)*(const unsigned short*)(line + at + i);
       w[i / 4] |= e << (8 * (i & 3));
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -40,7 +40,7 @@ template <int SIZE>
 __device__ __forceinline__ uint4 load16_once(const uint8_t* line, int64_t at, int64_t bytes) {
   if (line && at + 16 <= bytes) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(line + at));
     return v;
