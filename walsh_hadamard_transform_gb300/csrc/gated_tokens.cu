@@ -59,7 +59,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
 // NT: groups of 8 tokens.  U: stretches whose loads a warp has in flight together.
 template <typename T, int NT, int U, bool GRADIENTS>
 __global__ void __launch_bounds__(kTokenWarps * 32) gated_tokens_kernel(const GatedTokenParams p) {
-  __shared__ float sums[kTokenWarps][2][NT][32][4];
+  __shared__ __align__(16) float sums[kTokenWarps][2][NT][32][4];  // (float4 stores)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int j0 = blockIdx.x * 16;
   const uint8_t* w[2][2];
@@ -90,13 +90,13 @@ __global__ void __launch_bounds__(kTokenWarps * 32) gated_tokens_kernel(const Ga
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            wv[u][s][r][h] = load16_once<2>(w[s][r], at + 64 * h, p.bytes);
+            wv[u][s][r][h] = load16_once(w[s][r], at + 64 * h, p.bytes);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int token = 8 * i + g;
         const uint8_t* x = token < p.m ? p.x + token * p.ld_x : nullptr;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) xv[u][i][h] = load16<2>(x, at + 64 * h, p.bytes);
+        for (int h = 0; h < 2; ++h) xv[u][i][h] = load16(x, at + 64 * h, p.bytes);
       }
     }
 #pragma unroll
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kDxWarps * 32, 2) token_dx_kernel(const TokenG
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int j = j0 + u * 32 + warp * 4 + (lane >> 3);
-        w[u][s] = load16_once<2>(j < end ? p.w[s] + (int64_t)j * p.ld_w[s] : nullptr, (int64_t)col * 2,
+        w[u][s] = load16_once(j < end ? p.w[s] + (int64_t)j * p.ld_w[s] : nullptr, (int64_t)col * 2,
                                  (int64_t)p.d * 2);
       }
     const int line = threadIdx.x >> 1;  // two threads a line, dg then du
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kDwWarps * 32) token_dw_kernel(const TokenGrad
   float x[TM][8];
 #pragma unroll
   for (int t = 0; t < TM; ++t)
-    unpack8<T>(load16<2>(t < p.m ? p.x + t * p.ld_x : nullptr, (int64_t)col * 2, (int64_t)p.d * 2), x[t]);
+    unpack8<T>(load16(t < p.m ? p.x + t * p.ld_x : nullptr, (int64_t)col * 2, (int64_t)p.d * 2), x[t]);
   for (int i = threadIdx.x; i < 2 * kDwWarps * kDwLines * 2; i += kDwWarps * 32) {
     const int s = i / (kDwWarps * kDwLines * 2), line = i / 2 % (kDwWarps * kDwLines);
     const float4* from = (const float4*)(p.work + ((int64_t)s * p.f + first + line) * 8) + (i & 1);

@@ -65,7 +65,7 @@ template <int NT, int W, int S, int LINES>
 __global__ void __launch_bounds__(W * 32) tokens_kernel(const TokenParams p) {
   using R = Ring<NT, W, S>;
   extern __shared__ __align__(16) uint8_t rings[];
-  __shared__ float sums[W][NT][32][4];
+  __shared__ __align__(16) float sums[W][NT][32][4];  // (float4 stores)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int j0 = blockIdx.x * 16;
   uint8_t* ring = rings + warp * (S * R::kStage);

@@ -1,5 +1,5 @@
-// Products of a few tokens (lines of the first operand) with all lines of a weight: what the
-// kernels for single tokens and small batches share.
+// Products of a few tokens (lines of the first operand) with all lines of a weight: the scheme of
+// the kernels for single tokens and small batches, and their reads of 16-bit operands.
 //
 // With few tokens a product is bound by reading the weights once.  A warp reads 16 weight
 // lines into the fragments of 16 x 8 matrix products, 16 bytes a thread, without a tile that
@@ -18,25 +18,19 @@ namespace ff {
 
 constexpr int kTokenWarps = 8;
 
-// 16 bytes of a line of `bytes` bytes from `at` on: zero past its end and for line = null.
-// SIZE: bytes of an element (the line's start and `at` are multiples of 16 bytes).
-template <int SIZE>
+// 16 bytes of a line of `bytes` bytes of 16-bit elements from `at` on: zero past its end and for
+// line = null (the line's start and `at` are multiples of 16 bytes).
 __device__ __forceinline__ uint4 load16(const uint8_t* line, int64_t at, int64_t bytes) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (!line || at >= bytes) return v;
   if (at + 16 <= bytes) return *(const uint4*)(line + at);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 16; i += SIZE)
-    if (at + i < bytes) {
-      const uint32_t e = SIZE == 1 ? (uint32_t)line[at + i]
-                                   : (uint32_t)*(const unsigned short*)(line + at + i);
-      w[i / 4] |= e << (8 * (i & 3));
-    }
+  for (int i = 0; i < 16; i += 2)
+    if (at + i < bytes) w[i / 4] |= (uint32_t)*(const unsigned short*)(line + at + i) << (8 * (i & 3));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The same for weights: read once, so kept out of the way of what is used again.
-template <int SIZE>
 __device__ __forceinline__ uint4 load16_once(const uint8_t* line, int64_t at, int64_t bytes) {
   if (line && at + 16 <= bytes) {
     uint4 v;
@@ -45,7 +39,7 @@ __device__ __forceinline__ uint4 load16_once(const uint8_t* line, int64_t at, in
                  : "l"(line + at));
     return v;
   }
-  return load16<SIZE>(line, at, bytes);
+  return load16(line, at, bytes);
 }
 
 }  // namespace ff
