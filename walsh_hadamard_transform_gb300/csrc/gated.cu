@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
+  __shared__ volatile uint32_t copied;  // stages so far: an epilogue waits for a tile's all
 
   const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 8 * CG);
-    gave_up = 0;
+    gave_up = 0, copied = 0;
     for (int i = 0; i < 2; ++i) prefetch_map(&maps.a[i]), prefetch_map(&maps.b[i]);
   }
   if (warp == 1) tmem_alloc<CG>(&tmem_base, 2 * BN);
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
+          if (lane == 0) copied = copied + 1;
           if (++stage == C::kStages) stage = 0, parity ^= 1;
         }
       }
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 2; ++i)
             if (i * kChunk < kHalf) load_grad(half * kHalf + i * kChunk, dh[i]);
         }
-        if (!wait_or_leave(&acc_full[acc], acc_parity, &gave_up)) return;
+        if (!wait_or_leave(&acc_full[acc], acc_parity, &gave_up, false, &copied)) return;
         tmem_fence_after();
         if constexpr (SPLIT == 1) {
 #pragma unroll

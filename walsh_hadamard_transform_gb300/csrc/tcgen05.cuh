@@ -234,20 +234,34 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
-// A wait of a whole warp: at most about a second, and over at once when another role of the
-// CTA has given up.  false, in every lane: leave the role's loop.
+// The global timer in steps of 2^20 ns, about a millisecond.
+__device__ __forceinline__ uint32_t global_ms() { return (uint32_t)(global_ns() >> 20); }
+
+// A wait of a whole warp: at most about a second in which nothing comes forward, and over at once
+// when another role of the CTA has given up.  false, in every lane: leave the role's loop.
 // `seen`: what an earlier mbar_test of the same phase said (asked ahead, its answer is there
-// by now).
+// by now).  `progress`: what the role waited for counts its steps with, where one wait spans many
+// of them.  A device that other processes have had for a while in between has its clock go on
+// without the warp: no gap between two looks at it counts as more than a tenth of a second.
+template <typename... Progress>
 __device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int* gave_up,
-                                              bool seen = false) {
+                                              bool seen = false, Progress... progress) {
   bool done = seen || mbar_poll(bar, parity);
   for (int i = 0; i < 32 && !done; ++i) done = mbar_poll(bar, parity);
   if (!done) {  // the timer is slow to read: not before it is needed
-    const unsigned long long t0 = global_ns();
+    uint32_t last = global_ms(), spent = 0, steps = (0u + ... + *progress);
     for (uint32_t i = 1; i < (1u << 28); ++i) {
       done = mbar_poll(bar, parity);
       if (done) break;
-      if ((i & 63u) == 0 && (*gave_up || global_ns() - t0 > 1000000000ull)) break;
+      if ((i & 63u) == 0) {
+        const uint32_t now = global_ms();
+        spent += min(now - last, 100u), last = now;
+        if constexpr (sizeof...(Progress) > 0) {
+          const uint32_t at = (0u + ... + *progress);
+          if (at != steps) steps = at, spent = 0, i = 0;
+        }
+        if (*gave_up || spent > 1000u) break;
+      }
     }
     if (!done && !*gave_up) {
       atomicOr(&g_device_error, kErrTmaTimeout);
