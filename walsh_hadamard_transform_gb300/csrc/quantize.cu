@@ -230,7 +230,7 @@ __device__ __forceinline__ void stage_rows(const QuantizeParams& p, uint32_t to,
     for (int i = 0; i < 8; ++i, from += step) copy16(to + i * 512, from);
     return;
   }
-  const int bytes = min(16, max(0, (p.length - col) * 2));
+  const int bytes = 2 * min(8, max(0, p.length - col));  // (of a length times two, 31 bits are too few)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = 2 * i + (lane >> 4), line = strip * 16 + row;
@@ -256,7 +256,7 @@ __device__ __forceinline__ void stage_columns(const QuantizeParams& p, uint32_t 
     for (int i = 0; i < 8; ++i, from += step) copy16(to + column_at<W>(pos + 16 * i, chunk), from);
     return;
   }
-  const int bytes = min(16, max(0, (p.nl - line) * 2));
+  const int bytes = 2 * min(8, max(0, p.nl - line));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int pos = i * 16 + threadIdx.x / kChunks, row = block * 128 + pos;
