@@ -7,7 +7,8 @@
 //   bits 0, 1, 3, 4   one m16n8k16 matrix product of 16 lines by 16 elements with the
 //                     16 x 16 matrix of signs (zeros where an index bit stays as it is).
 //                     Signs and inputs are exact in 16 bits and the sums fp32; an fp32
-//                     input goes in as three bf16 pieces that add up to it exactly.
+//                     input goes in as three bf16 pieces that add up to it exactly (bf16
+//                     ends at 2^-133: a line's block below 2^-64 goes in times 2^64).
 //   bits 2, 5, 6      additions between the thread's own registers.
 //
 // Elements are assigned to the product's slots so that a thread holds the same elements
@@ -96,6 +97,20 @@ __device__ __forceinline__ uint32_t sign16(int ek, int en, int r) {
   return one | ((__popc(ek & en & low) & 1) << 15);
 }
 
+// max(|a|, b), NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(b));
+  return d;
+}
+
+// The largest of |a|, |b| and |c|, NaN if one of them is.
+__device__ __forceinline__ float max_magnitude(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // What a thread loads of one block: 8 consecutive elements in each group of 32 of its two
 // lines.  Axis 1: lines g and g + 8 of the strip, 16 bytes along a row at a time.  Axis 0:
 // lines 2 g and 2 g + 1, which lie side by side in every row of x, both with one load.
@@ -171,6 +186,35 @@ struct Block {
     }
   }
 
+  // fp32 lines whose values in this block are all below 2^-64, times 2^64: an element's pieces end
+  // 2^-24 below it, and bf16 at 2^-133.  (In other lines what is lost there is 2^-69 of the
+  // largest.)  undo: 2^-64 for such lines, else 1.  (8192 x 8192 87 -> 90.5 us along the columns, 118
+  // -> 125 down the rows; to look at the rotated values and go back where they are small cost as much.)
+  __device__ __forceinline__ void lift(float (&undo)[2]) {
+    static_assert(sizeof(T) == 4, "16-bit inputs are their own pieces");
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float top = 0.f;
+#pragma unroll
+      for (int grp = 0; grp < 4; ++grp)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          top = max_magnitude(__uint_as_float(w[grp][j][s]), __uint_as_float(w[grp][j + 1][s]), top);
+      top = max_magnitude(__shfl_xor_sync(~0u, top, 1), top);
+      top = max_magnitude(__shfl_xor_sync(~0u, top, 2), top);
+      const bool small = top < 0x1p-64f && top != 0.f;
+      undo[s] = small ? 0x1p-64f : 1.f;
+      if (__any_sync(~0u, small)) {
+        const float up = small ? 0x1p64f : 1.f;
+#pragma unroll
+        for (int grp = 0; grp < 4; ++grp)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            w[grp][j][s] = __float_as_uint(__uint_as_float(w[grp][j][s]) * up);
+      }
+    }
+  }
+
   // Elements 2 i and 2 i + 1 of a group of line s, as 16-bit pairs: the k-th piece.  An fp32
   // input is taken apart as it is read: call with k = 0, 1, 2 in turn.  Truncation leaves no
   // piece larger than its input, and 8 + 8 + 8 significant bits hold it exactly.
@@ -187,13 +231,6 @@ struct Block {
     }
   }
 };
-
-// max(|a|, b), NaN if either is.
-__device__ __forceinline__ float max_magnitude(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(b));
-  return d;
-}
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   uint16_t lo, hi;
@@ -262,13 +299,6 @@ __device__ __forceinline__ void stage_columns(const QuantizeParams& p, uint32_t 
     const int pos = i * 16 + threadIdx.x / kChunks, row = block * 128 + pos;
     copy16(to + column_at<W>(pos, chunk), p, (int64_t)row * p.ld_x + line, row < p.length ? bytes : 0);
   }
-}
-
-// The largest of |a|, |b| and |c|, NaN if one of them is.
-__device__ __forceinline__ float max_magnitude(float a, float b, float c) {
-  float d;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // Warps of a CTA: consecutive blocks of one strip (axis 1) or consecutive strips (axis 0), so
@@ -342,6 +372,8 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
   }
   for (int round = 0; block < end; block += kStep, ++round) {
     float y[4][2][2][4];  // group of 32, bit 2, bit 1, (line, bit 0)
+    float undo[2] = {1.f, 1.f};  // what takes y back to its size
+    if constexpr (sizeof(T) == 4) x.lift(undo);
     const int now = round % kStages * kStaged;
     if constexpr (STAGED) {
       stage(round + kStages - 1, block + (kStages - 1) * kStep);
@@ -432,6 +464,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
     for (int s = 0; s < 2; ++s) {
       top[s] = max_magnitude(__shfl_xor_sync(~0u, top[s], 1), top[s]);
       top[s] = max_magnitude(__shfl_xor_sync(~0u, top[s], 2), top[s]);
+      if constexpr (sizeof(T) == 4) top[s] *= undo[s];
     }
     if constexpr (LINES == 128) {
       __shared__ float tops[2][W];  // in turn: a warp may be a round ahead of another
@@ -454,6 +487,7 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
       const float reciprocal = __frcp_rn(top[s]), rough = 448.f * reciprocal;
       float factor = fmaf(fmaf(-rough, top[s], 448.f), reciprocal, rough);
       if (scale <= 0x1p-126f) factor = p.norm * 0x1p126f;
+      if constexpr (sizeof(T) == 4) factor *= undo[s];
       if (!(top[s] < INFINITY)) scale = factor = __uint_as_float(0x7fffffffu);
       const int l = lines[s];
       if (LINES == 1 ? t == 0 && l < p.nl : threadIdx.x == 0 && s == 0)
