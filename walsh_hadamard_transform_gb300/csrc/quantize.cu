@@ -478,17 +478,19 @@ __global__ void __launch_bounds__(kWarps<LINES> * 32, kLeast<T, AXIS, LINES>)
       top[0] = top[1] = m;
     }
 
+    float scales[2], factors[2];
+#pragma unroll
+    for (int s = 0; s < (LINES == 128 ? 1 : 2); ++s) {
+      // s = top norm / 448, and norm / s: above the least scale the norm cancels
+      scales[s] = fmaxf(top[s] * p.norm_448, 0x1p-126f);
+      factors[s] = scales[s] <= 0x1p-126f ? p.norm * 0x1p126f : __fdiv_rn(448.f, top[s]);
+      if (!(top[s] < INFINITY)) scales[s] = factors[s] = __uint_as_float(0x7fffffffu);
+    }
+    if constexpr (LINES == 128) scales[1] = scales[0], factors[1] = factors[0];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const bool whole = block * 128 + 128 <= p.full;
-      // s = top norm / 448, and norm / s: above the least scale the norm cancels.  448 / top comes
-      // from the reciprocal, corrected once by its remainder.
-      float scale = fmaxf(top[s] * p.norm_448, 0x1p-126f);
-      const float reciprocal = __frcp_rn(top[s]), rough = 448.f * reciprocal;
-      float factor = fmaf(fmaf(-rough, top[s], 448.f), reciprocal, rough);
-      if (scale <= 0x1p-126f) factor = p.norm * 0x1p126f;
-      if constexpr (sizeof(T) == 4) factor *= undo[s];
-      if (!(top[s] < INFINITY)) scale = factor = __uint_as_float(0x7fffffffu);
+      const float scale = scales[s], factor = sizeof(T) == 4 ? factors[s] * undo[s] : factors[s];
       const int l = lines[s];
       if (LINES == 1 ? t == 0 && l < p.nl : threadIdx.x == 0 && s == 0)
         p.scale[(int64_t)(LINES == 1 ? l : l / 128) * p.ld_scale + block] = scale;
