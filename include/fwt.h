@@ -319,7 +319,9 @@ int fwt_quantize_blocks(const void* x, int x_type, int64_t rows, int64_t cols, i
  * operands run along the contraction, as fwt_quantize_blocks writes them (for the
  * gradient products, along either axis).  Products and sums are fp32, in an order that
  * depends on the sizes and the device alone, with one rounding to c_type; the product of two
- * scales is rounded to fp32 first.  m or n = 0: nothing is written; k = 0: C is zero.
+ * scales is rounded to fp32 first (below 2^-126 to steps of 2^-149), unless that overflows: then
+ * a block's sum is multiplied by one scale after the other, which takes longer where a call has
+ * such scales.  m or n = 0: nothing is written; k = 0: C is zero.
  */
 int fwt_matmul_blocks(const void* a, int64_t ld_a, const float* a_scale, int64_t ld_a_scale,
                       const void* b, int64_t ld_b, const float* b_scale, int64_t ld_b_scale,

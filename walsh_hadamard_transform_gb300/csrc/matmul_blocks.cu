@@ -33,6 +33,7 @@
 #include "feed_forward.cuh"
 #include "ff_host.cuh"
 #include "fwt.h"
+#include "scales.cuh"
 #include "tcgen05.cuh"
 
 namespace fwt {
@@ -49,6 +50,9 @@ constexpr int kLeanRegisters = 72, kSumRegisters = 216;
 static_assert(128 * kLeanRegisters + 256 * kSumRegisters == 384 * 168, "the launch's registers");
 
 struct BlocksParams {
+  const uint8_t *a, *b;
+  int64_t ld_a, ld_b;
+  int k;
   const float *a_scale, *b_scale;
   int64_t ld_as, ld_bs;
   void* c;
@@ -162,6 +166,61 @@ __device__ __forceinline__ void store_rows(const BlocksParams& p, uint8_t* piece
   }
 }
 
+// 16 bytes of a line of k from `at` on: zero past its end and for line = null.
+__device__ __forceinline__ uint4 codes16(const uint8_t* line, int at, int k) {
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (line && at + 16 <= k) return *(const uint4*)(line + at);
+  if (line)
+    for (int i = 0; at + i < k; ++i) w[i / 4] |= (uint32_t)line[at + i] << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A warp's 32 rows and `cols` columns of C again, straight from global memory into 16 x 8 products:
+// for tiles with scales whose product overflows.  (In the loop of sums itself, a way for these
+// costs the others 5%, though no call takes it: the loop then holds its 128 sums differently.)
+template <int LINES>
+__device__ __noinline__ void sum_apart(const BlocksParams& p, int row0, int col0, int cols) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+  for (int sub = 0; sub < 2 * (cols / 8); ++sub) {
+    const int row = row0 + 16 * (sub & 1) + g, col = col0 + 8 * (sub >> 1);
+    if (col >= p.n) break;
+    const int rows[2] = {row, row + 8}, line = col + g;
+    const uint8_t* a[2] = {rows[0] < p.m ? p.a + (int64_t)rows[0] * p.ld_a : nullptr,
+                           rows[1] < p.m ? p.a + (int64_t)rows[1] * p.ld_a : nullptr};
+    const uint8_t* b = line < p.n ? p.b + (int64_t)line * p.ld_b : nullptr;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int block = 0; block < p.blocks; ++block) {
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // (which bytes meet in which slot of a product is free as long as both operands agree)
+        const int at = block * kBlock + 64 * h + 16 * t;
+        const uint4 lo = codes16(a[0], at, p.k), hi = codes16(a[1], at, p.k), x = codes16(b, at, p.k);
+        mma_e4m3(part, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+        mma_e4m3(part, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = rows[e >> 1], j = col + 2 * t + (e & 1);
+        if (i < p.m && j < p.n)
+          sum[e] = add_apart(sum[e], part[e], p.a_scale[i * p.ld_as + block],
+                             p.b_scale[j / LINES * p.ld_bs + block]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = rows[e >> 1], j = col + 2 * t + (e & 1);
+      if (i >= p.m || j >= p.n) continue;
+      const int64_t at = i * p.ld_c + j;
+      if (p.c_type == FWT_F32) ((float*)p.c)[at] = sum[e];
+      else if (p.c_type == FWT_BF16) ((__nv_bfloat16*)p.c)[at] = __float2bfloat16_rn(sum[e]);
+      else ((__half*)p.c)[at] = __float2half_rn(sum[e]);
+    }
+  }
+}
+
 template <int CG, int BN, int LINES, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     blocks_kernel(const __grid_constant__ BlocksMaps maps, const BlocksParams p) {
@@ -177,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       scales_full[2], scales_empty[2];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
+  __shared__ float overflow;  // not 0: some product of scales may
 
   const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
   uint8_t* after_ring = dynamic + (ring - smem_u32(dynamic)) + C::kStages * C::kStage;
@@ -216,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < C::kSlots; ++i) mbar_init(&slot_empty[part][i], 8 / C::kParts * CG);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&scales_full[i], 1), mbar_init(&scales_empty[i], 8);
-    gave_up = 0;
+    gave_up = 0, overflow = 0.f;
     prefetch_map(&maps.a), prefetch_map(&maps.b);
   }
   if (warp == 1) tmem_alloc<CG>(&tmem_base, C::kParts * C::kSlots * C::kCols);
@@ -316,7 +376,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               b[0] = scales4(p.b_scale, p.ld_bs, n0 / 128 + lane, (p.n + 127) / 128, t, p.blocks,
                              vec_bs);
             }
+            // the largest magnitudes, as whole numbers, of scales that are finite (of others the
+            // products are not, however they are taken)
+            uint32_t most[2] = {0, 0};
+            auto look = [&](uint32_t& top, float4 v) {
+              for (const float s : {v.x, v.y, v.z, v.w})
+                if (fabsf(s) < INFINITY) top = max(top, __float_as_uint(s) & 0x7fffffffu);
+            };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) look(most[0], a[i]);
+#pragma unroll
+            for (int i = 0; i < (LINES == 1 ? BN / 32 : 1); ++i)
+              if (LINES == 1 || lane < C::kBScales) look(most[1], b[i]);
+            const float top = __uint_as_float(__reduce_max_sync(~0u, most[0])) *
+                              __uint_as_float(__reduce_max_sync(~0u, most[1]));
             if (!wait_or_leave(&scales_empty[buffer], parity, &gave_up)) return;
+            if (!(top < INFINITY) && lane == 0) overflow = 1.f;
             float* to = scales + buffer * C::kScales;
             auto put = [&](int at, float4 v) {
               to[at] = v.x, to[at + kRow] = v.y, to[at + 2 * kRow] = v.z, to[at + 3 * kRow] = v.w;
@@ -453,6 +528,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             store(piece, row0, col + c, sum);
           }
+          bool again = false;
+          for (int r = 0; r < SPLIT; ++r)
+            again |= load_cluster(map_to_rank(smem_u32(&overflow), r)) != 0.f;
+          __syncwarp();
+          if (again && from < kHalf) sum_apart<LINES>(p, row0, col + from, min(kShare, kHalf - from));
+        }
+      }
+      if (SPLIT == 1 && overflow != 0.f) {
+        for (int index = first; index < tiles; index += stride) {
+          int m0, n0;
+          place(index, m0, n0);
+          __syncwarp();
+          sum_apart<LINES>(p, m0 + (int)rank * 128 + quarter * 32, n0 + half * kHalf, kHalf);
         }
       }
     }();
@@ -520,6 +608,7 @@ cudaError_t launch_matmul_blocks(CMat a, CMat a_scale, CMat b, CMat b_scale, int
   if (m <= 16 || (m <= kMostTokens && (int64_t)n * k <= 6 << 20))
     return launch_matmul_tokens(a, a_scale, b, b_scale, b_lines, c, c_type, m, n, k, st);
   BlocksParams p{};
+  p.a = (const uint8_t*)a.p, p.ld_a = a.ld, p.b = (const uint8_t*)b.p, p.ld_b = b.ld, p.k = k;
   p.a_scale = (const float*)a_scale.p, p.ld_as = a_scale.ld;
   p.b_scale = (const float*)b_scale.p, p.ld_bs = b_scale.ld;
   p.c = c.p, p.ld_c = c.ld, p.c_type = c_type;

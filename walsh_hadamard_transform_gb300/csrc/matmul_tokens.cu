@@ -18,6 +18,7 @@
 #include "feed_forward.cuh"
 #include "ff_host.cuh"
 #include "fwt.h"
+#include "scales.cuh"
 #include "tma.cuh"
 
 namespace fwt {
@@ -33,15 +34,6 @@ struct TokenParams {
   int64_t ld_c;
   int c_type, m, n, k, blocks;
 };
-
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // 16 (or 4) bytes to shared memory, `valid` of them from `from`, zeros after.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, int valid) {
@@ -121,22 +113,39 @@ __global__ void __launch_bounds__(W * 32) tokens_kernel(const TokenParams p) {
       for (int h = 0; h < 2; ++h)
         w[r][h] = *(const uint4*)(at + (g + 8 * r) * 128 + (((4 * h + t) ^ ((g & 1) << 2)) << 4));
     const float sw[2] = {scales[8 * NT + (LINES == 1 ? g : 0)], scales[8 * NT + (LINES == 1 ? g + 8 : 0)]};
+    float part[NT][4], most = 0.f;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      part[i][0] = part[i][1] = part[i][2] = part[i][3] = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint4 x = *(const uint4*)(at + R::kTokens + (8 * i + g) * 128 +
                                         (((4 * h + t) ^ ((g & 1) << 2)) << 4));
         const uint4 lo = w[0][h], hi = w[1][h];
-        mma_e4m3(part, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
-        mma_e4m3(part, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+        mma_e4m3(part[i], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+        mma_e4m3(part[i], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
       }
       const float2 sx = *(const float2*)&scales[8 * i + 2 * t];
-      sum[i][0] = fmaf(part[0], sw[0] * sx.x, sum[i][0]);
-      sum[i][1] = fmaf(part[1], sw[0] * sx.y, sum[i][1]);
-      sum[i][2] = fmaf(part[2], sw[1] * sx.x, sum[i][2]);
-      sum[i][3] = fmaf(part[3], sw[1] * sx.y, sum[i][3]);
+      most = fmaxf(most, fmaxf(fabsf(sx.x), fabsf(sx.y)));
+    }
+    // (one look at the block's scales, not one for each pair of them)
+    if (most * fmaxf(fabsf(sw[0]), fabsf(sw[1])) < INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float2 sx = *(const float2*)&scales[8 * i + 2 * t];
+        sum[i][0] = fmaf(part[i][0], sw[0] * sx.x, sum[i][0]);
+        sum[i][1] = fmaf(part[i][1], sw[0] * sx.y, sum[i][1]);
+        sum[i][2] = fmaf(part[i][2], sw[1] * sx.x, sum[i][2]);
+        sum[i][3] = fmaf(part[i][3], sw[1] * sx.y, sum[i][3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float2 sx = *(const float2*)&scales[8 * i + 2 * t];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum[i][e] = add_apart(sum[i][e], part[i][e], sw[e >> 1], e & 1 ? sx.y : sx.x);
+      }
     }
     __syncwarp();
     fill(stage, block + S * W);
