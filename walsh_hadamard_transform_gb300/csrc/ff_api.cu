@@ -36,15 +36,15 @@ bool window(const void* p, int64_t rows, int64_t cols, int64_t ld, int size, Win
   return !(rows > 0 && cols > 0 && !p);
 }
 
-// Whether two matrices share a byte.  Column windows of one matrix (the same pitch,
-// disjoint columns) do not.
+// Whether two matrices share a byte.  Column windows of one matrix (the same pitch, or the
+// one row of a window that has no other; disjoint columns) do not.
 bool overlap(const Window& a, const Window& b) {
   if (!a.rows || !b.rows || !a.width || !b.width) return false;
   const uintptr_t a_end = a.p + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
   const uintptr_t b_end = b.p + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
   if (a.p >= b_end || b.p >= a_end) return false;
-  if (a.pitch != b.pitch || a.pitch == 0) return true;
-  const int64_t pitch = a.pitch;
+  const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  if ((b.rows > 1 && b.pitch != pitch) || pitch == 0 || a.width > pitch || b.width > pitch) return true;
   const int64_t d = (int64_t)((b.p >= a.p ? (b.p - a.p) % (uintptr_t)pitch
                                           : (pitch - (int64_t)((a.p - b.p) % (uintptr_t)pitch)) % pitch));
   return !(d >= a.width && d + b.width <= pitch);
