@@ -92,6 +92,23 @@ def _run(device, stream, entry, *args):
         return entry(*args, handle)
 
 
+def _error(status, what, aligned, elements=()):
+    """The error of a call.  Where a matrix does not start its rows as the call asks for, says
+    which one: ``aligned`` are those on 16-byte boundaries, ``elements`` those on their elements'."""
+    if status == _fwt.FWT_ERR_MISALIGNED:
+        for tensors, unit in ((aligned, 16), (elements, 0)):
+            for name, t in tensors:
+                size = t.element_size()
+                row = t.stride(0) * size if t.dim() == 2 and t.shape[0] > 1 else 0
+                if t.data_ptr() % (unit or size) or (unit and row % unit):
+                    what += (f": {name} starts at {t.data_ptr() % (unit or size)} bytes past a multiple "
+                             f"of {unit or size}" + (f" and its rows are {row} bytes apart" if row else "")
+                             + (f"; as a window of rows padded to a multiple of {unit // size} elements "
+                                "it would be taken" if unit else ""))
+                    return _fwt.FwtError(status, what)
+    return _fwt.FwtError(status, what)
+
+
 def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None, stream=None):
     """Rotates ``x`` (rows, cols) along ``axis`` and quantises it to 8-bit e4m3.
 
@@ -128,7 +145,8 @@ def quantize_blocks(x, rotate: int = 0, axis: int = 1, lines: int = 1, out=None,
     st = _run(device, stream, _lib.fwt_quantize_blocks, x.data_ptr(), kind, rows, cols, ld, rotate,
               axis, lines, q.data_ptr(), ld_q, scale.data_ptr(), ld_s)
     if st != _fwt.FWT_OK:
-        raise _fwt.FwtError(st, f"fwt_quantize_blocks({rows} x {cols}, axis={axis})")
+        raise _error(st, f"fwt_quantize_blocks({rows} x {cols}, axis={axis})", [("codes", q)],
+                     [("x", x), ("scale", scale)])
     return q, scale
 
 
@@ -167,7 +185,8 @@ def matmul_blocks(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None)
               b.data_ptr(), ld_b, b_scale.data_ptr(), ld_bs, lines, out.data_ptr(), kind, ld_c, m, n,
               k)
     if st != _fwt.FWT_OK:
-        raise _fwt.FwtError(st, f"fwt_matmul_blocks(m={m}, n={n}, k={k})")
+        raise _error(st, f"fwt_matmul_blocks(m={m}, n={n}, k={k})", [("a", a), ("b", b)],
+                     [("a_scale", a_scale), ("b_scale", b_scale), ("out", out)])
     return out
 
 
@@ -204,7 +223,8 @@ def gated(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
     st = _run(device, stream, _lib.fwt_gated, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g,
               w_up.data_ptr(), ld_u, out.data_ptr(), ld_h, kind, act, m, f, d)
     if st != _fwt.FWT_OK:
-        raise _fwt.FwtError(st, f"fwt_gated(m={m}, f={f}, d={d})")
+        raise _error(st, f"fwt_gated(m={m}, f={f}, d={d})",
+                     [("x", x), ("w_gate", w_gate), ("w_up", w_up)], [("out", out)])
     return out
 
 
@@ -259,7 +279,9 @@ def gated_backward(grad, x, w_gate, w_up, activation: str = "silu", out=None, wo
               w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, p_dx, ld_dx, p_dg, ld_dg, p_du, ld_du,
               kind, act, m, f, d, workspace.data_ptr(), size)
     if st != _fwt.FWT_OK:
-        raise _fwt.FwtError(st, f"fwt_gated_backward(m={m}, f={f}, d={d})")
+        raise _error(st, f"fwt_gated_backward(m={m}, f={f}, d={d})",
+                     [("grad", grad), ("x", x), ("w_gate", w_gate), ("w_up", w_up),
+                      ("workspace", workspace)])
     return dx, dw_gate, dw_up
 
 
