@@ -395,7 +395,8 @@ int fwt_plan_factors(int n, int dtype, int* bits, int max_factors);
  * (read once per process), every transform, bit-range, bit-mask and phase call
  * prints one line to stderr before it launches: the dtype, n, batch and each planned
  * pass (kind, transformed bits K, tile size, and for column passes the row stride,
- * segment width and mover).  Host-buffer calls print one line per chunk.
+ * segment width and mover).  Host-buffer calls print one line per chunk, feed-forward
+ * operators one line per kernel, with how the work is cut.
  */
 
 /*
@@ -505,7 +506,7 @@ long long fwt_get_l2_chunk_bytes(void);
 /*
  * Per-pass tracing with caller-owned CUDA events (tracing without a profiler).
  * fwt_trace_events(events, capacity) arms tracing for the calling host thread:
- * every pass launched afterwards by this thread is bracketed by two
+ * every pass and every feed-forward kernel launched afterwards by this thread is bracketed by two
  * cudaEventRecord calls on the launch stream, into events[2i] and events[2i+1]
  * (events are cudaEvent_t handles created by the caller, with timing enabled),
  * until `capacity` events are used.  capacity == 0 disarms.  fwt_trace_count()

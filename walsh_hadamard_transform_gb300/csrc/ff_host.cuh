@@ -16,6 +16,10 @@ namespace fwt {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // Whether kernels are launched with programmatic stream serialisation (fwt_set_pdl).
 int pdl_mode();
+// A line of the plan log (FWT_LOG), and the events of fwt_trace_events around a launch.
+void log_kernel(const char* format, ...) __attribute__((format(printf, 1, 2)));
+cudaError_t trace_begin(cudaStream_t stream, bool& traced);
+cudaError_t trace_end(cudaStream_t stream);
 
 namespace ff {
 
@@ -70,7 +74,10 @@ cudaError_t launch_overlapped(void (*kernel)(KArgs...), unsigned grid, unsigned 
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  bool traced;
+  cudaError_t err = trace_begin(st, traced);
+  if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return err == cudaSuccess && traced ? trace_end(st) : err;
 }
 
 // The same for kernels with dynamic shared memory, whose limit the first launch on each

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -851,6 +852,28 @@ int run_phase(const float* re_in, const float* im_in, const float* theta, int64_
 int tma_l2_promotion() { return g_tma_promotion.load(); }
 int pdl_mode() { return g_pdl.load(std::memory_order_relaxed); }
 void set_last_cuda_error(int err) { g_last_cuda_error = err; }
+
+// One line of the plan log, where it is on.
+void log_kernel(const char* format, ...) {
+  if (!log_plans()) return;
+  char line[512];
+  va_list args;
+  va_start(args, format);
+  vsnprintf(line, sizeof line, format, args);
+  va_end(args);
+  fprintf(stderr, "fwt: %s\n", line);
+}
+
+// The events around one launch, while the thread has some left.
+cudaError_t trace_begin(cudaStream_t stream, bool& traced) {
+  traced = g_trace_count + 2 <= g_trace_capacity;
+  return traced ? cudaEventRecord((cudaEvent_t)g_trace_events[g_trace_count], stream) : cudaSuccess;
+}
+cudaError_t trace_end(cudaStream_t stream) {
+  const cudaError_t err = cudaEventRecord((cudaEvent_t)g_trace_events[g_trace_count + 1], stream);
+  g_trace_count += 2;
+  return err;
+}
 
 bool tensor_map_2d(CUtensorMap* out, CUtensorMapDataType dt, void* base, const cuuint64_t dims[2],
                    cuuint64_t row_stride_bytes, const cuuint32_t box[2], int l2_promotion) {

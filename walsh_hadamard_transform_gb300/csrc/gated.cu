@@ -561,6 +561,10 @@ cudaError_t launch_config(const GemmMaps& maps, const GemmParams& p, cudaStream_
   if (tiles > 0x7fffff00 / SPLIT) return cudaErrorInvalidConfiguration;
   const int64_t grid =
       SPLIT > 1 ? tiles * SPLIT : std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
+  constexpr const char* kMode[] = {"gated", "gated gradients", "gated dx", "gated dw"};
+  log_kernel("%s %s rows=%d cols=%d stages=%lld | tiles %dx%d split=%d", kMode[MODE],
+             std::is_same<T, __half>::value ? "f16" : "bf16", p.m, p.n, (long long)p.k_blocks * p.phases,
+             128 * CG, BN, SPLIT);
   return launch_cluster(gemm_kernel<T, MODE, CG, BN, SPLIT>, ready, (unsigned)grid, kThreads,
                         Config<CG, BN>::kSmem, CG * SPLIT, st, maps, p);
 }
@@ -690,6 +694,7 @@ cudaError_t launch_gated_bounds(CMat grad, CMat x, CMat w_gate, CMat w_up, Bound
   const int64_t rows = (int64_t)m + f, most = std::min(kMostBounds, 3 * multiprocessors());
   bounds.parts = (int)std::min<int64_t>(most, (rows + kBoundWarps - 1) / kBoundWarps);
   const BoundParams p{grad, x, w_gate, w_up, (float2*)bounds.pairs, m, f, d};
+  log_kernel("gated bounds f16 m=%d f=%d d=%d", m, f, d);
   return launch_overlapped(bounds_kernel, (unsigned)bounds.parts, kBoundWarps * 32, 0, 1, st, p);
 }
 

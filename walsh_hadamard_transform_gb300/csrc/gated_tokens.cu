@@ -309,7 +309,9 @@ __global__ void __launch_bounds__(kDwWarps * 32) token_dw_kernel(const TokenGrad
 template <typename T, int TM>
 cudaError_t launch_gradients(TokenGradientParams p, Mat dx, Mat dw_gate, Mat dw_up, cudaStream_t st) {
   cudaError_t err = cudaSuccess;
+  constexpr const char* kType = std::is_same<T, __half>::value ? "f16" : "bf16";
   if (dx.p) {
+    log_kernel("gated dx %s m=%d f=%d d=%d | tokens=%d", kType, p.m, p.f, p.d, TM);
     p.out[0] = dx.p, p.ld_out[0] = dx.ld;
     err = launch_overlapped(token_dx_kernel<T, TM>, (unsigned)((p.d + 63) / 64) * kDxCluster,
                             kDxWarps * 32, 0, kDxCluster, st, p);
@@ -321,6 +323,7 @@ cudaError_t launch_gradients(TokenGradientParams p, Mat dx, Mat dw_gate, Mat dw_
       p.out[s] = out[s].p, p.ld_out[s] = out[s].ld;
       p.vec &= ((uintptr_t)out[s].p & 15u) == 0 && out[s].ld % 8 == 0;
     }
+    log_kernel("gated dw %s m=%d f=%d d=%d | tokens=%d", kType, p.m, p.f, p.d, TM);
     const int strips = (p.d + 255) / 256, lines = kDwWarps * kDwLines;
     const int64_t grid = (int64_t)strips * ((p.f + lines - 1) / lines);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -331,6 +334,8 @@ cudaError_t launch_gradients(TokenGradientParams p, Mat dx, Mat dw_gate, Mat dw_
 
 template <typename T, int NT, int U, bool GRADIENTS = false>
 cudaError_t launch(const GatedTokenParams& p, cudaStream_t st) {
+  log_kernel("gated%s %s m=%d f=%d d=%d | tokens=%d", GRADIENTS ? " gradients" : "",
+             std::is_same<T, __half>::value ? "f16" : "bf16", p.m, p.f, (int)(p.bytes / 2), 8 * NT);
   return launch_overlapped(gated_tokens_kernel<T, NT, U, GRADIENTS>, (unsigned)((p.f + 15) / 16),
                            kTokenWarps * 32, 0, 1, st, p);
 }

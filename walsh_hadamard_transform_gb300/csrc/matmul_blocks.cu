@@ -567,6 +567,8 @@ cudaError_t launch_config(const BlocksMaps& maps, BlocksParams p, cudaStream_t s
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > 0x7fffff00 / SPLIT) return cudaErrorInvalidConfiguration;
   const int64_t grid = SPLIT > 1 ? tiles * SPLIT : std::min<int64_t>(tiles, multiprocessors() / CG) * CG;
+  log_kernel("matmul_blocks m=%d n=%d k=%d scale_lines=%d | tiles %dx%d rows=%d split=%d", p.m, p.n, p.k,
+             LINES, 128 * CG, BN, ROWS, SPLIT);
   return launch_cluster(blocks_kernel<CG, BN, LINES, ROWS, SPLIT>, ready, (unsigned)grid, kThreads,
                         Config<CG, BN, LINES, ROWS, SPLIT>::kSmem, CG * SPLIT, st, maps, p);
 }

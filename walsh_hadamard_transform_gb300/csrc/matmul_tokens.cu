@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(W * 32) tokens_kernel(const TokenParams p) {
 template <int NT, int W, int S, int LINES>
 cudaError_t launch(const TokenParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
+  log_kernel("matmul_blocks m=%d n=%d k=%d scale_lines=%d | tokens=%d warps=%d", p.m, p.n, p.k, LINES,
+             8 * NT, W);
   return launch_cluster(tokens_kernel<NT, W, S, LINES>, ready, (unsigned)((p.n + 15) / 16), W * 32,
                         Ring<NT, W, S>::kBytes, 1, st, p);
 }

@@ -528,6 +528,8 @@ cudaError_t launch(QuantizeParams p, cudaStream_t st) {
   p.rounds = (int)std::max<int64_t>(1, std::min<int64_t>(4, across * steps / (8 * multiprocessors())));
   const int64_t grid = (steps + p.rounds - 1) / p.rounds * across;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  log_kernel("quantize_blocks lines=%d length=%d rotate=%d axis=%d scale_lines=%d | %d bits%s rounds=%d",
+             p.nl, p.length, p.r, AXIS, LINES, (int)sizeof(T) * 8, STAGED ? " staged" : "", p.rounds);
   if constexpr (STAGED) {
     static std::atomic<uint64_t> ready{0};
     return launch_cluster(quantize_kernel<T, AXIS, LINES, true>, ready, (unsigned)grid, W * 32,
