@@ -37,14 +37,15 @@ inline bool swizzled_map(CUtensorMap* out, const void* p, int bytes, CUtensorMap
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Multiprocessors of the current device, asked once for each device.
+// Multiprocessors of the current device, asked once for each device; at least two, as many as a pair
+// of CTAs takes (also where no device answers: the launch then says so).
 inline int multiprocessors() {
   static std::atomic<int> known[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 2;
   int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
   if (!n) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) return 2;
     if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   }
   return n;
