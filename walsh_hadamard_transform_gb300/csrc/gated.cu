@@ -19,10 +19,11 @@
 // shared-memory traffic of the second.
 //
 // Bound, large: the tensor cores under the power limit.  8192 x 4096 x 8192 bf16 forward: 513
-// to 615 us by the values' spread and the GPU, 1790 to 2140 TFLOP/s, the tensor pipe active
-// 92% of the cycles; 8192 x 2048 x 8192 backward: 0.90 to 1.07 ms, 1540 to 1830 TFLOP/s.
+// to 530 us in bursts, 599 for seconds on end (1545 MHz), 2140 to 1840 TFLOP/s, the tensor pipe active
+// 92% of the cycles; 8192 x 2048 x 8192 backward: 0.92 and 1.04 ms (1530 MHz), 1800 and 1590 TFLOP/s.
 // Small: latency, some 3 us from launch to the last store and 0.2 to 0.3 us a stage; 333 x
-// 1008 x 2736 forward 7.1 us, 517 x 1008 x 2736 backward 38 us in three launches.
+// 1001 x 2731 forward 7.5 us, 517 x 1001 x 2731 backward 41 us in three launches, 50 us in
+// float16 with the bounds' before them.  64 x 2048 x 8192 backward: 64 us, float16 84.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

@@ -1,13 +1,15 @@
 // Gated projections of a few tokens: see tokens.cuh for the scheme.  A CTA owns 16 lines of
 // both weights; its warps take stretches of 64 elements of the contraction in turn, and the
 // join applies the activation.  Bound: HBM (the bytes of both weights): one token by
-// 2 x 8192 x 4096 23.0 us, 5.8 TB/s.
+// 2 x 8192 x 4096 24.6 us, 5.5 TB/s (23.8 with loads of the read-only path, which asks for weights
+// that no kernel before writes).
 //
 // Their gradients for up to 8 tokens, three kernels: the same products again with dg and du
 // left in fp32, a line of the weights after the other (8 tokens side by side); dx, which reads
 // both weights once more, in strips of 64 columns that a cluster shares out along f; dw_gate
 // and dw_up, up to eight multiply-adds an element, bound by writing them.  One token, 8192 x
-// 2048: 48 us in three launches (the bytes' floor is 30); eight 73, by the latency of dx.
+// 2048: 47 us in three launches (the bytes' floor is 20, 30 with the weights read twice as here);
+// eight 64, by the latency of dx.
 #include <cstdint>
 #include <type_traits>
 

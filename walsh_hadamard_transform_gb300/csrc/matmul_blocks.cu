@@ -12,16 +12,17 @@
 // two to a quarter of its rows: a tile of 256 columns costs them 128 values a thread and block.
 // Large products pair two CTAs on a tile of 256 x 256.
 //
-// Bound, large: those sums.  8192 x 8192 x 4096: 191 to 197 us, 2800 TFLOP/s; the tensor pipe
-// is active 53% of the cycles.  A block's products take 512 clocks and its sums some 800, in
+// Bound, large: the latency of those sums.  8192 x 8192 x 4096: 194 us in bursts, 2830 TFLOP/s, and
+// 218 us for seconds on end (1755 MHz under the power limit); the tensor pipe is active 50 to 53%
+// of the cycles, the issue slots 42%.  A block's products take 512 clocks and its sums some 800, in
 // which a warp mostly waits: without the additions, or without the reads of tensor memory, the
 // same kernel takes 167 us, without both and the stores 143.  Tried and slower: packed pairs of
 // multiply-adds (628 clocks a block against 327 for the sums alone: half the rate, and tensor
 // memory's registers had to be moved into pairs), 64 columns a warp and sixteen warps (216 us:
 // the steps around the sums then fill the issue slots), the next block's reads begun before the
 // last sums (225 us), the next wait asked ahead (219 us).  With a scale for every line of b
-// each sum takes two operations: 4096 x 8192 x 4096 in 166 us.
-// Small: latency, some 3 us and 0.25 us a block; 48 x 8192 x 4096 11.0 us (3.1 TB/s).
+// each sum takes two operations: 4096 x 8192 x 4096 in 155 us.
+// Small: latency, some 3 us and 0.25 us a block; 48 x 8192 x 4096 11.6 us (3.0 TB/s).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

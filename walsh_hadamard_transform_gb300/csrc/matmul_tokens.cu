@@ -6,8 +6,8 @@
 // Each warp has a ring of its own in shared memory that asynchronous copies fill: the bytes on
 // their way then cost no registers, and an SM holds enough of them.  (Loading straight to
 // registers measured 12.6 us for one token by 4096 x 8192: 163 registers a thread left one
-// CTA an SM, and two waves.)  One token by 4096 x 8192: 8.5 us, 3.9 TB/s, of which some 1.5 are
-// the launch; 16 tokens 10.6 us.
+// CTA an SM, and two waves.)  One token by 4096 x 8192: 8.75 us, 3.8 TB/s, of which some 1.5 are
+// the launch; 16 tokens 11.1 us.
 #include <atomic>
 #include <cstdint>
 

@@ -18,9 +18,11 @@
 // block crosses lanes (two shuffles a line, where butterflies across lanes would take four
 // shuffles an element and be bound by them).
 //
-// Bound: HBM by its bytes, issue and the latency of dependent instructions as it stands (52% of
-// the issue slots, 12 to 16 warps an SM): 8192 x 8192 bf16 in 39.4 us along the columns and 36.7
-// down the rows, 5.1 and 5.5 TB/s; one line of 8192 2.1 us, the launch.
+// Bound: HBM by its bytes, issue and the latency of dependent instructions as it stands (48% of
+// the issue slots, 12 to 16 warps an SM): 8192 x 8192 bf16 in 39.5 us along the columns and 36.5
+// down the rows, 5.1 and 5.5 TB/s, with 128 lines to a scale 39 and 40.4; one line of 8192 2.0 us,
+// the launch.  fp32 (eight warps an SM, no block ahead): 90 and 125 us, with 128 lines 98 and 118,
+// 2.7 to 3.7 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

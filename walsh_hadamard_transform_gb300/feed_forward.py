@@ -12,7 +12,8 @@ contiguous (stride 1 along the columns) and may be a window of a larger matrix;
 operands of products start every row on a 16-byte boundary.  Outputs made here have
 such rows too (padded where the width asks for it).  Every call runs on ``stream``
 (default: the current PyTorch stream) and does not synchronise; what it allocates belongs
-to that stream, as under ``torch.cuda.stream``.
+to that stream, as under ``torch.cuda.stream``.  A kernel whose waits give up leaves its output
+unwritten: ``device_status()``, which synchronises, tells.
 """
 from __future__ import annotations
 
