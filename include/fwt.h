@@ -367,6 +367,101 @@ int fwt_gated_backward(const void* grad, int64_t ld_grad, const void* x, int64_t
 size_t fwt_gated_backward_workspace_bytes(int64_t m, int64_t f);
 size_t fwt_gated_backward_workspace_bytes_for(int type, int64_t m, int64_t f);
 
+/*
+ * Keys and values of attention, rotated and held in 8 bits in pages: written as tokens come, read
+ * back, and attended to.
+ *
+ * The rotation spreads the few large channels of keys over their group before the codes are cut;
+ * q . k stays as it is when both are rotated, and an output of rotated values is turned back once.
+ *
+ * A page holds page_tokens tokens of every head: codes e4m3 as heads x page_tokens x dim bytes, and
+ * a scale for each token and head, heads x page_tokens bytes in e8m0 (byte b is 2^(b-127), 255 NaN).
+ * page_tokens is a multiple of 16; dim 64 or 128; pages lie *_stride bytes apart (at least a
+ * page; multiples of 16), so a cache may be the window of a pool that holds several layers, or keys and
+ * values side by side.  Arrays start on 16-byte boundaries.
+ */
+typedef struct fwt_cache {
+  void *k, *v;             /* codes */
+  void *k_scale, *v_scale; /* scales */
+  int64_t k_stride, v_stride, k_scale_stride, v_scale_stride;
+  int64_t pages;
+  int heads, page_tokens, dim;
+} fwt_cache;
+
+/*
+ * The sequences of a call, in DEVICE memory.  Row b of `table` (ld_table ints apart) names the pages
+ * of sequence b in the order of its tokens, most_pages at most; lengths[b] tokens of it are in the
+ * cache, those that the call writes among them.  Rows starts[b] .. starts[b+1] - 1 of the packed
+ * (tokens, heads, dim) operands are its last ones: with n = starts[b+1] - starts[b], row
+ * starts[b] + i is the token at position lengths[b] - n + i, in page table[b][position / page_tokens].
+ *
+ * The host reads none of it.  `starts` rises from 0 to at most `tokens`; rows behind starts[sequences]
+ * belong to no sequence: they are not read, and rows of outputs there not written.  What could point
+ * outside is taken as it would be nearest: starts beyond `tokens` as `tokens`, lengths below 0
+ * as 0 and beyond the table as the table's room; a page below 0 or not below `pages` holds no tokens,
+ * and nor do positions below 0.
+ */
+typedef struct fwt_sequences {
+  const int32_t* table;
+  int64_t ld_table, most_pages;
+  const int32_t *starts, *lengths;
+  int64_t sequences;
+} fwt_sequences;
+
+/*
+ * Writes k and v (tokens, heads, dim) of `type` into the cache.  Element [t][h][d] of k is at
+ * k + t * k_token + h * k_head + d; rows start on 16-byte boundaries.  Each aligned group of
+ * 2^rot_bits elements of a head (0 .. 6 for dim 64, 0 .. 7 for 128) becomes
+ * 2^(-rot_bits/2) H times itself, in fp32; then
+ *
+ *     s = the least 2^e, e >= -126, with max |y| <= 448 s,   code = e4m3(y / s)  (to nearest even).
+ *
+ * A power of two: it costs a floating-point code nothing, and multiplies without a rounding.  A row
+ * that holds an Inf or NaN, or overflows in the rotation, gets a NaN scale and codes of zero.  Tokens
+ * without a place (see fwt_sequences) are left out.  Two tokens of one call at the same place (a page
+ * that two sequences write to) leave either, or some of both.
+ */
+int fwt_cache_append(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                     int64_t v_head, int type, int64_t tokens, const fwt_cache* cache,
+                     const fwt_sequences* sequences, int rot_bits, fwt_stream_t stream);
+
+/*
+ * The last tokens of each sequence out of the cache, scaled and turned back, into k and v (tokens,
+ * heads, dim) of `type`: sums of codes in fp32, one rounding.  Rows without a place are zero.
+ */
+int fwt_cache_read(const fwt_cache* cache, const fwt_sequences* sequences, int rot_bits, void* k,
+                   int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, int type,
+                   int64_t tokens, fwt_stream_t stream);
+
+/*
+ * Attention of the last tokens of each sequence (its new ones, already in the cache) to all of it:
+ *
+ *     out[t][h] = R sum_j softmax_j(scale (R q[t][h]) . K[j][h']) V[j][h'],  h' = h / (q_heads / heads),
+ *
+ * R the rotation, K and V the cache's codes times their scales, over the positions j that the token
+ * at position i sees: 0 <= j < length; with `causal` j <= i; with window > 0 j > i - window.  A token
+ * that sees none gets zeros.  q and out: (tokens, q_heads, dim) of `type` (FWT_BF16 or FWT_F16), q_heads
+ * a multiple of the cache's heads.  A key or value whose scale is NaN makes NaN whatever sees
+ * it, and nothing else; codes of NaN, which fwt_cache_append does not write, may make NaN any row of
+ * the sequence and head.
+ *
+ * Scores, softmax and sums are fp32.  Queries after the rotation, and p = 2^(score - maximum), are
+ * rounded to float16 (tensor-core operands; half a unit is 2^-11), both held at powers of two that
+ * keep them in its range; codes become float16 exactly.
+ *
+ * longest: the most new tokens of any sequence, as far as the host knows (0: as if all had the
+ * same); it chooses between kernels and sizes the workspace, and a wrong one costs only time.
+ * workspace: DEVICE memory, 16-byte aligned, of at least fwt_cache_attention_workspace_bytes(q_heads, heads, dim,
+ * longest) bytes, for longest = 0 that of ceil(tokens / sequences); calls that may run at the same time
+ * need one each.
+ */
+int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* out, int64_t out_token,
+                        int64_t out_head, int type, int64_t tokens, int q_heads, const fwt_cache* cache,
+                        const fwt_sequences* sequences, int rot_bits, float scale, int causal,
+                        int64_t window, int64_t longest, void* workspace, size_t workspace_bytes,
+                        fwt_stream_t stream);
+size_t fwt_cache_attention_workspace_bytes(int q_heads, int heads, int dim, int64_t longest);
+
 /* Static text for a status code (never NULL). */
 const char* fwt_status_string(int status);
 

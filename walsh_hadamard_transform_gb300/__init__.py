@@ -9,8 +9,10 @@ pointers and marshal arguments only; every step of the transform runs in the
 CUDA kernels of ``libfwt_gb300.so``.  ``transform`` is the tensor-level wrapper:
 it checks dtypes, devices and contiguity, then calls the C ABI on the current
 PyTorch stream.  ``quantize_blocks``, ``matmul_blocks``, ``gated`` and
-``gated_backward`` (``feed_forward.py``) are the feed-forward operators.  There is no CPU fallback: without the compiled library (see
-``build.py``) every call raises.
+``gated_backward`` (``feed_forward.py``) are the feed-forward operators; ``new_cache``,
+``cache_append``, ``cache_read`` and ``cache_attention`` (``cache.py``) hold keys and values in 8 bits
+and attend to them.  There is no CPU fallback: without the compiled library (see ``build.py``) every
+call raises.
 """
 from __future__ import annotations
 
@@ -137,6 +139,8 @@ def library() -> ctypes.CDLL:
         lib.fwt_gated_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.fwt_gated_backward_workspace_bytes_for.argtypes = [ci, i64, i64]
         lib.fwt_gated_backward_workspace_bytes_for.restype = ctypes.c_size_t
+        from . import cache
+        cache.declare(lib)
         _lib = lib
     return _lib
 
@@ -603,3 +607,5 @@ def transform_host(re, im=None, out_re=None, out_im=None, normalize: bool = True
 
 from .feed_forward import (fwt_gated_backward_workspace_bytes, gated, gated_backward,  # noqa: E402,F401
                            matmul_blocks, quantize_blocks)
+from .cache import (Cache, cache_append, cache_attention, cache_read,  # noqa: E402,F401
+                    fwt_cache_attention_workspace_bytes, new_cache)

@@ -1,0 +1,489 @@
+// Attention of few rows (new tokens x query heads of a key head) over the 8-bit cache: decoding,
+// drafts, any call whose rows do not fill a tensor-memory tile.
+//
+//   S^T = K Q^T   keys are the 16 lines of a 16 x 8 product, rows its 8 columns
+//   p = 2^(s - m), m a running maximum; l = sum of p
+//   O^T += V^T P^T   the head dimension is the lines, the contraction runs over keys
+//
+// Bound: HBM, every byte of the cache seen once.  A warp takes 32 tokens at a time through a ring of its
+// own in shared memory that asynchronous copies fill, and reads the codes straight into the
+// fragments of both products: which elements of a contraction meet in which slot is free as long as
+// both operands agree, so a thread takes 16 consecutive bytes of a key, and of two values that are
+// neighbours in P one byte each side by side.  Codes become float16 without a rounding; the
+// scales of keys multiply scores, those of values multiply p.  P is rounded to float16 as
+// p * 2^(15 + e - e_max), at most 2^15, e the scale's exponent and e_max the largest so far: half a
+// unit in 2^-11, down to 2^-29 of the largest possible.  Queries are rounded to float16 once after
+// their rotation, each row at a power of two that takes its largest to 2^14.
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attention_plan.cuh"
+#include "cache.cuh"
+#include "feed_forward.cuh"
+#include "ff_host.cuh"
+#include "tma.cuh"
+
+namespace fwt {
+namespace ff {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kStep = 32;   // tokens that a warp takes at a time
+constexpr int kUnit = 128;  // tokens of a unit of the plan
+
+// NT: groups of 8 rows.
+template <int DIM, int NT>
+struct Layout {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kValues = kStep * DIM, kKeyScales = 2 * kValues, kValueScales = kKeyScales + kStep;
+  static constexpr int kStage = kValueScales + kStep;
+  static constexpr int kStages = DIM == 128 ? 3 : 6;
+  static constexpr int kRing = kStages * kStage;         // of a warp
+  static constexpr int kPitchQ = DIM * 2 + 16;           // bytes of a query row
+  static constexpr int kPitchSum = DIM + 4;              // floats of a row of sums
+  static constexpr int kQueries = kWarps * kRing;
+  static constexpr int kSums = kQueries + kRows * kPitchQ;
+  static constexpr int kBytes = kSums + kRows * kPitchSum * 4;
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^e in two factors, for -252 <= e <= 254.
+__device__ __forceinline__ float times_power(float v, int e) {
+  const int half = e >> 1;
+  return v * __uint_as_float((uint32_t)(127 + half) << 23) * __uint_as_float((uint32_t)(127 + e - half) << 23);
+}
+
+// Rows of codes in a stage: 16-byte pieces in an order by row, so that the fragments' reads meet all
+// banks (rows 2 c of values, half rows of keys).
+template <int DIM>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+  return row * DIM + ((piece ^ (DIM == 128 ? row & 6 : (row >> 1) & 3)) << 4);
+}
+
+template <int DIM, int NT>
+__global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const AttentionParams p) {
+  using L = Layout<DIM, NT>;
+  constexpr int kRows = L::kRows, kTiles = DIM / 16;
+  extern __shared__ __align__(16) uint8_t memory[];
+  __shared__ PlanScratch<kThreads> scratch;
+  __shared__ float row_scale[kRows];
+  __shared__ float tops[kWarps][kRows], totals[kWarps][kRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const uint8_t* ring = memory + warp * L::kRing;
+  const uint32_t ring_at = smem_u32(ring);
+  uint8_t* queries = memory + L::kQueries;
+  float* sums = (float*)(memory + L::kSums);
+  const CacheView& cache = p.cache;
+  pdl_begin();
+
+  Walk walk = find_share<kRows, kUnit>(p, blockIdx.x, gridDim.x, scratch);
+  if (walk.left == 0) {
+    if (threadIdx.x == 0) p.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+
+  // The warp's copies run ahead of its work, over items as well.
+  Walk ahead = walk;
+  int next = warp * kStep;  // of the present piece of `ahead`, in tokens
+  uint32_t present = 0;     // two bits a stage in flight: whether its halves have a page
+  int pages = -1;           // lanes 0 and 1: the pages of the next step's halves
+  auto settle = [&] {       // to a piece with a step for this warp, and its pages
+    while (ahead.left > 0) {
+      const int from = ahead.keys.low + ahead.unit * kUnit;
+      const int to = min(from + piece_units(ahead) * kUnit, ahead.keys.high);
+      if (from + next < to) {
+        const int pos = from + next + 16 * (lane & 1);
+        pages = pos < to ? page_of(cache, p.at, ahead.b, pos) : -1;
+        return;
+      }
+      next_piece<kRows, kUnit>(p, ahead);
+      next = warp * kStep;
+    }
+  };
+  auto fill = [&](int stage) {
+    uint32_t bits = 0;
+    if (ahead.left > 0) {
+      const int from = ahead.keys.low + ahead.unit * kUnit;
+      const int to = min(from + piece_units(ahead) * kUnit, ahead.keys.high);
+      const int pos = from + next;
+      const uint32_t at = ring_at + stage * L::kStage;
+      constexpr int kPieces = DIM / 16, kRowsAtOnce = 32 / kPieces;
+      const int piece = lane & (kPieces - 1), row0 = lane / kPieces;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int page = __shfl_sync(~0u, pages, half);
+        if (page >= 0) bits |= 1u << half;
+        const int64_t token = (int64_t)ahead.head * cache.page_tokens + (pos + 16 * half) % cache.page_tokens;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const uint8_t* codes = cache.codes[o] + page * cache.code_stride[o] + token * DIM + 16 * piece;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+            const int row = i * kRowsAtOnce + row0;
+            const bool there = page >= 0 && pos + 16 * half + row < to;
+            copy16(at + (o ? L::kValues : 0) + piece_at<DIM>(16 * half + row, piece),
+                   there ? (const void*)(codes + row * DIM) : p.parts, there);
+          }
+          if (lane == o)
+            copy16(at + (o ? L::kValueScales : L::kKeyScales) + 16 * half,
+                   page >= 0 ? (const void*)(cache.scales[o] + page * cache.scale_stride[o] + token) : p.parts,
+                   page >= 0);
+        }
+      }
+      next += kWarps * kStep;
+      settle();
+    }
+    present |= bits << (2 * (L::kStages - 1));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  settle();
+#pragma unroll
+  for (int s = 0; s < L::kStages; ++s) {
+    if (s) present >>= 2;
+    fill(s);
+  }
+
+  int stage = 0, flags = 0;
+  int4 note = make_int4(0, 0, 0, 0);
+  for (bool first_piece = true; walk.left > 0; first_piece = false) {
+    const int piece = piece_units(walk);
+    const bool starts = walk.unit == 0, ends = walk.unit + piece == walk.units;
+    const int from = walk.keys.low + walk.unit * kUnit;
+    const int to = min(from + piece * kUnit, walk.keys.high);
+    const int row0 = walk.block * kRows;  // of the sequence's rows with this head
+    const int rows = (int)min((int64_t)kRows, (int64_t)walk.s.count * p.group - row0);
+
+    // queries: rotated, a power of two for each row, float16
+    for (int r = warp; r < kRows; r += kWarps) {
+      constexpr int kOwn = DIM / 32;
+      float v[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) v[i] = 0.f;
+      if (r < rows) {
+        const int token = walk.s.row + (row0 + r) / p.group;
+        const int head = walk.head * p.group + (row0 + r) % p.group;
+        const uint32_t* q = (const uint32_t*)((const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + kOwn * lane);
+#pragma unroll
+        for (int i = 0; i < kOwn / 2; ++i) {
+          const float2 f = pair_to_float(q[i], p.type);
+          v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+      }
+      turn_row<DIM>(v, p.rot_bits, lane);
+      const float norm = rotation_norm(p.rot_bits);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        v[i] *= norm;
+        top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+      }
+      top = __reduce_max_sync(~0u, top);
+      const int e = max((int)(top >> 23), 27);  // (zero, and what is nearly so)
+      const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
+      uint32_t* to_q = (uint32_t*)(queries + r * L::kPitchQ) + kOwn / 2 * lane;
+#pragma unroll
+      for (int i = 0; i < kOwn / 2; ++i) to_q[i] = pair_from_float<__half>(v[2 * i] * up, v[2 * i + 1] * up);
+      if (lane == 0) row_scale[r] = p.scale * __uint_as_float((uint32_t)(e - 14) << 23);
+    }
+    __syncthreads();
+    uint32_t q[NT][DIM / 64][8];  // 16 consecutive elements of a row from 64 j + 16 c on
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < DIM / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 w = *(const uint4*)(queries + (8 * n + g) * L::kPitchQ + 128 * j + 32 * c + 16 * i);
+          q[n][j][4 * i] = w.x, q[n][j][4 * i + 1] = w.y, q[n][j][4 * i + 2] = w.z, q[n][j][4 * i + 3] = w.w;
+        }
+    float scale[NT][2], top[NT][2], total[NT][2];
+    Keys seen[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * c + e;
+        scale[n][e] = row_scale[r];
+        seen[n][e] = r < rows ? seen_by(p, walk.s, row0 + r) : Keys{0, 0};
+        top[n][e] = -INFINITY, total[n][e] = 0.f;
+      }
+    float o[kTiles][NT][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    int most = 0;  // the largest scale byte of the values so far
+
+    for (int pos = from + warp * kStep; pos < to; pos += kWarps * kStep) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
+      __syncwarp();
+      const uint8_t* at = ring + stage * L::kStage;
+      const uint32_t here = present & 3u;
+      float s[2][NT][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+        // (halves in the other order for odd rows: their pieces then lie in other banks)
+        uint4 k[2][DIM / 64];
+#pragma unroll
+        for (int j = 0; j < DIM / 64; ++j) {
+          const int half = DIM == 128 ? j ^ (g & 1) : j;
+          k[0][j] = *(const uint4*)(at + piece_at<DIM>(16 * t + g, 4 * half + c));
+          k[1][j] = *(const uint4*)(at + piece_at<DIM>(16 * t + g + 8, 4 * half + c));
+        }
+        if (DIM == 128 && (g & 1)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint4 w = k[r][0];
+            k[r][0] = k[r][DIM / 64 - 1], k[r][DIM / 64 - 1] = w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < DIM / 64; ++j) {
+          const uint32_t lo[4] = {k[0][j].x, k[0][j].y, k[0][j].z, k[0][j].w};
+          const uint32_t hi[4] = {k[1][j].x, k[1][j].y, k[1][j].z, k[1][j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = e4m3_to_f16x2(lo[i]), a2 = e4m3_to_f16x2(lo[i] >> 16);
+            const uint32_t a1 = e4m3_to_f16x2(hi[i]), a3 = e4m3_to_f16x2(hi[i] >> 16);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(s[t][n], a0, a1, a2, a3, q[n][j][2 * i], q[n][j][2 * i + 1]);
+          }
+        }
+      }
+      // this thread's tokens: pos + 16 t + 8 h + g
+      float key_scale[2][2];
+      int value_byte[2][2], largest = 0;
+      bool there[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int token = 16 * t + 8 * h + g;
+          there[t][h] = (here >> t & 1u) && pos + token < to;
+          key_scale[t][h] = scale_value(at[L::kKeyScales + token]);
+          value_byte[t][h] = there[t][h] ? at[L::kValueScales + token] : 0;
+          // (a value that is not a number: so is the score, for whoever sees it)
+          if (value_byte[t][h] == 255) key_scale[t][h] = scale_value(255), value_byte[t][h] = 0;
+          largest = max(largest, value_byte[t][h]);
+        }
+      largest = (int)__reduce_max_sync(~0u, (unsigned)largest);
+      bool moved = largest > most;
+      const float less = moved ? __uint_as_float((uint32_t)max(127 + most - largest, 0) << 23) : 1.f;
+      most = max(most, largest);
+      float keep[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int token = pos + 16 * t + 8 * h + g;
+              float& v = s[t][n][2 * h + e];
+              v = there[t][h] && token >= seen[n][e].low && token < seen[n][e].high
+                      ? v * scale[n][e] * key_scale[t][h]
+                      : -INFINITY;
+              x = fmaxf(x, v);
+            }
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+          x = fmaxf(x, top[n][e]);
+          const float base = x == -INFINITY ? 0.f : x;
+          keep[n][e] = exp2_fast(top[n][e] - base);
+          moved |= x > top[n][e];
+          top[n][e] = x;
+          total[n][e] *= keep[n][e];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& v = s[t][n][2 * h + e];
+              v = exp2_fast(v - base);
+              total[n][e] += v;
+            }
+        }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][n][e] *= keep[n][e & 1] * less;
+      }
+      // p with the values' scales, as the second product's columns
+      uint32_t b[2][NT][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = __uint_as_float((uint32_t)max(127 + 15 + value_byte[t][h] - most, 0) << 23);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            b[t][n][h] = transpose8x8(pair_from_float<__half>(s[t][n][2 * h] * f, s[t][n][2 * h + 1] * f));
+        }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t v[4][DIM / 32];  // tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9: DIM / 8 bytes from DIM / 8 g on
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * t + 2 * c + (i & 1) + 8 * (i >> 1);
+          const uint8_t* values = at + L::kValues;
+          if constexpr (DIM == 128) {
+            const uint4 w = *(const uint4*)(values + piece_at<DIM>(row, g));
+            v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
+          } else {
+            const uint2 w = *(const uint2*)(values + piece_at<DIM>(row, g >> 1) + 8 * (g & 1));
+            v[i][0] = w.x, v[i][1] = w.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          const uint32_t pick = i & 1 ? 0x7362u : 0x5140u;
+          const uint32_t w0 = __byte_perm(v[0][i / 2], v[1][i / 2], pick);
+          const uint32_t w1 = __byte_perm(v[2][i / 2], v[3][i / 2], pick);
+          const uint32_t a0 = e4m3_to_f16x2(w0), a1 = e4m3_to_f16x2(w0 >> 16);
+          const uint32_t a2 = e4m3_to_f16x2(w1), a3 = e4m3_to_f16x2(w1 >> 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(o[i][n], a0, a1, a2, a3, b[t][n][0], b[t][n][1]);
+        }
+      }
+      __syncwarp();
+      present >>= 2;
+      fill(stage);
+      if (++stage == L::kStages) stage = 0;
+    }
+
+    // the warps' sums together, one after the other
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = total[n][e];
+        l += __shfl_xor_sync(~0u, l, 4);
+        l += __shfl_xor_sync(~0u, l, 8);
+        l += __shfl_xor_sync(~0u, l, 16);
+        if (g == 0) tops[warp][8 * n + 2 * c + e] = top[n][e], totals[warp][8 * n + 2 * c + e] = l;
+      }
+    __syncthreads();
+    float weight[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[w][8 * n + 2 * c + e]);
+        weight[n][e] = m == -INFINITY ? (total[n][e] == total[n][e] ? 0.f : 1.f) : exp2_fast(top[n][e] - m);
+      }
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float* sum = sums + (8 * n + 2 * c + (e & 1)) * L::kPitchSum + DIM / 8 * g + 2 * i + (e >> 1);
+              const float v = times_power(o[i][n][e] * weight[n][e & 1], most - 142);
+              *sum = w ? *sum + v : v;
+            }
+      }
+      __syncthreads();
+    }
+
+    // out: the item's rows, or a part of them for launch_attention_join
+    const bool whole = starts && ends;
+    float* part = p.parts + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * part_floats(kRows, DIM);
+    for (int r = warp; r < rows; r += kWarps) {
+      constexpr int kOwn = DIM / 32;
+      float m = -INFINITY, l = 0.f, v[kOwn];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        l += totals[w][r] * (m == -INFINITY ? 1.f : exp2_fast(tops[w][r] - m));
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) v[i] = sums[r * L::kPitchSum + kOwn * lane + i];
+      if (whole) {
+        const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
+        turn_row<DIM>(v, p.rot_bits, lane);
+        const int token = walk.s.row + (row0 + r) / p.group;
+        const int head = walk.head * p.group + (row0 + r) % p.group;
+        uint32_t* to_out = (uint32_t*)((uint16_t*)p.out.p + token * p.out.token + head * p.out.head + kOwn * lane);
+#pragma unroll
+        for (int i = 0; i < kOwn / 2; ++i) to_out[i] = pair_from_float(v[2 * i] * norm, v[2 * i + 1] * norm, p.type);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) part[(int64_t)r * DIM + kOwn * lane + i] = v[i];
+        if (lane == 0) part[kRows * DIM + r] = m, part[kRows * DIM + kRows + r] = l;
+      }
+    }
+    if (!whole) {
+      if (!starts) flags |= kNoteHead | (ends ? kNoteHeadEnds : 0);
+      else flags |= kNoteTail, note.y = walk.b, note.z = walk.head, note.w = walk.block;
+    }
+    next_piece<kRows, kUnit>(p, walk);
+    __syncthreads();  // (the sums and queries are read)
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  note.x = flags;
+  if (threadIdx.x == 0) p.notes[blockIdx.x] = note;
+}
+
+template <int DIM, int NT>
+cudaError_t launch(const AttentionParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  const int ctas = std::min(multiprocessors(), kMostCtas);
+  log_kernel("cache_attention tokens=%d heads=%dx%d dim=%d sequences=%d | rows=%d ctas=%d", p.at.tokens,
+             p.cache.heads, p.group, DIM, p.at.sequences, 8 * NT, ctas);
+  const cudaError_t err = launch_cluster(attention_tokens_kernel<DIM, NT>, ready, (unsigned)ctas, kThreads,
+                                         Layout<DIM, NT>::kBytes, 1, st, p);
+  return err == cudaSuccess ? launch_attention_join(p, 8 * NT, ctas, st) : err;
+}
+template <int DIM>
+cudaError_t launch_rows(const AttentionParams& p, int rows, cudaStream_t st) {
+  if (rows == 8) return launch<DIM, 1>(p, st);
+  if (rows == 16) return launch<DIM, 2>(p, st);
+  return launch<DIM, 4>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tokens(const AttentionParams& p, int rows, cudaStream_t st) {
+  return p.dim == 64 ? launch_rows<64>(p, rows, st) : launch_rows<128>(p, rows, st);
+}
+
+}  // namespace ff
+}  // namespace fwt

@@ -1,0 +1,243 @@
+// Keys and values into the cache and back: rotated, with a scale for each token and head.
+//
+//   append   y = 2^(-r/2) H x in fp32, s = the least 2^e with max |y| <= 448 s, codes e4m3(y / s)
+//   read     x = 2^(-r/2) H (s codes)
+//
+// A row (a token's head) is spread over DIM / 16 lanes, 16 elements each: two runs of 8, half a
+// row apart, so that the lanes of a row read and write whole sectors in one instruction.  Bits 0 to
+// 2 and the top bit of the rotation are then among a lane's own elements, the others exchange
+// with a neighbour lane.  Scales are powers of two: a floating-point code loses nothing by it (its
+// relative step is the same at either end of a factor of two), and multiplying by one rounds nothing.
+//
+// Rows of several sequences lie one after the other; a CTA counts how many sequences end at or
+// before its first row, and its rows go on from there.
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda_runtime.h>
+
+#include "cache.cuh"
+#include "feed_forward.cuh"
+#include "ff_host.cuh"
+#include "tma.cuh"
+
+namespace fwt {
+namespace ff {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct MoveParams {
+  CacheView cache;
+  Places at;
+  Rows rows[2];
+  int rot_bits;
+};
+
+// Sequences that end at or before packed row `row`; every thread of the CTA calls it.
+__device__ __forceinline__ int sequences_before(const Places& at, int row) {
+  int before = 0;
+  for (int b0 = 0; b0 < at.sequences; b0 += kThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    before += __syncthreads_count(b < at.sequences && at.starts[b + 1] <= row);
+  }
+  return before;
+}
+
+// The sequence of row `row`, from `b` on, and its place: the page and the slot in it, page -1 for
+// none; false where the row is no sequence's.
+__device__ __forceinline__ bool locate(const MoveParams& p, int row, int b, int& page, int& slot) {
+  page = -1, slot = 0;
+  while (b < p.at.sequences && p.at.starts[b + 1] <= row) ++b;
+  if (b >= p.at.sequences) return false;
+  const Sequence s = sequence(p.at, p.cache.page_tokens, b);
+  if (row < s.row || row >= s.row + s.count) return false;
+  const int pos = s.length - (s.row + s.count - row);
+  if (pos >= 0) {
+    page = page_of(p.cache, p.at, b, pos);
+    slot = pos % p.cache.page_tokens;
+  }
+  return true;
+}
+
+// The rotation of a row over DIM / 16 lanes, 8 elements from `lane * 8` and 8 half a row on.
+template <int DIM>
+__device__ __forceinline__ void turn(float (&v)[16], int r, int lane) {
+  constexpr int kBits = DIM == 128 ? 7 : 6;
+  if (r > 0) turn_own<16, 1>(v);
+  if (r > 1) turn_own<16, 2>(v);
+  if (r > 2) turn_own<16, 4>(v);
+#pragma unroll
+  for (int bit = 3; bit < kBits - 1; ++bit)
+    if (r > bit) turn_lanes(v, 1 << (bit - 3), lane);
+  if (r == kBits) turn_own<16, 8>(v);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* from, float* v) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 q = ((const float4*)from)[i];
+      v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    }
+  } else {
+    const uint4 q = *(const uint4*)from;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = pair_to_float<T>(w[i]);
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* to, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ((float4*)to)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    *(uint4*)to = make_uint4(pair_from_float<T>(v[0], v[1]), pair_from_float<T>(v[2], v[3]),
+                             pair_from_float<T>(v[4], v[5]), pair_from_float<T>(v[6], v[7]));
+  }
+}
+
+template <typename T, int DIM>
+__global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
+  constexpr int kLanes = DIM / 16, kRows = kThreads / kLanes;
+  const int lane = threadIdx.x & (kLanes - 1), r = p.rot_bits;
+  const int64_t first = (int64_t)blockIdx.x * kRows, pair = first + threadIdx.x / kLanes;
+  pdl_begin();
+  const int before = sequences_before(p.at, (int)(first / p.cache.heads));
+  const int token = (int)(pair / p.cache.heads), head = (int)(pair - (int64_t)token * p.cache.heads);
+  int page, slot;
+  if (token >= p.at.tokens || !locate(p, token, before, page, slot)) page = -1;
+  // (lanes of a warp exchange: those without a row go along with zeros)
+  float v[2][16];
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const T* from = (const T*)p.rows[o].p + token * p.rows[o].token + head * p.rows[o].head + 8 * lane;
+    if (page >= 0) {
+      load8(from, v[o]), load8(from + DIM / 2, v[o] + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[o][i] = 0.f;
+    }
+  }
+  const float norm = 16.f * rotation_norm(r);
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    if (r) {  // 1/16 first, so that no sum of 128 overflows before the norm
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[o][i] *= 0.0625f;
+      turn<DIM>(v[o], r, lane);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[o][i] *= norm;
+    }
+    uint32_t top = 0;  // of magnitudes as bits: NaN is above all
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[o][i]) & 0x7fffffffu);
+#pragma unroll
+    for (int step = 1; step < kLanes; step *= 2) top = max(top, __shfl_xor_sync(~0u, top, step));
+    const uint32_t byte = scale_byte(__uint_as_float(top));
+    const float inverse = __uint_as_float((254u - byte) << 23);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = byte == 255u ? 0u
+                          : f32x2_to_e4m3(v[o][4 * i] * inverse, v[o][4 * i + 1] * inverse) |
+                                f32x2_to_e4m3(v[o][4 * i + 2] * inverse, v[o][4 * i + 3] * inverse) << 16;
+    if (page >= 0) {
+      const int64_t at = (int64_t)head * p.cache.page_tokens + slot;
+      uint8_t* codes = p.cache.codes[o] + page * p.cache.code_stride[o] + at * DIM + 8 * lane;
+      *(uint2*)codes = make_uint2(w[0], w[1]);
+      *(uint2*)(codes + DIM / 2) = make_uint2(w[2], w[3]);
+      if (lane == 0) p.cache.scales[o][page * p.cache.scale_stride[o] + at] = (uint8_t)byte;
+    }
+  }
+}
+
+template <typename T, int DIM>
+__global__ void __launch_bounds__(kThreads) read_kernel(const MoveParams p) {
+  constexpr int kLanes = DIM / 16, kRows = kThreads / kLanes;
+  const int lane = threadIdx.x & (kLanes - 1), r = p.rot_bits;
+  const int64_t first = (int64_t)blockIdx.x * kRows, pair = first + threadIdx.x / kLanes;
+  pdl_begin();
+  const int before = sequences_before(p.at, (int)(first / p.cache.heads));
+  const int token = (int)(pair / p.cache.heads), head = (int)(pair - (int64_t)token * p.cache.heads);
+  int page = -1, slot = 0;
+  const bool row = token < p.at.tokens && locate(p, token, before, page, slot);
+  uint2 w[2][2];
+  uint32_t byte[2];
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    w[o][0] = w[o][1] = make_uint2(0, 0), byte[o] = 127;
+    if (page >= 0) {
+      const int64_t at = (int64_t)head * p.cache.page_tokens + slot;
+      const uint8_t* codes = p.cache.codes[o] + page * p.cache.code_stride[o] + at * DIM + 8 * lane;
+      w[o][0] = *(const uint2*)codes, w[o][1] = *(const uint2*)(codes + DIM / 2);
+      byte[o] = p.cache.scales[o][page * p.cache.scale_stride[o] + at];
+    }
+  }
+  const float norm = rotation_norm(r);
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t q = i & 1 ? w[o][i / 2].y : w[o][i / 2].x;
+      const float2 lo = pair_to_float<__half>(e4m3_to_f16x2(q));
+      const float2 hi = pair_to_float<__half>(e4m3_to_f16x2(q >> 16));
+      v[4 * i] = lo.x, v[4 * i + 1] = lo.y, v[4 * i + 2] = hi.x, v[4 * i + 3] = hi.y;
+    }
+    turn<DIM>(v, r, lane);  // of codes: their sums are exact or nearly so
+    const float scale = scale_value(byte[o]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = v[i] * norm * scale;
+    if (row) {
+      T* to = (T*)p.rows[o].p + token * p.rows[o].token + head * p.rows[o].head + 8 * lane;
+      store8(to, v), store8(to + DIM / 2, v + 8);
+    }
+  }
+}
+
+template <template <typename, int> class Kernel, typename T>
+cudaError_t launch_dim(const MoveParams& p, int dim, const char* what, cudaStream_t st) {
+  const int64_t pairs = (int64_t)p.at.tokens * p.cache.heads, rows = kThreads / (dim / 16);
+  const int64_t grid = (pairs + rows - 1) / rows;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  log_kernel("%s tokens=%d heads=%d dim=%d | rows a CTA=%lld", what, p.at.tokens, p.cache.heads, dim,
+             (long long)rows);
+  return launch_overlapped(dim == 64 ? Kernel<T, 64>::get() : Kernel<T, 128>::get(), (unsigned)grid,
+                           kThreads, 0, 1, st, p);
+}
+template <typename T, int DIM>
+struct Append {
+  static auto get() { return append_kernel<T, DIM>; }
+};
+template <typename T, int DIM>
+struct Read {
+  static auto get() { return read_kernel<T, DIM>; }
+};
+template <template <typename, int> class Kernel>
+cudaError_t launch_type(const MoveParams& p, int type, int dim, const char* what, cudaStream_t st) {
+  if (type == FWT_F32) return launch_dim<Kernel, float>(p, dim, what, st);
+  if (type == FWT_F16) return launch_dim<Kernel, __half>(p, dim, what, st);
+  return launch_dim<Kernel, __nv_bfloat16>(p, dim, what, st);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
+                                const Places& at, cudaStream_t st) {
+  return launch_type<Append>(MoveParams{cache, at, {k, v}, rot_bits}, type, dim, "cache_append", st);
+}
+
+cudaError_t launch_cache_read(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
+                              const Places& at, cudaStream_t st) {
+  return launch_type<Read>(MoveParams{cache, at, {k, v}, rot_bits}, type, dim, "cache_read", st);
+}
+
+}  // namespace ff
+}  // namespace fwt

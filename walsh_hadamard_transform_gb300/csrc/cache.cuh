@@ -1,0 +1,187 @@
+// The cache of keys and values and how its kernels find their way in it.
+//
+// A page holds `page_tokens` tokens (a multiple of 16) of every head: codes as heads x tokens x dim
+// bytes, so that 16 tokens of a head are one run of memory that no page boundary cuts, and scales
+// as heads x tokens bytes, 16 of them one aligned 16-byte piece.
+//
+// Sequence b owns rows starts[b] .. starts[b + 1] of the packed operands: the last of its
+// lengths[b] tokens in the cache.  Both arrays are device memory that the host never reads, so
+// every kernel clamps what it takes from them: rows to the packed operand, lengths to the table,
+// and a page that is not one of the cache's holds nothing.
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "fwt.h"
+
+namespace fwt {
+namespace ff {
+
+struct CacheView {
+  uint8_t* codes[2];  // keys, values
+  uint8_t* scales[2];
+  int64_t code_stride[2], scale_stride[2];  // bytes from page to page
+  int pages, heads, page_tokens;
+};
+
+struct Places {
+  const int32_t* table;
+  int64_t ld_table;
+  int most_pages;
+  const int32_t *starts, *lengths;
+  int sequences, tokens;  // tokens: rows of the packed operands
+};
+
+// Rows of heads apart: element strides of a (tokens, heads, dim) operand.
+struct Rows {
+  void* p;
+  int64_t token, head;
+};
+
+struct AttentionParams {
+  CacheView cache;
+  Places at;
+  Rows q, out;
+  int type, group, dim, rot_bits;
+  float scale;   // of the scores, times log2(e)
+  int causal, window;
+  float* parts;  // see attention_plan.cuh
+  int4* notes;
+};
+
+// Launchers, their arguments checked (ff_api.cu's manner): every extent is at least 1.
+cudaError_t launch_cache_append(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
+                                const Places& at, cudaStream_t st);
+cudaError_t launch_cache_read(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
+                              const Places& at, cudaStream_t st);
+cudaError_t launch_attention_tokens(const AttentionParams& p, int rows, cudaStream_t st);
+cudaError_t launch_attention_join(const AttentionParams& p, int rows, int ctas, cudaStream_t st);
+
+constexpr int kMostCtas = 192;  // of an attention kernel; the workspace has room for their parts
+
+// A CTA's two parts: rows x dim sums, then a maximum and a total for each row.
+__host__ __device__ constexpr int64_t part_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
+
+constexpr int kMostLength = 0x7fff0000;  // tokens of a sequence (sums with a tile's fit 31 bits)
+
+struct Sequence {
+  int row, count, length;  // first packed row, rows, tokens in the cache
+};
+
+__device__ __forceinline__ Sequence sequence(const Places& at, int pages_tokens, int b) {
+  Sequence s;
+  s.row = min(max(at.starts[b], 0), at.tokens);
+  s.count = min(max(at.starts[b + 1], s.row), at.tokens) - s.row;
+  const int64_t room = min((int64_t)at.most_pages * pages_tokens, (int64_t)kMostLength);
+  s.length = (int)min((int64_t)max(at.lengths[b], 0), room);
+  return s;
+}
+
+// The page of token `pos` (below the sequence's length), -1 where there is none.
+__device__ __forceinline__ int page_of(const CacheView& c, const Places& at, int b, int pos) {
+  const int page = at.table[(int64_t)b * at.ld_table + pos / c.page_tokens];
+  return (unsigned)page < (unsigned)c.pages ? page : -1;
+}
+
+// ---- 8-bit values ----------------------------------------------------------------------
+
+// Two e4m3 codes (16 bits) as float16: exact.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
+  uint32_t v;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"((unsigned short)codes));
+  return v;
+}
+// float32 to e4m3, to nearest even, beyond 448 to 448.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
+  unsigned short v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+
+// 2^(byte - 127); NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fc00000u) : byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+}
+
+// The scale byte of a row of largest magnitude `top`: the least power of two from 2^-126 on that
+// takes it to 448 = 1.75 * 2^8 or below, 255 where it is not finite.  (2^-126 is the least whose
+// inverse is a finite float.)
+__device__ __forceinline__ uint32_t scale_byte(float top) {
+  const uint32_t bits = __float_as_uint(top) & 0x7fffffffu;
+  if (bits >= 0x7f800000u) return 255u;
+  const int e = (int)((bits + 0x1fffffu) >> 23) - 8;  // (a mantissa above 1.75 carries)
+  return (uint32_t)max(e, 1);
+}
+
+// ---- 16-bit and 32-bit rows ------------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ float2 pair_to_float(uint32_t v) {
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*(const __half2*)&v);
+    else return __bfloat1622float2(*(const __nv_bfloat162*)&v);
+  }
+  return make_float2(0.f, 0.f);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pair_from_float(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *(const uint32_t*)&v;
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t*)&v;
+  }
+}
+// Either 16-bit type by its code.
+__device__ __forceinline__ float2 pair_to_float(uint32_t v, int type) {
+  return type == FWT_F16 ? pair_to_float<__half>(v) : pair_to_float<__nv_bfloat16>(v);
+}
+__device__ __forceinline__ uint32_t pair_from_float(float a, float b, int type) {
+  return type == FWT_F16 ? pair_from_float<__half>(a, b) : pair_from_float<__nv_bfloat16>(a, b);
+}
+
+// ---- the rotation ----------------------------------------------------------------------
+
+// 2^(-r / 2).
+__device__ __forceinline__ float rotation_norm(int r) {
+  return __uint_as_float((uint32_t)(127 - r / 2) << 23) * (r & 1 ? 0.70710678118654752f : 1.f);
+}
+
+// One bit of the rotation among a thread's own values, STEP apart.
+template <int N, int STEP>
+__device__ __forceinline__ void turn_own(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (!(i & STEP)) {
+      const float a = v[i], b = v[i + STEP];
+      v[i] = a + b, v[i + STEP] = a - b;
+    }
+}
+// One bit across lanes `step` apart.
+template <int N>
+__device__ __forceinline__ void turn_lanes(float (&v)[N], int step, int lane) {
+  const float sign = lane & step ? -1.f : 1.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = fmaf(sign, v[i], __shfl_xor_sync(~0u, v[i], step));
+}
+
+// A row of DIM over the 32 lanes of a warp, DIM / 32 consecutive elements each, without the norm.
+template <int DIM>
+__device__ __forceinline__ void turn_row(float (&v)[DIM / 32], int r, int lane) {
+  constexpr int kOwn = DIM == 128 ? 2 : 1;  // bits of a lane's own elements
+  if (r > 0) turn_own<DIM / 32, 1>(v);
+  if constexpr (DIM == 128)
+    if (r > 1) turn_own<DIM / 32, 2>(v);
+#pragma unroll
+  for (int bit = 0; bit < 5; ++bit)
+    if (r > kOwn + bit) turn_lanes(v, 1 << bit, lane);
+}
+
+}  // namespace ff
+}  // namespace fwt
