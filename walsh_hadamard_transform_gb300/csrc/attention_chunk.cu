@@ -1,0 +1,641 @@
+// Attention of many rows (new tokens x query heads of a key head) over the 8-bit cache, on tensor cores:
+// prompts and chunks of them.
+//
+// An item is 256 rows with one key head, two tiles of 128; its keys come by 128.  For each tile and
+// step
+//
+//   S = Q K^T            128 x 128 in tensor memory
+//   P = 2^(c S - m)      a row a thread; float16, over S in tensor memory; l += P in fp32
+//   O += P V             in tensor memory, fp32
+//
+// and the two tiles take turns: while the tensor cores work on one, the other's softmax runs.  m is a
+// maximum of the row that may lag behind by a factor of 2^8 in P: only a larger step multiplies O
+// again, which is rare after the first keys.
+//
+// Four warps turn codes into float16 operands in the layout the products read (128-byte swizzle; keys
+// along the contraction, values across it).  The scales go in with them, exactly: a key's
+// factor is 2^(e - e_ref), e_ref the largest scale's exponent of the item's first keys, moved only
+// when one is more than 2^7 above it; what lies more than 2^15 below it keeps fewer bits
+// (float16's smallest step).  So c is one number a row and the softmax has no scales to look up.
+// Values the same, with O in units of 2^e_ref.  Queries are rounded to float16 once after their rotation,
+// each row at a power of two.
+//
+// Warps: 0 to 3 and 4 to 7 softmax and output of tile 0 and 1, 8 to 11 operands, 12 products.
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attention_plan.cuh"
+#include "cache.cuh"
+#include "feed_forward.cuh"
+#include "ff_host.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace fwt {
+namespace ff {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kKeys = 128;    // of a step; a unit of the plan
+constexpr int kStages = 2;    // of keys, and of values
+constexpr int kInfos = 4;     // see Info
+constexpr float kLag = 8.f;   // of a row's maximum, in powers of two
+
+// What the softmax has to know of a step's keys.  A ring of four: when step j + 3's is written, the
+// products of step j + 1 have been issued, which came after both tiles' softmax of step j.
+struct Info {
+  int key_ref, value_ref;  // scale bytes that stand for 1 in the operands
+  int special;             // whether any bit below is set
+  uint32_t hidden[4];      // bit i of word j: token 4 i + j is no token
+  uint32_t poison[4];      //                  its key or value is not a number
+};
+
+template <int DIM>
+struct Layout {
+  static constexpr int kChunks = DIM / 64;                 // of 64 elements, 128 bytes a row
+  static constexpr uint32_t kChunk = 128 * 128;            // bytes
+  static constexpr uint32_t kTile = kChunks * kChunk;      // 128 rows
+  static constexpr uint32_t kKeysAt = 2 * kTile, kValuesAt = kKeysAt + kStages * kTile;
+  static constexpr size_t kBytes = kValuesAt + kStages * kTile + 1024;
+};
+
+constexpr uint32_t kScoresAt = 0, kOutAt = 256;  // tensor memory columns; 128 and DIM a tile
+constexpr uint32_t kColumns = 512;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// 2^e in two factors, for -252 <= e <= 254.
+__device__ __forceinline__ float times_power(float v, int e) {
+  const int half = e >> 1;
+  return v * __uint_as_float((uint32_t)(127 + half) << 23) * __uint_as_float((uint32_t)(127 + e - half) << 23);
+}
+
+// 2^f in both halves of a pair of float16, f <= 7; zero below 2^-24.
+__device__ __forceinline__ uint32_t power_f16x2(int f) {
+  const uint32_t h = f >= -14 ? (uint32_t)(f + 15) << 10 : f >= -24 ? 1u << (f + 24) : 0u;
+  return h | h << 16;
+}
+__device__ __forceinline__ uint32_t multiply_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Bits 0 to R - 1 of the rotation among a thread's own N values, without the norm.
+template <int N>
+__device__ __forceinline__ void turn_all(float (&v)[N], int r) {
+  if (r > 0) turn_own<N, 1>(v);
+  if (r > 1) turn_own<N, 2>(v);
+  if (r > 2) turn_own<N, 4>(v);
+  if (r > 3) turn_own<N, 8>(v);
+  if (r > 4) turn_own<N, 16>(v);
+  if (r > 5) turn_own<N, 32>(v);
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const AttentionParams p) {
+  using L = Layout<DIM>;
+  extern __shared__ uint8_t dynamic[];
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], info_full[kInfos];
+  __shared__ Info infos[kInfos];
+  __shared__ float row_scale[kChunkRows];
+  __shared__ PlanScratch<kThreads> scratch;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int gave_up;
+  __shared__ volatile uint32_t issued;  // steps so far: a tile may sit out many
+
+  const uint32_t base = (smem_u32(dynamic) + 1023u) & ~1023u;
+  uint8_t* memory = dynamic + (base - smem_u32(dynamic));
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t)
+      mbar_init(&q_full[t], 4), mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 4), mbar_init(&o_full[t], 1);
+    for (int s = 0; s < kStages; ++s)
+      mbar_init(&k_full[s], 4), mbar_init(&k_empty[s], 1), mbar_init(&v_full[s], 4), mbar_init(&v_empty[s], 1);
+    for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
+    gave_up = 0, issued = 0;
+  }
+  if (warp == 12) tmem_alloc<1>(&tmem_base, kColumns);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_begin();
+
+  Walk walk = find_share<kChunkRows, kKeys>(p, blockIdx.x, gridDim.x, scratch);
+  const auto rows_of = [&](const Walk& w) {  // of the item
+    return (int)min((int64_t)kChunkRows, (int64_t)w.s.count * p.group - (int64_t)w.block * kChunkRows);
+  };
+
+  if (warp < 8) {
+    // softmax and output of tile `t`; this thread's row of it is 32 (warp & 3) + lane
+    [&] {
+      const int t = warp >> 2, quarter = warp & 3, mine = 32 * quarter + lane;
+      const uint32_t lanes = (uint32_t)quarter << 21;
+      const uint32_t scores = tmem + kScoresAt + 128 * t + lanes, out = tmem + kOutAt + DIM * t + lanes;
+      uint32_t steps = 0;              // of the share so far
+      uint32_t turns = 0, pieces = 0;  // steps and items of this tile
+
+      // the queries of the item where `w` stands, into shared memory
+      const auto stage_queries = [&](const Walk& w) {
+        const int rows = rows_of(w);
+        if (rows <= 128 * t) return;
+        const float norm = rotation_norm(p.rot_bits) * (p.scale < 0.f ? -1.f : 1.f);
+        constexpr int kOwn = DIM / 32, kAhead = 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += kAhead) {
+          uint32_t raw[kAhead][kOwn / 2];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int r = 128 * t + 32 * quarter + i0 + i;
+#pragma unroll
+            for (int j = 0; j < kOwn / 2; ++j) raw[i][j] = 0;
+            if (r < rows) {
+              const int64_t row = (int64_t)w.block * kChunkRows + r;
+              const int token = w.s.row + (int)(row / p.group), head = w.head * p.group + (int)(row % p.group);
+              const uint32_t* q = (const uint32_t*)((const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + kOwn * lane);
+#pragma unroll
+              for (int j = 0; j < kOwn / 2; ++j) raw[i][j] = q[j];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int r = 32 * quarter + i0 + i;
+            float v[kOwn];
+#pragma unroll
+            for (int j = 0; j < kOwn / 2; ++j) {
+              const float2 f = pair_to_float(raw[i][j], p.type);
+              v[2 * j] = f.x, v[2 * j + 1] = f.y;
+            }
+            turn_row<DIM>(v, p.rot_bits, lane);
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+              v[j] *= norm;
+              top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+            }
+            top = __reduce_max_sync(~0u, top);
+            const int e = max((int)(top >> 23), 27);  // (zero, and what is nearly so)
+            const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
+            const int d = kOwn * lane;
+            uint8_t* to = memory + t * L::kTile + (d >> 6) * L::kChunk + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2;
+#pragma unroll
+            for (int j = 0; j < kOwn / 2; ++j)
+              ((uint32_t*)to)[j] = pair_from_float<__half>(v[2 * j] * up, v[2 * j + 1] * up);
+            if (lane == 0) row_scale[128 * t + r] = fabsf(p.scale) * __uint_as_float((uint32_t)(e - 14) << 23);
+          }
+        }
+        fence_to_products();
+        __syncwarp();
+        mbar_arrive(&q_full[t], lane == 0);
+      };
+
+      Walk next = walk;
+      if (walk.left > 0) stage_queries(next);
+      while (walk.left > 0) {
+        const int count = piece_units(walk), rows = rows_of(walk);
+        const bool starts = walk.unit == 0, ends = walk.unit + count == walk.units;
+        next_piece<kChunkRows, kKeys>(p, next);
+        if (rows <= 128 * t) {
+          steps += count;
+          if (next.left > 0) stage_queries(next);
+          next_piece<kChunkRows, kKeys>(p, walk);
+          continue;
+        }
+        const int64_t row = (int64_t)walk.block * kChunkRows + 128 * t + mine;  // of the sequence's with this head
+        const bool valid = 128 * t + mine < rows;
+        const Keys seen = valid ? seen_by(p, walk.s, (int)row) : Keys{0, 0x7fffffff};
+        const float scale = row_scale[128 * t + mine];
+        float top = -INFINITY;
+        float2 total = make_float2(0.f, 0.f);
+        int value_ref = 0;
+        for (int step = 0; step < count; ++step, ++steps, ++turns) {
+          const int pos = walk.keys.low + (walk.unit + step) * kKeys;
+          // (first the scores: a tile that sits items out may look at the ring long before its step)
+          if (!wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
+          if (!wait_or_leave(&info_full[steps % kInfos], steps / kInfos & 1, &gave_up)) return;
+          tmem_fence_after();
+          const Info& info = infos[steps % kInfos];
+          const float c = fmaxf(times_power(scale, info.key_ref - 127), 0x1p-120f);
+          const int new_ref = info.value_ref;
+          const int from = seen.low - pos, to = seen.high - pos;  // of the step's keys
+          const bool special = info.special != 0;
+          const bool masked = special || __any_sync(~0u, from > 0 || to < kKeys);
+
+          const auto mask = [&](uint32_t(&v)[32], int at) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int key = at + i;
+              bool see = key >= from && key < to;
+              if (special) {
+                see = see && !(info.hidden[i & 3] >> (key >> 2) & 1u);
+                if (info.poison[i & 3] >> (key >> 2) & 1u) v[i] = 0x7fc00000u;
+              }
+              if (!see) v[i] = 0xff800000u;
+            }
+          };
+          float most = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_load32(scores + 32 * i, v);
+            tmem_wait_loads();
+            if (masked) mask(v, 32 * i);
+            float m[4] = {most, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                m[k] = max3(m[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+            most = max3(fmaxf(m[0], m[1]), m[2], m[3]);
+          }
+          most *= c;  // (c > 0; -inf stays)
+          float less = 1.f;
+          bool again = false;
+          if (most > top + kLag || top == -INFINITY) {
+            again = most > top && top != -INFINITY;
+            if (again) less = exp2_fast(top - most);
+            if (most > top) top = most;
+          }
+          if (step > 0 && __any_sync(~0u, again || new_ref != value_ref)) {
+            total.x *= less, total.y *= less;
+            // (moved up by more than 2^7; a smaller unit of nothing yet is no loss)
+            less *= __uint_as_float((uint32_t)max(127 + value_ref - new_ref, 0) << 23);
+#pragma unroll 1
+            for (int i = 0; i < DIM / 32; ++i) {
+              uint32_t v[32];
+              tmem_load32(out + 32 * i, v);
+              tmem_wait_loads();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * less);
+              tmem_store16(out + 32 * i, v);
+              tmem_store16(out + 32 * i + 16, v + 16);
+            }
+          }
+          value_ref = new_ref;
+          const float shift = top == -INFINITY ? 0.f : -top;
+          const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+          float2 sums[2] = {total, make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32], packed[16];
+            tmem_load32(scores + 32 * i, v);
+            tmem_wait_loads();
+            if (masked) mask(v, 32 * i);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 x = fma_pair(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, shift2);
+              x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+              sums[j & 1] = add_pair(sums[j & 1], x);
+              packed[j] = pair_from_float<__half>(x.x, x.y);
+            }
+            tmem_store16(scores + 16 * i, packed);
+          }
+          total = add_pair(sums[0], sums[1]);
+          tmem_wait_stores();
+          tmem_fence_before();
+          __syncwarp();
+          mbar_arrive(&p_full[t], lane == 0);
+        }
+        // the next item's queries while this one's last products run
+        if (next.left > 0) stage_queries(next);
+        if (!wait_or_leave(&o_full[t], pieces & 1, &gave_up)) return;
+        ++pieces;
+        tmem_fence_after();
+        const float l = total.x + total.y;
+        if (starts && ends) {
+          const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
+          const int token = walk.s.row + (int)(row / p.group), head = walk.head * p.group + (int)(row % p.group);
+          uint16_t* to = (uint16_t*)p.out.p + token * p.out.token + head * p.out.head;
+          // (64 of a row's elements at a time: the top bit of 128 first)
+#pragma unroll 1
+          for (int half = 0; half < DIM / 64; ++half) {
+            float o[64];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t v[32];
+              const bool both = DIM == 128 && p.rot_bits == 7;
+              tmem_load32(out + 32 * i + (both ? 0 : 64 * half), v);
+              tmem_wait_loads();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[32 * i + j] = __uint_as_float(v[j]);
+              if (both) {
+                tmem_load32(out + 32 * i + 64, v);
+                tmem_wait_loads();
+                const float sign = half ? -1.f : 1.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[32 * i + j] = fmaf(sign, __uint_as_float(v[j]), o[32 * i + j]);
+              }
+            }
+            turn_all(o, p.rot_bits);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) o[j] = times_power(o[j] * norm, value_ref - 127);
+            if (valid) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *(uint4*)(to + 64 * half + 8 * j) =
+                    make_uint4(pair_from_float(o[8 * j], o[8 * j + 1], p.type), pair_from_float(o[8 * j + 2], o[8 * j + 3], p.type),
+                               pair_from_float(o[8 * j + 4], o[8 * j + 5], p.type), pair_from_float(o[8 * j + 6], o[8 * j + 7], p.type));
+            }
+          }
+        } else {
+          float* part = p.parts + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * part_floats(kChunkRows, DIM);
+          const int r = 128 * t + mine;
+#pragma unroll 1
+          for (int i = 0; i < DIM / 32; ++i) {
+            uint32_t v[32];
+            tmem_load32(out + 32 * i, v);
+            tmem_wait_loads();
+            if (valid) {
+              float4* to = (float4*)(part + (int64_t)r * DIM + 32 * i);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = times_power(__uint_as_float(v[4 * j + k]), value_ref - 127);
+                to[j] = make_float4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          }
+          if (valid) part[kChunkRows * DIM + r] = top, part[kChunkRows * DIM + kChunkRows + r] = l;
+        }
+        tmem_fence_before();  // (before the next item's products write there, which wait for p_full)
+        next_piece<kChunkRows, kKeys>(p, walk);
+      }
+    }();
+  } else if (warp < 12) {
+    // operands: a row of codes is spread over DIM / 16 lanes, 16 bytes each
+    [&] {
+      constexpr int kLanes = DIM / 16, kRows = 32 / kLanes, kTimes = 128 / (4 * kRows);
+      const int w = warp - 8, sub = lane / kLanes, part = lane & (kLanes - 1);
+      const CacheView& cache = p.cache;
+      uint32_t steps = 0;
+
+      Walk ahead = walk;  // the steps whose codes are on their way
+      int ahead_step = 0;
+      uint4 codes[2][kTimes];
+      uint32_t bytes[2];          // scales of tokens 4 lane .. 4 lane + 3
+      int pages = -1;             // lanes 0 to 7: of the coming step's 16 tokens each
+      const auto position = [&](const Walk& at, int step) { return at.keys.low + (at.unit + step) * kKeys; };
+      const auto find_pages = [&] {
+        if (ahead.left <= 0) return;
+        const int pos = position(ahead, ahead_step) + 16 * (lane & 7);
+        pages = pos < ahead.keys.high ? page_of(cache, p.at, ahead.b, pos) : -1;
+      };
+      // one of a step's two operands
+      const auto fetch = [&](int o) {
+        if (ahead.left <= 0) return;
+        const int pos = position(ahead, ahead_step);
+        {
+          const int group = lane >> 2, page = __shfl_sync(~0u, pages, group);
+          const int slot = (pos + 16 * group) % cache.page_tokens;
+          bytes[o] = 0;
+          if (page >= 0)
+            bytes[o] = *(const uint32_t*)(cache.scales[o] + page * cache.scale_stride[o] +
+                                          (int64_t)ahead.head * cache.page_tokens + slot + 4 * (lane & 3));
+        }
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const int row = (4 * i + w) * kRows + sub, group = (4 * i + w) * kRows / 16;
+          const int page = __shfl_sync(~0u, pages, group);
+          codes[o][i] = make_uint4(0, 0, 0, 0);
+          if (page >= 0 && pos + row < ahead.keys.high) {
+            const int slot = (pos + 16 * group) % cache.page_tokens + (row & 15);
+            codes[o][i] = *(const uint4*)(cache.codes[o] + page * cache.code_stride[o] +
+                                          ((int64_t)ahead.head * cache.page_tokens + slot) * DIM + 16 * part);
+          }
+        }
+      };
+      // the fetched operand into shared memory; scale bytes `scales`, their unit `ref`
+      const auto convert = [&](int o, uint32_t at, uint32_t scales, int ref) {
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const int row = (4 * i + w) * kRows + sub;
+          const uint32_t four = __shfl_sync(~0u, scales, row >> 2);
+          const int byte = (four >> (8 * (row & 3))) & 255;
+          const uint32_t factor = byte == 255 ? 0u : power_f16x2(min(byte - ref, 7));  // (no token: any byte)
+          const uint32_t c[4] = {codes[o][i].x, codes[o][i].y, codes[o][i].z, codes[o][i].w};
+          uint4 v[2];
+          v[0] = make_uint4(multiply_f16x2(e4m3_to_f16x2(c[0]), factor), multiply_f16x2(e4m3_to_f16x2(c[0] >> 16), factor),
+                            multiply_f16x2(e4m3_to_f16x2(c[1]), factor), multiply_f16x2(e4m3_to_f16x2(c[1] >> 16), factor));
+          v[1] = make_uint4(multiply_f16x2(e4m3_to_f16x2(c[2]), factor), multiply_f16x2(e4m3_to_f16x2(c[2] >> 16), factor),
+                            multiply_f16x2(e4m3_to_f16x2(c[3]), factor), multiply_f16x2(e4m3_to_f16x2(c[3] >> 16), factor));
+          // (lanes of the second 64 elements write their pieces in the other order: eight lanes
+          // then meet all banks)
+          const int first = part >> 2, piece = 2 * (part & 3);
+          uint8_t* to = memory + at + (part >> 2) * L::kChunk + row * 128;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int which = k ^ first;
+            *(uint4*)(to + (((piece + which) ^ (row & 7)) << 4)) = which ? v[1] : v[0];
+          }
+        }
+        fence_to_products();
+        __syncwarp();
+      };
+
+      find_pages();
+      fetch(0), fetch(1);
+      while (walk.left > 0) {
+        const int count = piece_units(walk);
+        int ref[2] = {0, 0};
+        for (int step = 0; step < count; ++step, ++steps) {
+          const int stage = steps % kStages;
+          const uint32_t parity = (steps / kStages & 1) ^ 1;
+          const uint32_t scales[2] = {bytes[0], bytes[1]};
+          // tokens of this lane that are there, and what the softmax has to know
+          uint32_t hidden = 0, poison = 0;  // a bit for each of the four
+          {
+            const int pos = position(walk, step);
+            const int page = __shfl_sync(~0u, pages, lane >> 2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool there = page >= 0 && pos + 4 * lane + j < walk.keys.high;
+              const uint32_t b0 = scales[0] >> (8 * j) & 255u, b1 = scales[1] >> (8 * j) & 255u;
+              if (page < 0) hidden |= 1u << j;
+              if (there && (b0 == 255u || b1 == 255u)) poison |= 1u << j;
+            }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              uint32_t most = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t b = scales[o] >> (8 * j) & 255u;
+                if (page >= 0 && pos + 4 * lane + j < walk.keys.high && b != 255u) most = max(most, b);
+              }
+              most = __reduce_max_sync(~0u, most);
+              if (step == 0 || (int)most > ref[o] + 7) ref[o] = (int)most;
+            }
+          }
+          if (w == 0) {
+            Info& info = infos[steps % kInfos];
+            const uint32_t any = __ballot_sync(~0u, hidden | poison);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t h = __ballot_sync(~0u, hidden >> j & 1u), q = __ballot_sync(~0u, poison >> j & 1u);
+              if (lane == 0) info.hidden[j] = h, info.poison[j] = q;
+            }
+            // (written when the stage is free: see Info)
+            if (!wait_or_leave(&k_empty[stage], parity, &gave_up)) return;
+            if (lane == 0) info.key_ref = ref[0], info.value_ref = ref[1], info.special = any != 0;
+            __syncwarp();
+            mbar_arrive(&info_full[steps % kInfos], lane == 0);
+          } else {
+            if (!wait_or_leave(&k_empty[stage], parity, &gave_up)) return;
+          }
+          convert(0, L::kKeysAt + stage * L::kTile, scales[0], ref[0]);
+          mbar_arrive(&k_full[stage], lane == 0);
+          // on to the next step's codes
+          if (++ahead_step == piece_units(ahead)) next_piece<kChunkRows, kKeys>(p, ahead), ahead_step = 0;
+          find_pages();
+          fetch(0);
+          if (!wait_or_leave(&v_empty[stage], parity, &gave_up)) return;
+          convert(1, L::kValuesAt + stage * L::kTile, scales[1], ref[1]);
+          mbar_arrive(&v_full[stage], lane == 0);
+          fetch(1);
+        }
+        next_piece<kChunkRows, kKeys>(p, walk);
+      }
+    }();
+  } else if (warp == 12) {
+    // products
+    [&] {
+      constexpr uint32_t kOfScores = instruction(0, false, false, 128, 128);
+      constexpr uint32_t kOfOut = instruction(0, false, true, 128, DIM);
+      uint32_t steps = 0, turns[2] = {0, 0}, pieces[2] = {0, 0};
+      const auto scores = [&](int t, int stage) {
+        const uint64_t a = operand(base + t * L::kTile, 16), b = operand(base + L::kKeysAt + stage * L::kTile, 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < DIM / 16; ++kk) {
+            const uint32_t at = (kk >> 2) * (L::kChunk >> 4) + (kk & 3) * 2;
+            mma_tile<1, 2>(tmem + kScoresAt + 128 * t, a + at, b + at, kOfScores, kk > 0);
+          }
+          mma_commit<1>(&s_full[t]);
+        }
+        __syncwarp();
+      };
+      while (walk.left > 0) {
+        const int count = piece_units(walk), tiles = rows_of(walk) > 128 ? 2 : 1;
+        if (!wait_or_leave(&k_full[steps % kStages], steps / kStages & 1, &gave_up)) return;
+        for (int t = 0; t < tiles; ++t) {
+          if (!wait_or_leave(&q_full[t], pieces[t] & 1, &gave_up)) return;
+          ++pieces[t];
+          tmem_fence_after();
+          scores(t, steps % kStages);
+        }
+        if (elect_one()) mma_commit<1>(&k_empty[steps % kStages]);
+        __syncwarp();
+        for (int step = 0; step < count; ++step, ++steps) {
+          if (lane == 0) issued = steps;
+          const int stage = steps % kStages, next_stage = (steps + 1) % kStages;
+          const bool more = step + 1 < count;
+          for (int t = 0; t < tiles; ++t) {
+            if (t == 0 && !wait_or_leave(&v_full[stage], steps / kStages & 1, &gave_up)) return;
+            if (!wait_or_leave(&p_full[t], turns[t] & 1, &gave_up)) return;
+            ++turns[t];
+            tmem_fence_after();
+            const uint64_t b = operand(base + L::kValuesAt + stage * L::kTile, L::kChunk);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 rows of values, 8 columns of pairs of P
+                mma_tile_from_tmem(tmem + kOutAt + DIM * t, tmem + kScoresAt + 128 * t + 8 * kk, b + kk * 128,
+                                   kOfOut, step + kk > 0);
+              if (t + 1 == tiles) mma_commit<1>(&v_empty[stage]);
+              if (!more) mma_commit<1>(&o_full[t]);
+            }
+            __syncwarp();
+            if (more) {
+              if (t == 0 && !wait_or_leave(&k_full[next_stage], (steps + 1) / kStages & 1, &gave_up)) return;
+              scores(t, next_stage);
+              if (t + 1 == tiles) {
+                if (elect_one()) mma_commit<1>(&k_empty[next_stage]);
+                __syncwarp();
+              }
+            }
+          }
+        }
+        next_piece<kChunkRows, kKeys>(p, walk);
+      }
+    }();
+  }
+
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (gave_up) drain();
+  tmem_fence_after();
+  if (warp == 12) tmem_free<1>(tmem, kColumns);
+  // what there is to join (a thread of a warp that has kept its share's start walks it once more)
+  if (warp == 13) {
+    int4 note = make_int4(0, 0, 0, 0);
+    while (walk.left > 0) {
+      const int count = piece_units(walk);
+      const bool starts = walk.unit == 0, ends = walk.unit + count == walk.units;
+      if (!starts) note.x |= kNoteHead | (ends ? kNoteHeadEnds : 0);
+      else if (!ends) note.x |= kNoteTail, note.y = walk.b, note.z = walk.head, note.w = walk.block;
+      next_piece<kChunkRows, kKeys>(p, walk);
+    }
+    if (gave_up) note.x &= kNoteHead | kNoteHeadEnds;
+    if (lane == 0) p.notes[blockIdx.x] = note;
+  }
+}
+
+template <int DIM>
+cudaError_t launch(const AttentionParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  const int ctas = std::min(multiprocessors(), kMostCtas);
+  log_kernel("cache_attention tokens=%d heads=%dx%d dim=%d sequences=%d | rows=%d ctas=%d", p.at.tokens,
+             p.cache.heads, p.group, DIM, p.at.sequences, kChunkRows, ctas);
+  const cudaError_t err = launch_cluster(attention_chunk_kernel<DIM>, ready, (unsigned)ctas, kThreads,
+                                         Layout<DIM>::kBytes, 1, st, p);
+  return err == cudaSuccess ? launch_attention_join(p, kChunkRows, ctas, st) : err;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_chunk(const AttentionParams& p, cudaStream_t st) {
+  return p.dim == 64 ? launch<64>(p, st) : launch<128>(p, st);
+}
+
+// Reads and clears this translation unit's device error word (synchronising).
+cudaError_t read_device_error_attention(unsigned int* out) {
+  const unsigned int zero = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(out, g_device_error, sizeof(unsigned int));
+  if (err == cudaSuccess && *out)
+    err = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(unsigned int));
+  return err;
+}
+
+}  // namespace ff
+}  // namespace fwt

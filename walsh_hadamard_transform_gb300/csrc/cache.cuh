@@ -60,6 +60,8 @@ cudaError_t launch_cache_append(Rows k, Rows v, int type, int dim, int rot_bits,
 cudaError_t launch_cache_read(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
                               const Places& at, cudaStream_t st);
 cudaError_t launch_attention_tokens(const AttentionParams& p, int rows, cudaStream_t st);
+cudaError_t launch_attention_chunk(const AttentionParams& p, cudaStream_t st);
+constexpr int kChunkRows = 256;  // rows of an item there
 cudaError_t launch_attention_join(const AttentionParams& p, int rows, int ctas, cudaStream_t st);
 
 constexpr int kMostCtas = 192;  // of an attention kernel; the workspace has room for their parts

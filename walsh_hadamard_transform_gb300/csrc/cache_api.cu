@@ -135,7 +135,7 @@ int most_rotation(int dim) { return dim == 64 ? 6 : 7; }
 // Rows of an item.  A call whose sequences have few rows for each key head goes by groups of 8.
 int item_rows(int64_t longest, int64_t group) {
   const int64_t rows = longest * group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kChunkRows;
 }
 
 }  // namespace
@@ -253,7 +253,9 @@ int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* ou
   p.scale = scale * 1.44269504088896341f;  // scores in powers of two
   p.causal = causal, p.window = (int)std::min<int64_t>(window, 1 << 30);
   p.notes = (int4*)workspace, p.parts = (float*)((char*)workspace + kMostCtas * sizeof(int4));
-  return done(launch_attention_tokens(p, item_rows(longest, p.group), (cudaStream_t)stream));
+  const int rows_each = item_rows(longest, p.group);
+  return done(rows_each == kChunkRows ? launch_attention_chunk(p, (cudaStream_t)stream)
+                                      : launch_attention_tokens(p, rows_each, (cudaStream_t)stream));
 }
 
 }  // extern "C"

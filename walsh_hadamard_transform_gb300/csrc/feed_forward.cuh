@@ -68,6 +68,7 @@ cudaError_t launch_gated_dw(CMat dg, CMat du, CMat x, Mat dw_gate, Mat dw_up, Bo
 // Read and clear the device error words of the kernels that wait (synchronising).
 cudaError_t read_device_error_gated(unsigned int* out);
 cudaError_t read_device_error_matmul(unsigned int* out);
+cudaError_t read_device_error_attention(unsigned int* out);
 
 }  // namespace ff
 }  // namespace fwt

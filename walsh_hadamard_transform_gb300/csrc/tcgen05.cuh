@@ -144,6 +144,19 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
       : "r"(addr));
 }
 
+// The same for stores of 16 columns, which are done after tmem_wait_stores().
+__device__ __forceinline__ void tmem_wait_stores() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
+      " %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
 // ---- matrix products -----------------------------------------------------------------
 
 // Shared-memory operand descriptor, 128-byte swizzle.  K-major: atoms of 8 lines 1024 bytes
@@ -189,6 +202,21 @@ __device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uin
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
+}
+
+// The same with A in tensor memory, two 16-bit elements a column, a line a lane.
+__device__ __forceinline__ void mma_tile_from_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                                   uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+
+// Writes of this thread to shared memory, seen by products issued after what it signals next.
+__device__ __forceinline__ void fence_to_products() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // `bar` (at the same place in each CTA of the pair) gets one arrival when the products
