@@ -60,7 +60,8 @@ struct Layout {
   static constexpr uint32_t kChunk = 128 * 128;            // bytes
   static constexpr uint32_t kTile = kChunks * kChunk;      // 128 rows
   static constexpr uint32_t kKeysAt = 2 * kTile, kValuesAt = kKeysAt + kStages * kTile;
-  static constexpr size_t kBytes = kValuesAt + kStages * kTile + 1024;
+  static constexpr uint32_t kFactorsAt = kValuesAt + kStages * kTile;  // of each operand warp, both operands
+  static constexpr size_t kBytes = kFactorsAt + 4 * 2 * 128 * 4 + 1024;
 };
 
 constexpr uint32_t kScoresAt = 0, kOutAt = 256;  // tensor memory columns; 128 and DIM a tile
@@ -92,6 +93,19 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+
+// Registers a thread from here on, for whole warpgroups: their sum stays what the CTA started with
+// (4 x 128 x 128).
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr int kSoftmaxRegisters = 184, kOperandRegisters = 104, kProductRegisters = 40;
+static_assert(2 * kSoftmaxRegisters + kOperandRegisters + kProductRegisters <= 4 * 128, "what the CTA has");
 
 // 2^e in two factors, for -252 <= e <= 254.
 __device__ __forceinline__ float times_power(float v, int e) {
@@ -133,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
   __shared__ volatile uint32_t issued;  // steps so far: a tile may sit out many
+  __shared__ Walk walks[kThreads / 32][2];  // of each warp: where it stands, and one item ahead
 
   const uint32_t base = (smem_u32(dynamic) + 1023u) & ~1023u;
   uint8_t* memory = dynamic + (base - smem_u32(dynamic));
@@ -152,12 +167,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   const uint32_t tmem = tmem_base;
   pdl_begin();
 
-  Walk walk = find_share<kChunkRows, kKeys>(p, blockIdx.x, gridDim.x, scratch);
+  // (in shared memory: registers are dear, and a step needs little of it)
+  Walk &walk = walks[warp][0], &next = walks[warp][1];
+  {
+    const Walk share = find_share<kChunkRows, kKeys>(p, blockIdx.x, gridDim.x, scratch);
+    if (lane == 0) walk = next = share;
+    __syncwarp();
+  }
+  const auto advance = [&](Walk& w) {
+    __syncwarp();
+    if (lane == 0) next_piece<kChunkRows, kKeys>(p, w);
+    __syncwarp();
+  };
   const auto rows_of = [&](const Walk& w) {  // of the item
     return (int)min((int64_t)kChunkRows, (int64_t)w.s.count * p.group - (int64_t)w.block * kChunkRows);
   };
 
   if (warp < 8) {
+    registers_up<kSoftmaxRegisters>();
     // softmax and output of tile `t`; this thread's row of it is 32 (warp & 3) + lane
     [&] {
       const int t = warp >> 2, quarter = warp & 3, mine = 32 * quarter + lane;
@@ -181,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
 #pragma unroll
             for (int j = 0; j < kOwn / 2; ++j) raw[i][j] = 0;
             if (r < rows) {
-              const int64_t row = (int64_t)w.block * kChunkRows + r;
-              const int token = w.s.row + (int)(row / p.group), head = w.head * p.group + (int)(row % p.group);
+              const int row = w.block * kChunkRows + r;  // (rows times heads fit 31 bits)
+              const int token = w.s.row + row / p.group, head = w.head * p.group + row % p.group;
               const uint32_t* q = (const uint32_t*)((const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + kOwn * lane);
 #pragma unroll
               for (int j = 0; j < kOwn / 2; ++j) raw[i][j] = q[j];
@@ -220,66 +247,64 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         mbar_arrive(&q_full[t], lane == 0);
       };
 
-      Walk next = walk;
       if (walk.left > 0) stage_queries(next);
       while (walk.left > 0) {
         const int count = piece_units(walk), rows = rows_of(walk);
         const bool starts = walk.unit == 0, ends = walk.unit + count == walk.units;
-        next_piece<kChunkRows, kKeys>(p, next);
+        advance(next);
         if (rows <= 128 * t) {
           steps += count;
           if (next.left > 0) stage_queries(next);
-          next_piece<kChunkRows, kKeys>(p, walk);
+          advance(walk);
           continue;
         }
-        const int64_t row = (int64_t)walk.block * kChunkRows + 128 * t + mine;  // of the sequence's with this head
         const bool valid = 128 * t + mine < rows;
-        const Keys seen = valid ? seen_by(p, walk.s, (int)row) : Keys{0, 0x7fffffff};
+        const Keys seen = valid ? seen_by(p, walk.s, walk.block * kChunkRows + 128 * t + mine) : Keys{0, 0x7fffffff};
+        const int first_key = walk.keys.low + walk.unit * kKeys;
         const float scale = row_scale[128 * t + mine];
         float top = -INFINITY;
         float2 total = make_float2(0.f, 0.f);
         int value_ref = 0;
         for (int step = 0; step < count; ++step, ++steps, ++turns) {
-          const int pos = walk.keys.low + (walk.unit + step) * kKeys;
-          // (first the scores: a tile that sits items out may look at the ring long before its step)
-          if (!wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
+          const int pos = first_key + step * kKeys;
+          // (the scores before the first look at the ring: a tile that sits items out would see it long
+          // before its step)
+          if (step == 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
           if (!wait_or_leave(&info_full[steps % kInfos], steps / kInfos & 1, &gave_up)) return;
-          tmem_fence_after();
           const Info& info = infos[steps % kInfos];
           const float c = fmaxf(times_power(scale, info.key_ref - 127), 0x1p-120f);
           const int new_ref = info.value_ref;
           const int from = seen.low - pos, to = seen.high - pos;  // of the step's keys
           const bool special = info.special != 0;
           const bool masked = special || __any_sync(~0u, from > 0 || to < kKeys);
+          if (step > 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
+          tmem_fence_after();
 
-          const auto mask = [&](uint32_t(&v)[32], int at) {
+          uint32_t v[4][32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = at + i;
+          for (int i = 0; i < 4; ++i) tmem_load32(scores + 32 * i, v[i]);
+          tmem_wait_loads();
+          if (masked) {
+#pragma unroll
+            for (int key = 0; key < kKeys; ++key) {
+              uint32_t& x = v[key / 32][key & 31];
               bool see = key >= from && key < to;
               if (special) {
-                see = see && !(info.hidden[i & 3] >> (key >> 2) & 1u);
-                if (info.poison[i & 3] >> (key >> 2) & 1u) v[i] = 0x7fc00000u;
+                see = see && !(info.hidden[key & 3] >> (key >> 2) & 1u);
+                if (info.poison[key & 3] >> (key >> 2) & 1u) x = 0x7fc00000u;
               }
-              if (!see) v[i] = 0xff800000u;
+              if (!see) x = 0xff800000u;
             }
-          };
-          float most = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[32];
-            tmem_load32(scores + 32 * i, v);
-            tmem_wait_loads();
-            if (masked) mask(v, 32 * i);
-            float m[4] = {most, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                m[k] = max3(m[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
-            most = max3(fmaxf(m[0], m[1]), m[2], m[3]);
           }
-          most *= c;  // (c > 0; -inf stays)
+          float m[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m[i] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              m[j / 2 & 7] = max3(m[j / 2 & 7], __uint_as_float(v[i][j]), __uint_as_float(v[i][j + 1]));
+          const float most = max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c;  // (c > 0)
           float less = 1.f;
           bool again = false;
           if (most > top + kLag || top == -INFINITY) {
@@ -287,41 +312,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
             if (again) less = exp2_fast(top - most);
             if (most > top) top = most;
           }
-          if (step > 0 && __any_sync(~0u, again || new_ref != value_ref)) {
-            total.x *= less, total.y *= less;
-            // (moved up by more than 2^7; a smaller unit of nothing yet is no loss)
-            less *= __uint_as_float((uint32_t)max(127 + value_ref - new_ref, 0) << 23);
-#pragma unroll 1
-            for (int i = 0; i < DIM / 32; ++i) {
-              uint32_t v[32];
-              tmem_load32(out + 32 * i, v);
-              tmem_wait_loads();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * less);
-              tmem_store16(out + 32 * i, v);
-              tmem_store16(out + 32 * i + 16, v + 16);
-            }
-          }
-          value_ref = new_ref;
+          const bool moved = step > 0 && __any_sync(~0u, again || new_ref != value_ref);
           const float shift = top == -INFINITY ? 0.f : -top;
           const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-          float2 sums[2] = {total, make_float2(0.f, 0.f)};
+          float2 sums[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sums[i] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t v[32], packed[16];
-            tmem_load32(scores + 32 * i, v);
-            tmem_wait_loads();
-            if (masked) mask(v, 32 * i);
+            uint32_t packed[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              float2 x = fma_pair(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, shift2);
+              float2 x = fma_pair(make_float2(__uint_as_float(v[i][2 * j]), __uint_as_float(v[i][2 * j + 1])), c2, shift2);
               x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
-              sums[j & 1] = add_pair(sums[j & 1], x);
+              sums[j & 3] = add_pair(sums[j & 3], x);
               packed[j] = pair_from_float<__half>(x.x, x.y);
             }
             tmem_store16(scores + 16 * i, packed);
           }
-          total = add_pair(sums[0], sums[1]);
+          if (moved) {  // what is there so far, in the new units
+            total.x *= less, total.y *= less;
+            less *= __uint_as_float((uint32_t)max(127 + value_ref - new_ref, 0) << 23);
+#pragma unroll 1
+            for (int i = 0; i < DIM / 32; ++i) {
+              uint32_t o[32];
+              tmem_load32(out + 32 * i, o);
+              tmem_wait_loads();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * less);
+              tmem_store16(out + 32 * i, o);
+              tmem_store16(out + 32 * i + 16, o + 16);
+            }
+          }
+          value_ref = new_ref;
+          total = add_pair(total, add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])));
           tmem_wait_stores();
           tmem_fence_before();
           __syncwarp();
@@ -335,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         const float l = total.x + total.y;
         if (starts && ends) {
           const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
-          const int token = walk.s.row + (int)(row / p.group), head = walk.head * p.group + (int)(row % p.group);
+          const int row = walk.block * kChunkRows + 128 * t + mine;  // of the sequence's with this head
+          const int token = walk.s.row + row / p.group, head = walk.head * p.group + row % p.group;
           uint16_t* to = (uint16_t*)p.out.p + token * p.out.token + head * p.out.head;
           // (64 of a row's elements at a time: the top bit of 128 first)
 #pragma unroll 1
@@ -390,60 +415,61 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           if (valid) part[kChunkRows * DIM + r] = top, part[kChunkRows * DIM + kChunkRows + r] = l;
         }
         tmem_fence_before();  // (before the next item's products write there, which wait for p_full)
-        next_piece<kChunkRows, kKeys>(p, walk);
+        advance(walk);
       }
     }();
   } else if (warp < 12) {
     // operands: a row of codes is spread over DIM / 16 lanes, 16 bytes each
+    registers_down<kOperandRegisters>();
     [&] {
       constexpr int kLanes = DIM / 16, kRows = 32 / kLanes, kTimes = 128 / (4 * kRows);
       const int w = warp - 8, sub = lane / kLanes, part = lane & (kLanes - 1);
       const CacheView& cache = p.cache;
-      uint32_t steps = 0;
+      uint32_t* factors = (uint32_t*)(memory + L::kFactorsAt) + w * 256;
 
-      Walk ahead = walk;  // the steps whose codes are on their way
-      int ahead_step = 0;
-      uint4 codes[2][kTimes];
-      uint32_t bytes[2];          // scales of tokens 4 lane .. 4 lane + 3
-      int pages = -1;             // lanes 0 to 7: of the coming step's 16 tokens each
-      const auto position = [&](const Walk& at, int step) { return at.keys.low + (at.unit + step) * kKeys; };
-      const auto find_pages = [&] {
-        if (ahead.left <= 0) return;
-        const int pos = position(ahead, ahead_step) + 16 * (lane & 7);
-        pages = pos < ahead.keys.high ? page_of(cache, p.at, ahead.b, pos) : -1;
+      // A step's place.  Its pages are looked up two steps ahead and its codes fetched one ahead.
+      struct Spot {
+        int pos, high, head, page;  // page: lane i's is that of tokens 16 (i & 7) on
+        bool first;                 // of an item
       };
-      // one of a step's two operands
-      const auto fetch = [&](int o) {
-        if (ahead.left <= 0) return;
-        const int pos = position(ahead, ahead_step);
+      int64_t far_left = walk.left;
+      int far_step = 0;
+      const auto look = [&]() -> Spot {
+        Spot at{0, 0, 0, -1, false};
+        if (far_left <= 0) return at;
+        at.pos = walk.keys.low + (walk.unit + far_step) * kKeys, at.high = walk.keys.high;
+        at.head = walk.head, at.first = far_step == 0;
+        const int pos = at.pos + 16 * (lane & 7);
+        if (pos < at.high) at.page = page_of(cache, p.at, walk.b, pos);
+        --far_left;
+        if (++far_step == piece_units(walk)) advance(walk), far_step = 0;
+        return at;
+      };
+      uint4 codes[2][kTimes];
+      uint32_t bytes[2];  // scales of tokens 4 lane .. 4 lane + 3; of no token: 0
+      const auto fetch = [&](const Spot& at, int o) {
+        const int first = (at.pos + 16 * (lane & 7)) % cache.page_tokens + at.head * cache.page_tokens;
         {
-          const int group = lane >> 2, page = __shfl_sync(~0u, pages, group);
-          const int slot = (pos + 16 * group) % cache.page_tokens;
+          const int page = __shfl_sync(~0u, at.page, lane >> 2), token = __shfl_sync(~0u, first, lane >> 2);
           bytes[o] = 0;
           if (page >= 0)
-            bytes[o] = *(const uint32_t*)(cache.scales[o] + page * cache.scale_stride[o] +
-                                          (int64_t)ahead.head * cache.page_tokens + slot + 4 * (lane & 3));
+            bytes[o] = *(const uint32_t*)(cache.scales[o] + page * cache.scale_stride[o] + token + 4 * (lane & 3));
         }
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
           const int row = (4 * i + w) * kRows + sub, group = (4 * i + w) * kRows / 16;
-          const int page = __shfl_sync(~0u, pages, group);
+          const int page = __shfl_sync(~0u, at.page, group), token = __shfl_sync(~0u, first, group) + (row & 15);
           codes[o][i] = make_uint4(0, 0, 0, 0);
-          if (page >= 0 && pos + row < ahead.keys.high) {
-            const int slot = (pos + 16 * group) % cache.page_tokens + (row & 15);
-            codes[o][i] = *(const uint4*)(cache.codes[o] + page * cache.code_stride[o] +
-                                          ((int64_t)ahead.head * cache.page_tokens + slot) * DIM + 16 * part);
-          }
+          if (page >= 0 && at.pos + row < at.high)
+            codes[o][i] = *(const uint4*)(cache.codes[o] + page * cache.code_stride[o] + (int64_t)token * DIM + 16 * part);
         }
       };
-      // the fetched operand into shared memory; scale bytes `scales`, their unit `ref`
-      const auto convert = [&](int o, uint32_t at, uint32_t scales, int ref) {
+      // the fetched operand into shared memory
+      const auto convert = [&](int o, uint32_t at) {
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
           const int row = (4 * i + w) * kRows + sub;
-          const uint32_t four = __shfl_sync(~0u, scales, row >> 2);
-          const int byte = (four >> (8 * (row & 3))) & 255;
-          const uint32_t factor = byte == 255 ? 0u : power_f16x2(min(byte - ref, 7));  // (no token: any byte)
+          const uint32_t factor = factors[128 * o + row];
           const uint32_t c[4] = {codes[o][i].x, codes[o][i].y, codes[o][i].z, codes[o][i].w};
           uint4 v[2];
           v[0] = make_uint4(multiply_f16x2(e4m3_to_f16x2(c[0]), factor), multiply_f16x2(e4m3_to_f16x2(c[0] >> 16), factor),
@@ -464,72 +490,63 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         __syncwarp();
       };
 
-      find_pages();
-      fetch(0), fetch(1);
-      while (walk.left > 0) {
-        const int count = piece_units(walk);
-        int ref[2] = {0, 0};
-        for (int step = 0; step < count; ++step, ++steps) {
-          const int stage = steps % kStages;
-          const uint32_t parity = (steps / kStages & 1) ^ 1;
-          const uint32_t scales[2] = {bytes[0], bytes[1]};
-          // tokens of this lane that are there, and what the softmax has to know
-          uint32_t hidden = 0, poison = 0;  // a bit for each of the four
-          {
-            const int pos = position(walk, step);
-            const int page = __shfl_sync(~0u, pages, lane >> 2);
+      const int64_t all = walk.left;
+      Spot now = look();
+      fetch(now, 0), fetch(now, 1);
+      Spot next = look();
+      int ref[2] = {0, 0};
+      uint32_t steps = 0;
+      for (int64_t left = all; left > 0; --left, ++steps) {
+        const int stage = steps % kStages;
+        const uint32_t parity = (steps / kStages & 1) ^ 1;
+        const Spot then = look();
+        // tokens of this lane that are there; units and factors of the scales
+        const int there = min(max(now.high - now.pos - 4 * lane, 0), 4);
+        const uint32_t valid = there == 4 ? ~0u : (1u << (8 * there)) - 1u;
+        uint32_t bad = 0;  // bytes of tokens that are not numbers
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const uint32_t nan = __vcmpeq4(bytes[o], ~0u) & valid, clean = bytes[o] & valid & ~nan;
+          bad |= nan;
+          uint32_t most = __vmaxu4(clean, clean >> 16);
+          most = __reduce_max_sync(~0u, max(most & 255u, most >> 8 & 255u));
+          if (now.first || (int)most > ref[o] + 7) ref[o] = (int)most;
+          uint32_t f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = power_f16x2((int)(clean >> (8 * j) & 255u) - ref[o]);
+          *(uint4*)(factors + 128 * o + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        __syncwarp();
+        if (w == 0) {
+          Info& info = infos[steps % kInfos];
+          const bool none = __shfl_sync(~0u, now.page, lane >> 2) < 0;
+          const uint32_t special = __ballot_sync(~0u, none || bad);
+          if (special) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const bool there = page >= 0 && pos + 4 * lane + j < walk.keys.high;
-              const uint32_t b0 = scales[0] >> (8 * j) & 255u, b1 = scales[1] >> (8 * j) & 255u;
-              if (page < 0) hidden |= 1u << j;
-              if (there && (b0 == 255u || b1 == 255u)) poison |= 1u << j;
-            }
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              uint32_t most = 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t b = scales[o] >> (8 * j) & 255u;
-                if (page >= 0 && pos + 4 * lane + j < walk.keys.high && b != 255u) most = max(most, b);
-              }
-              most = __reduce_max_sync(~0u, most);
-              if (step == 0 || (int)most > ref[o] + 7) ref[o] = (int)most;
-            }
-          }
-          if (w == 0) {
-            Info& info = infos[steps % kInfos];
-            const uint32_t any = __ballot_sync(~0u, hidden | poison);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t h = __ballot_sync(~0u, hidden >> j & 1u), q = __ballot_sync(~0u, poison >> j & 1u);
+              const uint32_t h = __ballot_sync(~0u, none), q = __ballot_sync(~0u, bad >> (8 * j) & 1u);
               if (lane == 0) info.hidden[j] = h, info.poison[j] = q;
             }
-            // (written when the stage is free: see Info)
-            if (!wait_or_leave(&k_empty[stage], parity, &gave_up)) return;
-            if (lane == 0) info.key_ref = ref[0], info.value_ref = ref[1], info.special = any != 0;
-            __syncwarp();
-            mbar_arrive(&info_full[steps % kInfos], lane == 0);
-          } else {
-            if (!wait_or_leave(&k_empty[stage], parity, &gave_up)) return;
           }
-          convert(0, L::kKeysAt + stage * L::kTile, scales[0], ref[0]);
-          mbar_arrive(&k_full[stage], lane == 0);
-          // on to the next step's codes
-          if (++ahead_step == piece_units(ahead)) next_piece<kChunkRows, kKeys>(p, ahead), ahead_step = 0;
-          find_pages();
-          fetch(0);
-          if (!wait_or_leave(&v_empty[stage], parity, &gave_up)) return;
-          convert(1, L::kValuesAt + stage * L::kTile, scales[1], ref[1]);
-          mbar_arrive(&v_full[stage], lane == 0);
-          fetch(1);
+          if (lane == 0) info.key_ref = ref[0], info.value_ref = ref[1], info.special = special != 0;
+          __syncwarp();
+          mbar_arrive(&info_full[steps % kInfos], lane == 0);
         }
-        next_piece<kChunkRows, kKeys>(p, walk);
+        if (!wait_or_leave(&k_empty[stage], parity, &gave_up)) return;
+        convert(0, L::kKeysAt + stage * L::kTile);
+        mbar_arrive(&k_full[stage], lane == 0);
+        fetch(next, 0);
+        if (!wait_or_leave(&v_empty[stage], parity, &gave_up)) return;
+        convert(1, L::kValuesAt + stage * L::kTile);
+        mbar_arrive(&v_full[stage], lane == 0);
+        fetch(next, 1);
+        now = next, next = then;
       }
     }();
-  } else if (warp == 12) {
-    // products
-    [&] {
+  } else {
+    registers_down<kProductRegisters>();
+    // products, by the first of these warps
+    if (warp == 12) [&] {
       constexpr uint32_t kOfScores = instruction(0, false, false, 128, 128);
       constexpr uint32_t kOfOut = instruction(0, false, true, 128, DIM);
       uint32_t steps = 0, turns[2] = {0, 0}, pieces[2] = {0, 0};
@@ -585,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
             }
           }
         }
-        next_piece<kChunkRows, kKeys>(p, walk);
+        advance(walk);
       }
     }();
   }
@@ -596,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   if (gave_up) drain();
   tmem_fence_after();
   if (warp == 12) tmem_free<1>(tmem, kColumns);
-  // what there is to join (a thread of a warp that has kept its share's start walks it once more)
+  // what there is to join (warp 13 has kept the share's start and walks it once more)
   if (warp == 13) {
     int4 note = make_int4(0, 0, 0, 0);
     while (walk.left > 0) {
@@ -604,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
       const bool starts = walk.unit == 0, ends = walk.unit + count == walk.units;
       if (!starts) note.x |= kNoteHead | (ends ? kNoteHeadEnds : 0);
       else if (!ends) note.x |= kNoteTail, note.y = walk.b, note.z = walk.head, note.w = walk.block;
-      next_piece<kChunkRows, kKeys>(p, walk);
+      advance(walk);
     }
     if (gave_up) note.x &= kNoteHead | kNoteHeadEnds;
     if (lane == 0) p.notes[blockIdx.x] = note;
