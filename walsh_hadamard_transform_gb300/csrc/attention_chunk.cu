@@ -14,13 +14,14 @@
 //
 // Four warps turn codes into float16 operands in the layout the products read (128-byte swizzle; keys
 // along the contraction, values across it).  The scales go in with them, exactly: a key's
-// factor is 2^(e - e_ref), e_ref the largest scale's exponent of the item's first keys, moved only
-// when one is more than 2^7 above it; what lies more than 2^15 below it keeps fewer bits
+// factor is 2^(4 + e - e_ref), e_ref the largest scale's exponent of the item's first keys, moved only
+// when one is more than 2^3 above it; what lies more than 2^19 below it keeps fewer bits
 // (float16's smallest step).  So c is one number a row and the softmax has no scales to look up.
 // Values the same, with O in units of 2^e_ref.  Queries are rounded to float16 once after their rotation,
 // each row at a power of two.
 //
-// Warps: 0 to 3 and 4 to 7 softmax and output of tile 0 and 1, 8 to 11 operands, 12 products.
+// Warps: 0 to 3 and 4 to 7 softmax and output of tile 0 and 1, 8 to 11 operands, 12 products, 13 the
+// pages and scales of the steps ahead, 14 what there is to join.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -42,17 +43,20 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kKeys = 128;    // of a step; a unit of the plan
 constexpr int kStages = 2;    // of keys, and of values
-constexpr int kInfos = 4;     // see Info
+constexpr int kAhead = 4;     // steps known at a time
 constexpr float kLag = 8.f;   // of a row's maximum, in powers of two
 
-// What the softmax has to know of a step's keys.  A ring of four: when step j + 3's is written, the
-// products of step j + 1 have been issued, which came after both tiles' softmax of step j.
-struct Info {
-  int key_ref, value_ref;  // scale bytes that stand for 1 in the operands
-  int special;             // whether any bit below is set
-  uint32_t hidden[4];      // bit i of word j: token 4 i + j is no token
-  uint32_t poison[4];      //                  its key or value is not a number
+// What a step's keys are, found by one warp some steps ahead and kept until its last product.
+struct Step {
+  uint32_t factors[2][kKeys];  // of keys and of values: a power of two, float16 twice
+  const uint8_t* codes[2][8];  // of each 16 tokens of the key head; null: no page
+  int there;                   // tokens of the step that the item has
+  int key_ref, value_ref;      // scale bytes that stand for 2^kRaise in the operands
+  int special;                 // whether any bit below is set
+  uint32_t hidden[4];          // bit i of word j: token 32 j + i is no token
+  uint32_t poison[4];          //                   its key or value is not a number
 };
+constexpr int kRaise = 4;  // the largest scale at first; it may rise to 2^7 before the unit moves
 
 template <int DIM>
 struct Layout {
@@ -60,8 +64,8 @@ struct Layout {
   static constexpr uint32_t kChunk = 128 * 128;            // bytes
   static constexpr uint32_t kTile = kChunks * kChunk;      // 128 rows
   static constexpr uint32_t kKeysAt = 2 * kTile, kValuesAt = kKeysAt + kStages * kTile;
-  static constexpr uint32_t kFactorsAt = kValuesAt + kStages * kTile;  // of each operand warp, both operands
-  static constexpr size_t kBytes = kFactorsAt + 4 * 2 * 128 * 4 + 1024;
+  static constexpr uint32_t kStepsAt = kValuesAt + kStages * kTile;
+  static constexpr size_t kBytes = kStepsAt + kAhead * sizeof(Step) + 1024;
 };
 
 constexpr uint32_t kScoresAt = 0, kOutAt = 256;  // tensor memory columns; 128 and DIM a tile
@@ -104,7 +108,7 @@ template <int N>
 __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-constexpr int kSoftmaxRegisters = 184, kOperandRegisters = 104, kProductRegisters = 40;
+constexpr int kSoftmaxRegisters = 176, kOperandRegisters = 104, kProductRegisters = 56;
 static_assert(2 * kSoftmaxRegisters + kOperandRegisters + kProductRegisters <= 4 * 128, "what the CTA has");
 
 // 2^e in two factors, for -252 <= e <= 254.
@@ -135,13 +139,75 @@ __device__ __forceinline__ void turn_all(float (&v)[N], int r) {
   if (r > 5) turn_own<N, 32>(v);
 }
 
+__device__ __forceinline__ int rows_of(const AttentionParams& p, const Walk& w) {  // of the item
+  return min(kChunkRows, w.s.count * p.group - w.block * kChunkRows);
+}
+
+// The queries of tile `t` of the item where `w` stands: rotated, each row at a power of two, as
+// float16 into the layout that the products read.  By the four warps of the tile, 32 rows each;
+// a row is spread over DIM / 16 lanes.
+template <int DIM>
+__device__ __noinline__ void stage_queries(const AttentionParams& p, const Walk& w, int t, uint8_t* memory,
+                                           float* row_scale, uint64_t* full) {
+  using L = Layout<DIM>;
+  constexpr int kLanes = DIM / 16, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, part = lane & (kLanes - 1);
+  const int row0 = 32 * (threadIdx.x >> 5 & 3) + sub, rows = rows_of(p, w) - 128 * t;
+  if (rows <= 0) return;
+  const float norm = rotation_norm(p.rot_bits) * (p.scale < 0.f ? -1.f : 1.f);
+#pragma unroll 1
+  for (int r = row0; r < row0 + 32; r += kRows) {
+    uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (r < rows) {
+      const int row = w.block * kChunkRows + 128 * t + r;  // (rows times heads fit 31 bits)
+      const int token = w.s.row + quotient(row, p.by_group), head = w.head * p.group + remainder(row, p.by_group);
+      const uint16_t* q = (const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + 8 * part;
+      raw[0] = *(const uint4*)q, raw[1] = *(const uint4*)(q + DIM / 2);
+    }
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = pair_to_float(x[j], p.type);
+        v[8 * k + 2 * j] = f.x, v[8 * k + 2 * j + 1] = f.y;
+      }
+    }
+    turn_spread<DIM>(v, p.rot_bits, part);
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      v[j] *= norm;
+      top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int step = 1; step < kLanes; step *= 2) top = max(top, __shfl_xor_sync(~0u, top, step));
+    const int e = max((int)(top >> 23), 27);  // (zero, and what is nearly so)
+    const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int piece = part + (DIM == 128 ? 0 : 4 * k);
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = pair_from_float<__half>(v[8 * k + 2 * j] * up, v[8 * k + 2 * j + 1] * up);
+      *(uint4*)(memory + t * L::kTile + (DIM == 128 ? k * L::kChunk : 0) + r * 128 + ((piece ^ (r & 7)) << 4)) =
+          make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    if (part == 0) row_scale[128 * t + r] = fabsf(p.scale) * __uint_as_float((uint32_t)(e - 14) << 23);
+  }
+  fence_to_products();
+  __syncwarp();
+  mbar_arrive(full, lane == 0);
+}
+
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const AttentionParams p) {
   using L = Layout<DIM>;
   extern __shared__ uint8_t dynamic[];
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], info_full[kInfos];
-  __shared__ Info infos[kInfos];
+  __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  __shared__ uint64_t known[kAhead], done[kAhead];  // steps that are found, and over
   __shared__ float row_scale[kChunkRows];
   __shared__ PlanScratch<kThreads> scratch;
   __shared__ uint32_t tmem_base;
@@ -151,13 +217,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
 
   const uint32_t base = (smem_u32(dynamic) + 1023u) & ~1023u;
   uint8_t* memory = dynamic + (base - smem_u32(dynamic));
+  Step* const ring = (Step*)(memory + L::kStepsAt);
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t)
       mbar_init(&q_full[t], 4), mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 4), mbar_init(&o_full[t], 1);
     for (int s = 0; s < kStages; ++s)
       mbar_init(&k_full[s], 4), mbar_init(&k_empty[s], 1), mbar_init(&v_full[s], 4), mbar_init(&v_empty[s], 1);
-    for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
+    for (int i = 0; i < kAhead; ++i) mbar_init(&known[i], 1), mbar_init(&done[i], 1);
     gave_up = 0, issued = 0;
   }
   if (warp == 12) tmem_alloc<1>(&tmem_base, kColumns);
@@ -179,10 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
     if (lane == 0) next_piece<kChunkRows, kKeys>(p, w);
     __syncwarp();
   };
-  const auto rows_of = [&](const Walk& w) {  // of the item
-    return (int)min((int64_t)kChunkRows, (int64_t)w.s.count * p.group - (int64_t)w.block * kChunkRows);
-  };
-
   if (warp < 8) {
     registers_up<kSoftmaxRegisters>();
     // softmax and output of tile `t`; this thread's row of it is 32 (warp & 3) + lane
@@ -193,68 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
       uint32_t steps = 0;              // of the share so far
       uint32_t turns = 0, pieces = 0;  // steps and items of this tile
 
-      // the queries of the item where `w` stands, into shared memory
-      const auto stage_queries = [&](const Walk& w) {
-        const int rows = rows_of(w);
-        if (rows <= 128 * t) return;
-        const float norm = rotation_norm(p.rot_bits) * (p.scale < 0.f ? -1.f : 1.f);
-        constexpr int kOwn = DIM / 32, kAhead = 8;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += kAhead) {
-          uint32_t raw[kAhead][kOwn / 2];
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const int r = 128 * t + 32 * quarter + i0 + i;
-#pragma unroll
-            for (int j = 0; j < kOwn / 2; ++j) raw[i][j] = 0;
-            if (r < rows) {
-              const int row = w.block * kChunkRows + r;  // (rows times heads fit 31 bits)
-              const int token = w.s.row + row / p.group, head = w.head * p.group + row % p.group;
-              const uint32_t* q = (const uint32_t*)((const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + kOwn * lane);
-#pragma unroll
-              for (int j = 0; j < kOwn / 2; ++j) raw[i][j] = q[j];
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const int r = 32 * quarter + i0 + i;
-            float v[kOwn];
-#pragma unroll
-            for (int j = 0; j < kOwn / 2; ++j) {
-              const float2 f = pair_to_float(raw[i][j], p.type);
-              v[2 * j] = f.x, v[2 * j + 1] = f.y;
-            }
-            turn_row<DIM>(v, p.rot_bits, lane);
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-              v[j] *= norm;
-              top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
-            }
-            top = __reduce_max_sync(~0u, top);
-            const int e = max((int)(top >> 23), 27);  // (zero, and what is nearly so)
-            const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
-            const int d = kOwn * lane;
-            uint8_t* to = memory + t * L::kTile + (d >> 6) * L::kChunk + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2;
-#pragma unroll
-            for (int j = 0; j < kOwn / 2; ++j)
-              ((uint32_t*)to)[j] = pair_from_float<__half>(v[2 * j] * up, v[2 * j + 1] * up);
-            if (lane == 0) row_scale[128 * t + r] = fabsf(p.scale) * __uint_as_float((uint32_t)(e - 14) << 23);
-          }
-        }
-        fence_to_products();
-        __syncwarp();
-        mbar_arrive(&q_full[t], lane == 0);
-      };
-
-      if (walk.left > 0) stage_queries(next);
+      if (walk.left > 0) stage_queries<DIM>(p, next, t, memory, row_scale, &q_full[t]);
       while (walk.left > 0) {
-        const int count = piece_units(walk), rows = rows_of(walk);
+        const int count = piece_units(walk), rows = rows_of(p, walk);
         const bool starts = walk.unit == 0, ends = walk.unit + count == walk.units;
         advance(next);
         if (rows <= 128 * t) {
           steps += count;
-          if (next.left > 0) stage_queries(next);
+          if (next.left > 0) stage_queries<DIM>(p, next, t, memory, row_scale, &q_full[t]);
           advance(walk);
           continue;
         }
@@ -270,9 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           // (the scores before the first look at the ring: a tile that sits items out would see it long
           // before its step)
           if (step == 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
-          if (!wait_or_leave(&info_full[steps % kInfos], steps / kInfos & 1, &gave_up)) return;
-          const Info& info = infos[steps % kInfos];
-          const float c = fmaxf(times_power(scale, info.key_ref - 127), 0x1p-120f);
+          if (!wait_or_leave(&known[steps % kAhead], steps / kAhead & 1, &gave_up)) return;
+          const Step& info = ring[steps % kAhead];
+          const float c = fmaxf(times_power(scale, info.key_ref - (127 + kRaise)), 0x1p-120f);
           const int new_ref = info.value_ref;
           const int from = seen.low - pos, to = seen.high - pos;  // of the step's keys
           const bool special = info.special != 0;
@@ -286,14 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           tmem_wait_loads();
           if (masked) {
 #pragma unroll
-            for (int key = 0; key < kKeys; ++key) {
-              uint32_t& x = v[key / 32][key & 31];
-              bool see = key >= from && key < to;
-              if (special) {
-                see = see && !(info.hidden[key & 3] >> (key >> 2) & 1u);
-                if (info.poison[key & 3] >> (key >> 2) & 1u) x = 0x7fc00000u;
+            for (int i = 0; i < 4; ++i) {
+              // bits of keys 32 i on: those below `to`, less those below `from`
+              const int low = min(max(from - 32 * i, 0), 32), high = min(max(to - 32 * i, 0), 32);
+              uint32_t see = (uint32_t)((1ull << high) - 1) & ~(uint32_t)((1ull << low) - 1);
+              uint32_t poison = 0;
+              if (special) see &= ~info.hidden[i], poison = info.poison[i] & see;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[i][j] = see & 1u << j ? v[i][j] : 0xff800000u;
+              if (__any_sync(~0u, poison != 0)) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[i][j] = poison & 1u << j ? 0x7fc00000u : v[i][j];
               }
-              if (!see) x = 0xff800000u;
             }
           }
           float m[8];
@@ -352,15 +365,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           mbar_arrive(&p_full[t], lane == 0);
         }
         // the next item's queries while this one's last products run
-        if (next.left > 0) stage_queries(next);
+        if (next.left > 0) stage_queries<DIM>(p, next, t, memory, row_scale, &q_full[t]);
         if (!wait_or_leave(&o_full[t], pieces & 1, &gave_up)) return;
         ++pieces;
         tmem_fence_after();
         const float l = total.x + total.y;
+        // 2^e, e from -131 to 123, in two factors
+        const int e = value_ref - (127 + kRaise), half_e = e >> 1;
+        const float units[2] = {__uint_as_float((uint32_t)(127 + half_e) << 23), __uint_as_float((uint32_t)(127 + e - half_e) << 23)};
         if (starts && ends) {
           const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
+          const float unit[2] = {norm * units[0], units[1]};
           const int row = walk.block * kChunkRows + 128 * t + mine;  // of the sequence's with this head
-          const int token = walk.s.row + row / p.group, head = walk.head * p.group + row % p.group;
+          const int token = walk.s.row + quotient(row, p.by_group), head = walk.head * p.group + remainder(row, p.by_group);
           uint16_t* to = (uint16_t*)p.out.p + token * p.out.token + head * p.out.head;
           // (64 of a row's elements at a time: the top bit of 128 first)
 #pragma unroll 1
@@ -384,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
             }
             turn_all(o, p.rot_bits);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) o[j] = times_power(o[j] * norm, value_ref - 127);
+            for (int j = 0; j < 64; ++j) o[j] = o[j] * unit[0] * unit[1];
             if (valid) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
@@ -407,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
               for (int j = 0; j < 8; ++j) {
                 float o[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = times_power(__uint_as_float(v[4 * j + k]), value_ref - 127);
+                for (int k = 0; k < 4; ++k) o[k] = __uint_as_float(v[4 * j + k]) * units[0] * units[1];
                 to[j] = make_float4(o[0], o[1], o[2], o[3]);
               }
             }
@@ -419,71 +436,46 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
       }
     }();
   } else if (warp < 12) {
-    // operands: a row of codes is spread over DIM / 16 lanes, 16 bytes each
+    // operands: a row of codes is spread over DIM / 16 lanes, 16 bytes each: two runs of 8, half a
+    // row apart (64: one of 16), so that eight lanes' stores meet all banks
     registers_down<kOperandRegisters>();
     [&] {
       constexpr int kLanes = DIM / 16, kRows = 32 / kLanes, kTimes = 128 / (4 * kRows);
+      constexpr int kApart = DIM == 128 ? 64 : 8;  // bytes between a lane's two runs
       const int w = warp - 8, sub = lane / kLanes, part = lane & (kLanes - 1);
-      const CacheView& cache = p.cache;
-      uint32_t* factors = (uint32_t*)(memory + L::kFactorsAt) + w * 256;
-
-      // A step's place.  Its pages are looked up two steps ahead and its codes fetched one ahead.
-      struct Spot {
-        int pos, high, head, page;  // page: lane i's is that of tokens 16 (i & 7) on
-        bool first;                 // of an item
-      };
-      int64_t far_left = walk.left;
-      int far_step = 0;
-      const auto look = [&]() -> Spot {
-        Spot at{0, 0, 0, -1, false};
-        if (far_left <= 0) return at;
-        at.pos = walk.keys.low + (walk.unit + far_step) * kKeys, at.high = walk.keys.high;
-        at.head = walk.head, at.first = far_step == 0;
-        const int pos = at.pos + 16 * (lane & 7);
-        if (pos < at.high) at.page = page_of(cache, p.at, walk.b, pos);
-        --far_left;
-        if (++far_step == piece_units(walk)) advance(walk), far_step = 0;
-        return at;
-      };
-      uint4 codes[2][kTimes];
-      uint32_t bytes[2];  // scales of tokens 4 lane .. 4 lane + 3; of no token: 0
-      const auto fetch = [&](const Spot& at, int o) {
-        const int first = (at.pos + 16 * (lane & 7)) % cache.page_tokens + at.head * cache.page_tokens;
-        {
-          const int page = __shfl_sync(~0u, at.page, lane >> 2), token = __shfl_sync(~0u, first, lane >> 2);
-          bytes[o] = 0;
-          if (page >= 0)
-            bytes[o] = *(const uint32_t*)(cache.scales[o] + page * cache.scale_stride[o] + token + 4 * (lane & 3));
-        }
+      const int row0 = w * kRows + sub;  // and every 4 kRows on, a multiple of 16
+      const int code_at = (row0 & 15) * DIM + part * (DIM == 128 ? 8 : 16);
+      // where the two runs go: pieces of 16 bytes, swizzled by row
+      uint32_t to[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int piece = DIM == 128 ? part : 2 * part + k;
+        to[k] = (DIM == 128 ? k * L::kChunk : 0) + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+      }
+      uint2 codes[2][kTimes][2];
+      const auto fetch = [&](const Step& at, int o) {
+        const int there = at.there;
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
-          const int row = (4 * i + w) * kRows + sub, group = (4 * i + w) * kRows / 16;
-          const int page = __shfl_sync(~0u, at.page, group), token = __shfl_sync(~0u, first, group) + (row & 15);
-          codes[o][i] = make_uint4(0, 0, 0, 0);
-          if (page >= 0 && at.pos + row < at.high)
-            codes[o][i] = *(const uint4*)(cache.codes[o] + page * cache.code_stride[o] + (int64_t)token * DIM + 16 * part);
+          const uint8_t* from = at.codes[o][(4 * i + w) * kRows / 16];
+          codes[o][i][0] = codes[o][i][1] = make_uint2(0, 0);
+          if (from && row0 + 4 * kRows * i < there) {
+            from += code_at;
+            codes[o][i][0] = *(const uint2*)from, codes[o][i][1] = *(const uint2*)(from + kApart);
+          }
         }
       };
       // the fetched operand into shared memory
-      const auto convert = [&](int o, uint32_t at) {
+      const auto convert = [&](const Step& at, int o, uint32_t tile) {
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
-          const int row = (4 * i + w) * kRows + sub;
-          const uint32_t factor = factors[128 * o + row];
-          const uint32_t c[4] = {codes[o][i].x, codes[o][i].y, codes[o][i].z, codes[o][i].w};
-          uint4 v[2];
-          v[0] = make_uint4(multiply_f16x2(e4m3_to_f16x2(c[0]), factor), multiply_f16x2(e4m3_to_f16x2(c[0] >> 16), factor),
-                            multiply_f16x2(e4m3_to_f16x2(c[1]), factor), multiply_f16x2(e4m3_to_f16x2(c[1] >> 16), factor));
-          v[1] = make_uint4(multiply_f16x2(e4m3_to_f16x2(c[2]), factor), multiply_f16x2(e4m3_to_f16x2(c[2] >> 16), factor),
-                            multiply_f16x2(e4m3_to_f16x2(c[3]), factor), multiply_f16x2(e4m3_to_f16x2(c[3] >> 16), factor));
-          // (lanes of the second 64 elements write their pieces in the other order: eight lanes
-          // then meet all banks)
-          const int first = part >> 2, piece = 2 * (part & 3);
-          uint8_t* to = memory + at + (part >> 2) * L::kChunk + row * 128;
+          const uint32_t factor = at.factors[o][row0 + 4 * kRows * i];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int which = k ^ first;
-            *(uint4*)(to + (((piece + which) ^ (row & 7)) << 4)) = which ? v[1] : v[0];
+            const uint2 c = codes[o][i][k];
+            *(uint4*)(memory + tile + to[k] + 4 * kRows * 128 * i) =
+                make_uint4(multiply_f16x2(e4m3_to_f16x2(c.x), factor), multiply_f16x2(e4m3_to_f16x2(c.x >> 16), factor),
+                           multiply_f16x2(e4m3_to_f16x2(c.y), factor), multiply_f16x2(e4m3_to_f16x2(c.y >> 16), factor));
           }
         }
         fence_to_products();
@@ -491,56 +483,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
       };
 
       const int64_t all = walk.left;
-      Spot now = look();
-      fetch(now, 0), fetch(now, 1);
-      Spot next = look();
-      int ref[2] = {0, 0};
+      if (all == 0 || !wait_or_leave(&known[0], 0, &gave_up)) return;
+      fetch(ring[0], 0), fetch(ring[0], 1);
       uint32_t steps = 0;
       for (int64_t left = all; left > 0; --left, ++steps) {
         const int stage = steps % kStages;
         const uint32_t parity = (steps / kStages & 1) ^ 1;
-        const Spot then = look();
-        // tokens of this lane that are there; units and factors of the scales
-        const int there = min(max(now.high - now.pos - 4 * lane, 0), 4);
-        const uint32_t valid = there == 4 ? ~0u : (1u << (8 * there)) - 1u;
-        uint32_t bad = 0;  // bytes of tokens that are not numbers
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const uint32_t nan = __vcmpeq4(bytes[o], ~0u) & valid, clean = bytes[o] & valid & ~nan;
-          bad |= nan;
-          uint32_t most = __vmaxu4(clean, clean >> 16);
-          most = __reduce_max_sync(~0u, max(most & 255u, most >> 8 & 255u));
-          if (now.first || (int)most > ref[o] + 7) ref[o] = (int)most;
-          uint32_t f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = power_f16x2((int)(clean >> (8 * j) & 255u) - ref[o]);
-          *(uint4*)(factors + 128 * o + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
-        }
-        __syncwarp();
-        if (w == 0) {
-          Info& info = infos[steps % kInfos];
-          const bool none = __shfl_sync(~0u, now.page, lane >> 2) < 0;
-          const uint32_t special = __ballot_sync(~0u, none || bad);
-          if (special) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t h = __ballot_sync(~0u, none), q = __ballot_sync(~0u, bad >> (8 * j) & 1u);
-              if (lane == 0) info.hidden[j] = h, info.poison[j] = q;
-            }
-          }
-          if (lane == 0) info.key_ref = ref[0], info.value_ref = ref[1], info.special = special != 0;
-          __syncwarp();
-          mbar_arrive(&info_full[steps % kInfos], lane == 0);
-        }
+        const Step &now = ring[steps % kAhead], &next = ring[(steps + 1) % kAhead];
         if (!wait_or_leave(&k_empty[stage], parity, &gave_up)) return;
-        convert(0, L::kKeysAt + stage * L::kTile);
+        convert(now, 0, L::kKeysAt + stage * L::kTile);
         mbar_arrive(&k_full[stage], lane == 0);
-        fetch(next, 0);
+        if (left > 1) {
+          if (!wait_or_leave(&known[(steps + 1) % kAhead], (steps + 1) / kAhead & 1, &gave_up)) return;
+          fetch(next, 0);
+        }
         if (!wait_or_leave(&v_empty[stage], parity, &gave_up)) return;
-        convert(1, L::kValuesAt + stage * L::kTile);
+        convert(now, 1, L::kValuesAt + stage * L::kTile);
         mbar_arrive(&v_full[stage], lane == 0);
-        fetch(next, 1);
-        now = next, next = then;
+        if (left > 1) fetch(next, 1);
       }
     }();
   } else {
@@ -563,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         __syncwarp();
       };
       while (walk.left > 0) {
-        const int count = piece_units(walk), tiles = rows_of(walk) > 128 ? 2 : 1;
+        const int count = piece_units(walk), tiles = rows_of(p, walk) > 128 ? 2 : 1;
         if (!wait_or_leave(&k_full[steps % kStages], steps / kStages & 1, &gave_up)) return;
         for (int t = 0; t < tiles; ++t) {
           if (!wait_or_leave(&q_full[t], pieces[t] & 1, &gave_up)) return;
@@ -588,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
               for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 rows of values, 8 columns of pairs of P
                 mma_tile_from_tmem(tmem + kOutAt + DIM * t, tmem + kScoresAt + 128 * t + 8 * kk, b + kk * 128,
                                    kOfOut, step + kk > 0);
-              if (t + 1 == tiles) mma_commit<1>(&v_empty[stage]);
+              if (t + 1 == tiles) mma_commit<1>(&v_empty[stage]), mma_commit<1>(&done[steps % kAhead]);
               if (!more) mma_commit<1>(&o_full[t]);
             }
             __syncwarp();
@@ -605,6 +565,83 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         advance(walk);
       }
     }();
+    // what the steps are, by the second
+    if (warp == 13) [&] {
+      const CacheView& cache = p.cache;
+      // A step's place: lane i has the page of tokens 16 (i & 7) on, and where they start in it.  Found
+      // two steps ahead, and its scales read one ahead.
+      struct Spot {
+        int there, page, token;
+        bool first;  // of an item
+      };
+      int64_t far_left = walk.left;
+      const int64_t all = far_left;
+      int far_step = 0;
+      const auto look = [&]() -> Spot {
+        Spot at{0, -1, 0, false};
+        if (far_left <= 0) return at;
+        const int from = walk.keys.low + (walk.unit + far_step) * kKeys;
+        at.there = min(walk.keys.high - from, kKeys), at.first = far_step == 0;
+        const int pos = from + 16 * (lane & 7);
+        if (pos < walk.keys.high) at.page = page_of(cache, p.at, walk.b, pos);
+        at.token = remainder(pos, cache.by_page) + walk.head * cache.page_tokens;
+        --far_left;
+        if (++far_step == piece_units(walk)) advance(walk), far_step = 0;
+        return at;
+      };
+      uint32_t bytes[2];  // scales of tokens 4 lane .. 4 lane + 3
+      const auto read_scales = [&](const Spot& at) {
+        const int page = __shfl_sync(~0u, at.page, lane >> 2), token = __shfl_sync(~0u, at.token, lane >> 2);
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+          bytes[o] = page < 0 ? 0
+                              : *(const uint32_t*)(cache.scales[o] + page * cache.scale_stride[o] + token + 4 * (lane & 3));
+      };
+      Spot now = look(), next = look();
+      read_scales(now);
+      int ref[2] = {0, 0};
+      uint32_t steps = 0;
+      for (int64_t left = all; left > 0; --left, ++steps) {
+        Step& to = ring[steps % kAhead];
+        const Spot then = look();
+        const uint32_t read[2] = {bytes[0], bytes[1]};
+        read_scales(next);
+        if (!wait_or_leave(&done[steps % kAhead], (steps / kAhead & 1) ^ 1, &gave_up)) return;
+        const int there = min(max(now.there - 4 * lane, 0), 4);
+        const uint32_t valid = there == 4 ? ~0u : (1u << (8 * there)) - 1u;
+        uint32_t bad = 0;  // bytes of tokens that are not numbers
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const uint32_t nan = __vcmpeq4(read[o], ~0u) & valid, clean = read[o] & valid & ~nan;
+          bad |= nan;
+          uint32_t most = __vmaxu4(clean, clean >> 16);
+          most = __reduce_max_sync(~0u, max(most & 255u, most >> 8 & 255u));
+          if (now.first || (int)most > ref[o] + 7 - kRaise) ref[o] = (int)most;
+          uint32_t f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = power_f16x2((int)(clean >> (8 * j) & 255u) - ref[o] + kRaise);
+          *(uint4*)(to.factors[o] + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+          if (lane < 8)
+            to.codes[o][lane] = now.page < 0 ? nullptr : cache.codes[o] + now.page * cache.code_stride[o] + (int64_t)now.token * DIM;
+        }
+        const bool none = __shfl_sync(~0u, now.page, lane >> 2) < 0 && 16 * (lane >> 2) < now.there;
+        const uint32_t special = __ballot_sync(~0u, none || bad);
+        if (special) {
+          // four bits of a lane's tokens each, eight lanes a word
+          uint32_t h = none ? 0xfu : 0u, q = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q |= (bad >> (8 * j) & 1u) << j;
+          h <<= 4 * (lane & 7), q <<= 4 * (lane & 7);
+#pragma unroll
+          for (int o = 1; o < 8; o *= 2) h |= __shfl_xor_sync(~0u, h, o), q |= __shfl_xor_sync(~0u, q, o);
+          if ((lane & 7) == 0) to.hidden[lane >> 3] = h, to.poison[lane >> 3] = q;
+        }
+        if (lane == 0) to.there = now.there, to.key_ref = ref[0], to.value_ref = ref[1], to.special = special != 0;
+        __syncwarp();
+        mbar_arrive(&known[steps % kAhead], lane == 0);
+        now = next, next = then;
+      }
+    }();
   }
 
   __syncwarp();
@@ -613,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   if (gave_up) drain();
   tmem_fence_after();
   if (warp == 12) tmem_free<1>(tmem, kColumns);
-  // what there is to join (warp 13 has kept the share's start and walks it once more)
-  if (warp == 13) {
+  // what there is to join (warp 14 has kept the share's start and walks it once more)
+  if (warp == 14) {
     int4 note = make_int4(0, 0, 0, 0);
     while (walk.left > 0) {
       const int count = piece_units(walk);

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams
   }
   turn_row<DIM>(v, p.rot_bits, lane);
   const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
-  const int token = s.row + (int)(row / p.group), head = note.z * p.group + (int)(row % p.group);
+  const int token = s.row + quotient((int)row, p.by_group), head = note.z * p.group + remainder((int)row, p.by_group);
   uint32_t* out = (uint32_t*)((uint16_t*)p.out.p + token * p.out.token + head * p.out.head + kOwn * lane);
 #pragma unroll
   for (int j = 0; j < kOwn / 2; ++j) out[j] = pair_from_float(v[2 * j] * norm, v[2 * j + 1] * norm, p.type);

@@ -32,13 +32,14 @@ struct Keys {
 
 template <int ROWS>
 __device__ __forceinline__ int blocks_of(const AttentionParams& p, const Sequence& s) {
-  return (int)(((int64_t)s.count * p.group + ROWS - 1) / ROWS);
+  return (s.count * p.group + ROWS - 1) / ROWS;
 }
 
 template <int ROWS>
 __device__ __forceinline__ Keys keys_of(const AttentionParams& p, const Sequence& s, int block) {
-  const int first = (int)((int64_t)block * ROWS / p.group);
-  const int last = min(s.count - 1, (int)(((int64_t)(block + 1) * ROWS - 1) / p.group));
+  // (rows and a block more fit 31 bits)
+  const int first = quotient(block * ROWS, p.by_group);
+  const int last = min(s.count - 1, quotient(block * ROWS + ROWS - 1, p.by_group));
   const int own = s.length - s.count;  // position of the first new token
   Keys k;
   k.high = p.causal ? min(s.length, max(own + last + 1, 0)) : s.length;
@@ -52,6 +53,8 @@ __device__ __forceinline__ int units_of(const Keys& k) {
 }
 
 // Units of one key head of the sequences of a warp's lanes (sequence b in each; count 0: none).
+// (What runs once or once an item is kept out of line: a kernel's loops have to stay in the instruction
+// cache.  Inlined throughout, the kernels were of 150 and 320 KB, and four times as slow.)
 template <int ROWS, int UNIT>
 __device__ __forceinline__ int64_t units_of_sequence(const AttentionParams& p, const Sequence& s, int lane) {
   constexpr int kAlone = 4;  // blocks that a lane counts by itself
@@ -204,7 +207,7 @@ __device__ __forceinline__ void next_piece(const AttentionParams& p, Walk& w) {
 
 // What keys row `r` (a new token and query head of the sequence) sees: [low, high).
 __device__ __forceinline__ Keys seen_by(const AttentionParams& p, const Sequence& s, int r) {
-  const int own = s.length - s.count + r / p.group;
+  const int own = s.length - s.count + quotient(r, p.by_group);
   Keys k;
   k.high = p.causal ? min(s.length, max(own + 1, 0)) : s.length;
   k.low = p.window ? max(own + 1 - p.window, 0) : 0;

@@ -87,11 +87,12 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 }
 
 template <int DIM, int NT>
-__global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const AttentionParams p) {
   using L = Layout<DIM, NT>;
   constexpr int kRows = L::kRows, kTiles = DIM / 16;
   extern __shared__ __align__(16) uint8_t memory[];
   __shared__ PlanScratch<kThreads> scratch;
+  __shared__ Walk walks[kWarps][2];  // of each warp: where it stands, and where its copies do
   __shared__ float row_scale[kRows];
   __shared__ float tops[kWarps][kRows], totals[kWarps][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -102,36 +103,51 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
   const CacheView& cache = p.cache;
   pdl_begin();
 
-  Walk walk = find_share<kRows, kUnit>(p, blockIdx.x, gridDim.x, scratch);
+  // (in shared memory: a step needs little of them)
+  Walk &walk = walks[warp][0], &ahead = walks[warp][1];
+  {
+    const Walk share = find_share<kRows, kUnit>(p, blockIdx.x, gridDim.x, scratch);
+    if (lane == 0) walk = ahead = share;
+    __syncwarp();
+  }
   if (walk.left == 0) {
     if (threadIdx.x == 0) p.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
+  const auto advance = [&](Walk& w) {
+    __syncwarp();
+    if (lane == 0) next_piece<kRows, kUnit>(p, w);
+    __syncwarp();
+  };
 
-  // The warp's copies run ahead of its work, over items as well.
-  Walk ahead = walk;
-  int next = warp * kStep;  // of the present piece of `ahead`, in tokens
-  uint32_t present = 0;     // two bits a stage in flight: whether its halves have a page
-  int pages = -1;           // lanes 0 and 1: the pages of the next step's halves
-  auto settle = [&] {       // to a piece with a step for this warp, and its pages
-    while (ahead.left > 0) {
-      const int from = ahead.keys.low + ahead.unit * kUnit;
-      const int to = min(from + piece_units(ahead) * kUnit, ahead.keys.high);
-      if (from + next < to) {
-        const int pos = from + next + 16 * (lane & 1);
-        pages = pos < to ? page_of(cache, p.at, ahead.b, pos) : -1;
+  // The warp's copies run ahead of its work, over items as well: where the next one starts, and ends.
+  int pos_ahead = 0, to_ahead = 0, head_ahead = 0;
+  bool some = true;       // whether there is a next one
+  bool fresh = true;      // whether `ahead` is at an item that this warp has not looked at
+  uint32_t present = 0;   // two bits a stage in flight: whether its halves have a page
+  int pages = -1;         // lanes 0 and 1: the pages of the next step's halves
+  const auto settle = [&] {
+    while (true) {
+      if (fresh) {
+        const int from = ahead.keys.low + ahead.unit * kUnit;
+        to_ahead = min(from + piece_units(ahead) * kUnit, ahead.keys.high);
+        pos_ahead = from + warp * kStep, head_ahead = ahead.head, fresh = false;
+      }
+      if (pos_ahead < to_ahead) break;
+      advance(ahead);
+      fresh = true;
+      if (ahead.left <= 0) {
+        some = false;
         return;
       }
-      next_piece<kRows, kUnit>(p, ahead);
-      next = warp * kStep;
     }
+    const int pos = pos_ahead + 16 * (lane & 1);
+    pages = pos < to_ahead ? page_of(cache, p.at, ahead.b, pos) : -1;
   };
-  auto fill = [&](int stage) {
+  const auto fill = [&](int stage) {
     uint32_t bits = 0;
-    if (ahead.left > 0) {
-      const int from = ahead.keys.low + ahead.unit * kUnit;
-      const int to = min(from + piece_units(ahead) * kUnit, ahead.keys.high);
-      const int pos = from + next;
+    if (some) {
+      const int pos = pos_ahead, to = to_ahead;
       const uint32_t at = ring_at + stage * L::kStage;
       constexpr int kPieces = DIM / 16, kRowsAtOnce = 32 / kPieces;
       const int piece = lane & (kPieces - 1), row0 = lane / kPieces;
@@ -139,16 +155,16 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
       for (int half = 0; half < 2; ++half) {
         const int page = __shfl_sync(~0u, pages, half);
         if (page >= 0) bits |= 1u << half;
-        const int64_t token = (int64_t)ahead.head * cache.page_tokens + (pos + 16 * half) % cache.page_tokens;
+        const int64_t token = (int64_t)head_ahead * cache.page_tokens + remainder(pos + 16 * half, cache.by_page);
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          const uint8_t* codes = cache.codes[o] + page * cache.code_stride[o] + token * DIM + 16 * piece;
+          const uint8_t* codes = cache.codes[o] + page * cache.code_stride[o] + (token + row0) * DIM + 16 * piece;
 #pragma unroll
           for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
             const int row = i * kRowsAtOnce + row0;
             const bool there = page >= 0 && pos + 16 * half + row < to;
             copy16(at + (o ? L::kValues : 0) + piece_at<DIM>(16 * half + row, piece),
-                   there ? (const void*)(codes + row * DIM) : p.parts, there);
+                   there ? (const void*)(codes + i * kRowsAtOnce * DIM) : p.parts, there);
           }
           if (lane == o)
             copy16(at + (o ? L::kValueScales : L::kKeyScales) + 16 * half,
@@ -156,14 +172,14 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
                    page >= 0);
         }
       }
-      next += kWarps * kStep;
+      pos_ahead += kWarps * kStep;
       settle();
     }
     present |= bits << (2 * (L::kStages - 1));
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   settle();
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < L::kStages; ++s) {
     if (s) present >>= 2;
     fill(s);
@@ -171,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
 
   int stage = 0, flags = 0;
   int4 note = make_int4(0, 0, 0, 0);
-  for (bool first_piece = true; walk.left > 0; first_piece = false) {
+  while (walk.left > 0) {
     const int piece = piece_units(walk);
     const bool starts = walk.unit == 0, ends = walk.unit + piece == walk.units;
     const int from = walk.keys.low + walk.unit * kUnit;
@@ -186,8 +202,8 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) v[i] = 0.f;
       if (r < rows) {
-        const int token = walk.s.row + (row0 + r) / p.group;
-        const int head = walk.head * p.group + (row0 + r) % p.group;
+        const int token = walk.s.row + quotient(row0 + r, p.by_group);
+        const int head = walk.head * p.group + remainder(row0 + r, p.by_group);
         const uint32_t* q = (const uint32_t*)((const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + kOwn * lane);
 #pragma unroll
         for (int i = 0; i < kOwn / 2; ++i) {
@@ -439,8 +455,8 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
       if (whole) {
         const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
         turn_row<DIM>(v, p.rot_bits, lane);
-        const int token = walk.s.row + (row0 + r) / p.group;
-        const int head = walk.head * p.group + (row0 + r) % p.group;
+        const int token = walk.s.row + quotient(row0 + r, p.by_group);
+        const int head = walk.head * p.group + remainder(row0 + r, p.by_group);
         uint32_t* to_out = (uint32_t*)((uint16_t*)p.out.p + token * p.out.token + head * p.out.head + kOwn * lane);
 #pragma unroll
         for (int i = 0; i < kOwn / 2; ++i) to_out[i] = pair_from_float(v[2 * i] * norm, v[2 * i + 1] * norm, p.type);
@@ -454,7 +470,7 @@ __global__ void __launch_bounds__(kThreads) attention_tokens_kernel(const Attent
       if (!starts) flags |= kNoteHead | (ends ? kNoteHeadEnds : 0);
       else flags |= kNoteTail, note.y = walk.b, note.z = walk.head, note.w = walk.block;
     }
-    next_piece<kRows, kUnit>(p, walk);
+    advance(walk);
     __syncthreads();  // (the sums and queries are read)
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");

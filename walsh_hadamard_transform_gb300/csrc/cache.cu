@@ -55,22 +55,9 @@ __device__ __forceinline__ bool locate(const MoveParams& p, int row, int b, int&
   const int pos = s.length - (s.row + s.count - row);
   if (pos >= 0) {
     page = page_of(p.cache, p.at, b, pos);
-    slot = pos % p.cache.page_tokens;
+    slot = remainder(pos, p.cache.by_page);
   }
   return true;
-}
-
-// The rotation of a row over DIM / 16 lanes, 8 elements from `lane * 8` and 8 half a row on.
-template <int DIM>
-__device__ __forceinline__ void turn(float (&v)[16], int r, int lane) {
-  constexpr int kBits = DIM == 128 ? 7 : 6;
-  if (r > 0) turn_own<16, 1>(v);
-  if (r > 1) turn_own<16, 2>(v);
-  if (r > 2) turn_own<16, 4>(v);
-#pragma unroll
-  for (int bit = 3; bit < kBits - 1; ++bit)
-    if (r > bit) turn_lanes(v, 1 << (bit - 3), lane);
-  if (r == kBits) turn_own<16, 8>(v);
 }
 
 template <typename T>
@@ -131,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
     if (r) {  // 1/16 first, so that no sum of 128 overflows before the norm
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[o][i] *= 0.0625f;
-      turn<DIM>(v[o], r, lane);
+      turn_spread<DIM>(v[o], r, lane);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[o][i] *= norm;
     }
@@ -191,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const MoveParams p) {
       const float2 hi = pair_to_float<__half>(e4m3_to_f16x2(q >> 16));
       v[4 * i] = lo.x, v[4 * i + 1] = lo.y, v[4 * i + 2] = hi.x, v[4 * i + 3] = hi.y;
     }
-    turn<DIM>(v, r, lane);  // of codes: their sums are exact or nearly so
+    turn_spread<DIM>(v, r, lane);  // of codes: their sums are exact or nearly so
     const float scale = scale_value(byte[o]);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = v[i] * norm * scale;

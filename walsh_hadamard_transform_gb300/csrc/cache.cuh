@@ -22,11 +22,28 @@
 namespace fwt {
 namespace ff {
 
+// Division by a number that the host knows, of 0 <= n < 2^31: with 2^s >= d > 2^(s-1) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (floor(n m / 2^32) + n) / 2^s, rounded down (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
+struct Divisor {
+  uint32_t d, multiplier, shift;
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while (s < 31 && (1u << s) < d) ++s;
+  return {d, (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1), s};
+}
+__device__ __forceinline__ int quotient(int n, const Divisor& by) {
+  return (int)((__umulhi((uint32_t)n, by.multiplier) + (uint32_t)n) >> by.shift);
+}
+__device__ __forceinline__ int remainder(int n, const Divisor& by) { return n - quotient(n, by) * (int)by.d; }
+
 struct CacheView {
   uint8_t* codes[2];  // keys, values
   uint8_t* scales[2];
   int64_t code_stride[2], scale_stride[2];  // bytes from page to page
   int pages, heads, page_tokens;
+  Divisor by_page;  // page_tokens
 };
 
 struct Places {
@@ -48,6 +65,7 @@ struct AttentionParams {
   Places at;
   Rows q, out;
   int type, group, dim, rot_bits;
+  Divisor by_group;
   float scale;   // of the scores, times log2(e)
   int causal, window;
   float* parts;  // see attention_plan.cuh
@@ -86,7 +104,7 @@ __device__ __forceinline__ Sequence sequence(const Places& at, int pages_tokens,
 
 // The page of token `pos` (below the sequence's length), -1 where there is none.
 __device__ __forceinline__ int page_of(const CacheView& c, const Places& at, int b, int pos) {
-  const int page = at.table[(int64_t)b * at.ld_table + pos / c.page_tokens];
+  const int page = at.table[(int64_t)b * at.ld_table + quotient(pos, c.by_page)];
   return (unsigned)page < (unsigned)c.pages ? page : -1;
 }
 
@@ -171,6 +189,19 @@ __device__ __forceinline__ void turn_lanes(float (&v)[N], int step, int lane) {
   const float sign = lane & step ? -1.f : 1.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = fmaf(sign, v[i], __shfl_xor_sync(~0u, v[i], step));
+}
+
+// A row over DIM / 16 lanes, each with 8 elements from 8 `lane` on and 8 half a row on: without the norm.
+template <int DIM>
+__device__ __forceinline__ void turn_spread(float (&v)[16], int r, int lane) {
+  constexpr int kBits = DIM == 128 ? 7 : 6;
+  if (r > 0) turn_own<16, 1>(v);
+  if (r > 1) turn_own<16, 2>(v);
+  if (r > 2) turn_own<16, 4>(v);
+#pragma unroll
+  for (int bit = 3; bit < kBits - 1; ++bit)
+    if (r > bit) turn_lanes(v, 1 << (bit - 3), lane);
+  if (r == kBits) turn_own<16, 8>(v);
 }
 
 // A row of DIM over the 32 lanes of a warp, DIM / 32 consecutive elements each, without the norm.

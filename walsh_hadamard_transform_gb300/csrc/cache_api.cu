@@ -100,6 +100,7 @@ int check_cache(const fwt_cache* c, Call& call) {
     call.view.code_stride[o] = strides[o][0], call.view.scale_stride[o] = strides[o][1];
   }
   call.view.pages = (int)c->pages, call.view.heads = c->heads, call.view.page_tokens = c->page_tokens;
+  call.view.by_page = divisor((uint32_t)c->page_tokens);
   return straight ? FWT_OK : FWT_ERR_MISALIGNED;
 }
 
@@ -249,7 +250,7 @@ int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* ou
     if (!apart(spans[1], c) || !apart(work, c)) return FWT_ERR_INVALID_ARG;
   AttentionParams p;
   p.cache = call.view, p.at = call.at, p.q = rows[0], p.out = rows[1];
-  p.type = type, p.group = q_heads / cache->heads, p.dim = cache->dim, p.rot_bits = rot_bits;
+  p.type = type, p.group = q_heads / cache->heads, p.by_group = divisor((uint32_t)p.group), p.dim = cache->dim, p.rot_bits = rot_bits;
   p.scale = scale * 1.44269504088896341f;  // scores in powers of two
   p.causal = causal, p.window = (int)std::min<int64_t>(window, 1 << 30);
   p.notes = (int4*)workspace, p.parts = (float*)((char*)workspace + kMostCtas * sizeof(int4));
