@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   __shared__ uint64_t known[kAhead], done[kAhead];  // steps that are found, and over
   __shared__ float row_scale[kChunkRows];
-  __shared__ PlanScratch<kThreads> scratch;
+  __shared__ PlanScratch scratch;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
   __shared__ volatile uint32_t issued;  // steps so far: a tile may sit out many
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   // (in shared memory: registers are dear, and a step needs little of it)
   Walk &walk = walks[warp][0], &next = walks[warp][1];
   {
-    const Walk share = find_share<kChunkRows, kKeys>(p, blockIdx.x, gridDim.x, scratch);
+    const Walk share = find_share<kChunkRows, kKeys, 1, kThreads>(p, blockIdx.x, gridDim.x, scratch);
     if (lane == 0) walk = next = share;
     __syncwarp();
   }

@@ -22,9 +22,9 @@ namespace {
 constexpr int kWarps = 8;
 
 template <int DIM>
-__global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams p, int rows_all, int ctas) {
+__global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams p, int rows_all, int workers) {
   const int lane = threadIdx.x & 31;
-  const int owner = blockIdx.x % ctas, r = blockIdx.x / ctas * kWarps + (threadIdx.x >> 5);
+  const int owner = blockIdx.x % workers, r = blockIdx.x / workers * kWarps + (threadIdx.x >> 5);
   pdl_begin();
   const int4 note = p.notes[owner];
   if (!(note.x & kNoteTail)) return;
@@ -33,9 +33,9 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams
   if (r >= rows_all || row >= (int64_t)s.count * p.group) return;
   const int64_t floats = part_floats(rows_all, DIM);
   // parts: 2 owner + 1, then 2 i of the CTAs that follow, up to the one that ends the item
-  int last = ctas - 1;
-  for (int i0 = owner + 1; i0 < ctas; i0 += 32) {
-    const uint32_t ends = __ballot_sync(~0u, i0 + lane < ctas && (p.notes[min(i0 + lane, ctas - 1)].x & kNoteHeadEnds));
+  int last = workers - 1;
+  for (int i0 = owner + 1; i0 < workers; i0 += 32) {
+    const uint32_t ends = __ballot_sync(~0u, i0 + lane < workers && (p.notes[min(i0 + lane, workers - 1)].x & kNoteHeadEnds));
     if (ends) {
       last = i0 + __ffs(ends) - 1;
       break;
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams
   float l = 0.f, v[kOwn];
 #pragma unroll
   for (int j = 0; j < kOwn; ++j) v[j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = owner; i <= last; ++i) {
     const float* part = p.parts + (2 * (int64_t)i + (i == owner)) * floats;
     const float top = part[rows_all * DIM + r], total = part[rows_all * DIM + rows_all + r];
@@ -71,11 +71,11 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams
 
 }  // namespace
 
-cudaError_t launch_attention_join(const AttentionParams& p, int rows, int ctas, cudaStream_t st) {
-  const unsigned grid = (unsigned)(ctas * ((rows + kWarps - 1) / kWarps));
-  log_kernel("cache_attention join rows=%d ctas=%d", rows, ctas);
+cudaError_t launch_attention_join(const AttentionParams& p, int rows, int workers, cudaStream_t st) {
+  const unsigned grid = (unsigned)(workers * ((rows + kWarps - 1) / kWarps));
+  log_kernel("cache_attention join rows=%d workers=%d", rows, workers);
   return launch_overlapped(p.dim == 64 ? join_kernel<64> : join_kernel<128>, grid, kWarps * 32, 0, 1, st, p,
-                           rows, ctas);
+                           rows, workers);
 }
 
 }  // namespace ff

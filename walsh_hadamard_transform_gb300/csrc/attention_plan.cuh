@@ -3,12 +3,12 @@
 // An item is a block of ROWS rows (new tokens x query heads of one key head) of a sequence with one
 // key head; its keys, from the first that one of its rows sees, are cut into units of UNIT tokens, at
 // least one.  All units of the call, in the order of sequences, key heads, blocks, are dealt out in
-// equal consecutive shares, so that a CTA's work does not depend on how lengths are spread; a share
-// begins and ends inside an item as it may.  The host does not know the lengths: every CTA adds
-// them up for itself.
+// equal consecutive shares, so that no worker's time depends on how lengths are spread; a share
+// begins and ends inside an item as it may.  Workers are CTAs, or warps where an item has few rows.
+// The host does not know the lengths: every CTA adds them up for itself.
 //
-// What a CTA has done of an item that is not all its own goes to the workspace: part 2 i of CTA i is
-// of the item that its share begins in the middle of, part 2 i + 1 of the one that it ends in the
+// What worker i has done of an item that is not all its own goes to the workspace: part 2 i is of
+// the item that its share begins in the middle of, part 2 i + 1 of the one that it ends in the
 // middle of.  notes[i] says which there are, and launch_attention_join() puts them together in the
 // order of the keys, so that results depend on nothing but the arguments.
 #pragma once
@@ -53,8 +53,8 @@ __device__ __forceinline__ int units_of(const Keys& k) {
 }
 
 // Units of one key head of the sequences of a warp's lanes (sequence b in each; count 0: none).
-// (What runs once or once an item is kept out of line: a kernel's loops have to stay in the instruction
-// cache.  Inlined throughout, the kernels were of 150 and 320 KB, and four times as slow.)
+// (Loops here are not unrolled, and divisions few: code that runs once comes from memory, and with 150 and
+// 320 KB of it the kernels took twice as long.)
 template <int ROWS, int UNIT>
 __device__ __forceinline__ int64_t units_of_sequence(const AttentionParams& p, const Sequence& s, int lane) {
   constexpr int kAlone = 4;  // blocks that a lane counts by itself
@@ -86,94 +86,81 @@ struct Walk {
   int64_t left;     // units of the share from `unit` on
 };
 
-template <int THREADS>
+constexpr int kGroups = 256;  // that the sequences are added up in
 struct PlanScratch {
-  int64_t warp_units[THREADS / 32];
-  int64_t rem, per_head;
-  int b;
+  int64_t units[kGroups];  // of one key head
 };
 
-// The share of CTA `cta` of `ctas`; every thread of the CTA calls it.  left = 0: there is none.
-template <int ROWS, int UNIT, int THREADS>
-__device__ __forceinline__ Walk find_share(const AttentionParams& p, int cta, int ctas,
-                                           PlanScratch<THREADS>& scratch) {
-  constexpr int kWarps = THREADS / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = p.cache.heads;
-  auto units_at = [&](int b) {
-    Sequence s{0, 0, 0};
+// The share of worker `worker` of `workers`, at least LEAST units while there are enough; every thread of
+// the CTA calls it, with a worker of its warp's.  left = 0: there is none.
+template <int ROWS, int UNIT, int LEAST, int THREADS>
+__device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker, int workers, PlanScratch& scratch) {
+  const int lane = threadIdx.x & 31, heads = p.cache.heads;
+  const int span = (p.at.sequences + 32 * kGroups - 1) / (32 * kGroups) * 32;  // sequences of a group
+  const int groups = (p.at.sequences + span - 1) / span;
+  Sequence s{0, 0, 0};
+  const auto units_at = [&](int b) {
+    s.count = 0;
     if (b < p.at.sequences) s = sequence(p.at, p.cache.page_tokens, b);
     return units_of_sequence<ROWS, UNIT>(p, s, lane);
   };
-  int64_t first = units_at((int)threadIdx.x), mine = first;
-  for (int b0 = THREADS; b0 < p.at.sequences; b0 += THREADS) mine += units_at(b0 + (int)threadIdx.x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-  if (lane == 0) scratch.warp_units[warp] = mine;
+  // (32 values of a warp added up from the first on)
+  const auto upto = [&](int64_t v) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t other = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += other;
+    }
+    return v;
+  };
+#pragma unroll 1
+  for (int i = threadIdx.x >> 5; i < groups; i += THREADS / 32) {
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < span; b0 += 32) sum += units_at(i * span + b0 + lane);
+    sum = upto(sum);
+    if (lane == 31) scratch.units[i] = sum;
+  }
   __syncthreads();
   int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += scratch.warp_units[w];
+#pragma unroll 1
+  for (int i0 = 0; i0 < groups; i0 += 32)
+    total += __shfl_sync(~0u, upto(i0 + lane < groups ? scratch.units[i0 + lane] : 0), 31);
   total *= heads;
-  const int shares = (int)min((int64_t)ctas, total);
   Walk walk;
   walk.left = 0, walk.unit = walk.units = 0, walk.b = walk.head = walk.block = 0;
   walk.s = Sequence{0, 0, 0}, walk.keys = Keys{0, 0};
-  if (cta >= shares) return walk;
-  const int64_t begin = total * cta / shares, end = total * (cta + 1) / shares;
-  // the sequence that holds unit `begin`
-  int64_t before = 0;
-  for (int b0 = 0; b0 < p.at.sequences; b0 += THREADS) {
-    const int64_t units = b0 ? units_at(b0 + (int)threadIdx.x) : first;
-    int64_t upto = units;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t other = __shfl_up_sync(~0u, upto, o);
-      if (lane >= o) upto += other;
+  const int shares = (int)min((int64_t)workers, (total + LEAST - 1) / LEAST);
+  if (worker >= shares) return walk;
+  const int64_t each = total / shares, more = total - each * shares;
+  int64_t rem = each * worker + min((int64_t)worker, more);
+  walk.left = each + (worker < more);
+  // its group, its sequence, its head, its block: each time 32 at once, the first beyond `rem`
+  const auto find = [&](int count, int64_t times, const auto& units_of_one) {
+    int at = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      const int64_t units = units_of_one(i0 + lane) * times, sum = upto(units);
+      const uint32_t beyond = __ballot_sync(~0u, sum > rem);
+      const int hit = beyond ? __ffs(beyond) - 1 : 31;
+      at = i0 + hit;
+      rem -= __shfl_sync(~0u, beyond ? sum - units : sum, hit);
+      if (beyond) break;
     }
-    __syncthreads();
-    if (lane == 31) scratch.warp_units[warp] = upto;
-    __syncthreads();
-    int64_t chunk = 0, below = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) below += scratch.warp_units[w];
-      chunk += scratch.warp_units[w];
-    }
-    const int64_t from = (before + below + upto - units) * heads;
-    if (units && from <= begin && begin < from + units * heads)
-      scratch.b = b0 + (int)threadIdx.x, scratch.rem = begin - from, scratch.per_head = units;
-    before += chunk;
-    if (before * heads > begin) break;
-  }
-  __syncthreads();
-  walk.b = scratch.b;
-  walk.head = (int)(scratch.rem / scratch.per_head);
-  int64_t rem = scratch.rem % scratch.per_head;
+    return at;
+  };
+  const int group = find(groups, heads, [&](int i) { return i < groups ? scratch.units[i] : 0; });
+  walk.b = group * span + find(span, heads, [&](int i) { return units_at(group * span + i); });
   walk.s = sequence(p.at, p.cache.page_tokens, walk.b);
-  walk.left = end - begin;
-  // the block, 32 at a time
   const int blocks = blocks_of<ROWS>(p, walk.s);
-  for (int i0 = 0; i0 < blocks; i0 += 32) {
-    const int i = i0 + lane;
-    const Keys k = keys_of<ROWS>(p, walk.s, min(i, blocks - 1));
-    const int units = i < blocks ? units_of<UNIT>(k) : 0;
-    int64_t upto = units;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t other = __shfl_up_sync(~0u, upto, o);
-      if (lane >= o) upto += other;
-    }
-    const uint32_t beyond = __ballot_sync(~0u, upto > rem);
-    if (beyond) {
-      const int at = __ffs(beyond) - 1;
-      walk.block = i0 + at;
-      walk.unit = (int)(rem - __shfl_sync(~0u, upto - units, at));
-      walk.units = __shfl_sync(~0u, units, at);
-      walk.keys.low = __shfl_sync(~0u, k.low, at), walk.keys.high = __shfl_sync(~0u, k.high, at);
-      break;
-    }
-    rem -= __shfl_sync(~0u, upto, 31);
-  }
+  const int64_t per_head = __shfl_sync(~0u, units_at(walk.b + lane), 0);
+  walk.head = (int)(rem / per_head), rem -= walk.head * per_head;
+  walk.block = find(blocks, 1, [&](int i) {
+    return (int64_t)(i < blocks ? units_of<UNIT>(keys_of<ROWS>(p, walk.s, i)) : 0);
+  });
+  walk.unit = (int)rem;
+  walk.keys = keys_of<ROWS>(p, walk.s, walk.block);
+  walk.units = units_of<UNIT>(walk.keys);
   return walk;
 }
 

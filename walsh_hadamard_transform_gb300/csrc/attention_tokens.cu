@@ -5,15 +5,18 @@
 //   p = 2^(s - m), m a running maximum; l = sum of p
 //   O^T += V^T P^T   the head dimension is the lines, the contraction runs over keys
 //
-// Bound: HBM, every byte of the cache seen once.  A warp takes 32 tokens at a time through a ring of its
-// own in shared memory that asynchronous copies fill, and reads the codes straight into the
-// fragments of both products: which elements of a contraction meet in which slot is free as long as
-// both operands agree, so a thread takes 16 consecutive bytes of a key, and of two values that are
-// neighbours in P one byte each side by side.  Codes become float16 without a rounding; the
-// scales of keys multiply scores, those of values multiply p.  P is rounded to float16 as
-// p * 2^(15 + e - e_max), at most 2^15, e the scale's exponent and e_max the largest so far: half a
-// unit in 2^-11, down to 2^-29 of the largest possible.  Queries are rounded to float16 once after
-// their rotation, each row at a power of two that takes its largest to 2^14.
+// Bound: HBM, every byte of the cache seen once.  A warp is on its own: it takes 32 tokens at a time
+// through a ring of its own in shared memory that asynchronous copies fill, over items as well, and
+// reads the codes straight into the fragments of both products: which elements of a contraction
+// meet in which slot is free as long as both operands agree, so a thread takes 16 consecutive bytes
+// of a key, and of two values that are neighbours in P one byte each side by side.  Queries and
+// outputs are turned in those fragments' layouts too.  (With the warps of a CTA on one item, and their sums
+// joined in shared memory, an item cost 15,000 clocks besides its keys: 64 sequences of 256 to 16384 tokens
+// 237 us.)  Codes become float16 without a rounding; the scales of keys multiply scores, those of
+// values multiply p.  P is rounded to float16 as p * 2^(15 + e - e_max), at most 2^15, e the scale's
+// exponent and e_max the largest so far: half a unit in 2^-11, down to 2^-29 of the largest possible.
+// Queries are rounded to float16 once after their rotation, each row at a power of two that takes
+// its largest to 2^14.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -31,23 +34,17 @@ namespace fwt {
 namespace ff {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = kTokenWorkers, kThreads = kWarps * 32;
 constexpr int kStep = 32;   // tokens that a warp takes at a time
-constexpr int kUnit = 128;  // tokens of a unit of the plan
+constexpr int kLeast = 4;   // steps of a share: fewer cost more in joining than they save
 
-// NT: groups of 8 rows.
-template <int DIM, int NT>
+template <int DIM>
 struct Layout {
-  static constexpr int kRows = 8 * NT;
   static constexpr int kValues = kStep * DIM, kKeyScales = 2 * kValues, kValueScales = kKeyScales + kStep;
   static constexpr int kStage = kValueScales + kStep;
   static constexpr int kStages = DIM == 128 ? 3 : 6;
-  static constexpr int kRing = kStages * kStage;         // of a warp
-  static constexpr int kPitchQ = DIM * 2 + 16;           // bytes of a query row
-  static constexpr int kPitchSum = DIM + 4;              // floats of a row of sums
-  static constexpr int kQueries = kWarps * kRing;
-  static constexpr int kSums = kQueries + kRows * kPitchQ;
-  static constexpr int kBytes = kSums + kRows * kPitchSum * 4;
+  static constexpr int kRing = kStages * kStage;  // of a warp
+  static constexpr int kBytes = kWarps * kRing;
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
@@ -73,12 +70,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// 2^e in two factors, for -252 <= e <= 254.
-__device__ __forceinline__ float times_power(float v, int e) {
-  const int half = e >> 1;
-  return v * __uint_as_float((uint32_t)(127 + half) << 23) * __uint_as_float((uint32_t)(127 + e - half) << 23);
-}
-
 // Rows of codes in a stage: 16-byte pieces in an order by row, so that the fragments' reads meet all
 // banks (rows 2 c of values, half rows of keys).
 template <int DIM>
@@ -86,52 +77,51 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
   return row * DIM + ((piece ^ (DIM == 128 ? row & 6 : (row >> 1) & 3)) << 4);
 }
 
+// NT: groups of 8 rows.
 template <int DIM, int NT>
 __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const AttentionParams p) {
-  using L = Layout<DIM, NT>;
-  constexpr int kRows = L::kRows, kTiles = DIM / 16;
+  using L = Layout<DIM>;
+  constexpr int kRows = 8 * NT, kTiles = DIM / 16, kHalves = DIM / 64;
   extern __shared__ __align__(16) uint8_t memory[];
-  __shared__ PlanScratch<kThreads> scratch;
+  __shared__ PlanScratch scratch;
   __shared__ Walk walks[kWarps][2];  // of each warp: where it stands, and where its copies do
-  __shared__ float row_scale[kRows];
-  __shared__ float tops[kWarps][kRows], totals[kWarps][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  // (the shares of few go to as many multiprocessors as there are)
+  const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
   const uint8_t* ring = memory + warp * L::kRing;
   const uint32_t ring_at = smem_u32(ring);
-  uint8_t* queries = memory + L::kQueries;
-  float* sums = (float*)(memory + L::kSums);
   const CacheView& cache = p.cache;
   pdl_begin();
 
   // (in shared memory: a step needs little of them)
   Walk &walk = walks[warp][0], &ahead = walks[warp][1];
   {
-    const Walk share = find_share<kRows, kUnit>(p, blockIdx.x, gridDim.x, scratch);
+    const Walk share = find_share<kRows, kStep, kLeast, kThreads>(p, worker, kWarps * (int)gridDim.x, scratch);
     if (lane == 0) walk = ahead = share;
     __syncwarp();
   }
   if (walk.left == 0) {
-    if (threadIdx.x == 0) p.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (lane == 0) p.notes[worker] = make_int4(0, 0, 0, 0);
     return;
   }
   const auto advance = [&](Walk& w) {
     __syncwarp();
-    if (lane == 0) next_piece<kRows, kUnit>(p, w);
+    if (lane == 0) next_piece<kRows, kStep>(p, w);
     __syncwarp();
   };
 
   // The warp's copies run ahead of its work, over items as well: where the next one starts, and ends.
   int pos_ahead = 0, to_ahead = 0, head_ahead = 0;
   bool some = true;       // whether there is a next one
-  bool fresh = true;      // whether `ahead` is at an item that this warp has not looked at
+  bool fresh = true;      // whether `ahead` is at an item not looked at yet
   uint32_t present = 0;   // two bits a stage in flight: whether its halves have a page
   int pages = -1;         // lanes 0 and 1: the pages of the next step's halves
   const auto settle = [&] {
     while (true) {
       if (fresh) {
-        const int from = ahead.keys.low + ahead.unit * kUnit;
-        to_ahead = min(from + piece_units(ahead) * kUnit, ahead.keys.high);
-        pos_ahead = from + warp * kStep, head_ahead = ahead.head, fresh = false;
+        pos_ahead = ahead.keys.low + ahead.unit * kStep;
+        to_ahead = min(pos_ahead + piece_units(ahead) * kStep, ahead.keys.high);
+        head_ahead = ahead.head, fresh = false;
       }
       if (pos_ahead < to_ahead) break;
       advance(ahead);
@@ -172,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
                    page >= 0);
         }
       }
-      pos_ahead += kWarps * kStep;
+      pos_ahead += kStep;
       settle();
     }
     present |= bits << (2 * (L::kStages - 1));
@@ -190,65 +180,72 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
   while (walk.left > 0) {
     const int piece = piece_units(walk);
     const bool starts = walk.unit == 0, ends = walk.unit + piece == walk.units;
-    const int from = walk.keys.low + walk.unit * kUnit;
-    const int to = min(from + piece * kUnit, walk.keys.high);
+    const int from = walk.keys.low + walk.unit * kStep;
+    const int to = min(from + piece * kStep, walk.keys.high);
     const int row0 = walk.block * kRows;  // of the sequence's rows with this head
-    const int rows = (int)min((int64_t)kRows, (int64_t)walk.s.count * p.group - row0);
+    const int rows = min(kRows, walk.s.count * p.group - row0);
 
-    // queries: rotated, a power of two for each row, float16
-    for (int r = warp; r < kRows; r += kWarps) {
-      constexpr int kOwn = DIM / 32;
-      float v[kOwn];
+    // queries: rotated, a power of two for each row, float16; thread (g, c) has of row g the 16
+    // elements from 64 j + 16 c on
+    uint32_t q[NT][kHalves][8];
+    float scale[NT][2];
+    Keys seen[NT][2];
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) v[i] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + g;
+      float v[kHalves * 16];
+#pragma unroll
+      for (int i = 0; i < kHalves * 16; ++i) v[i] = 0.f;
       if (r < rows) {
         const int token = walk.s.row + quotient(row0 + r, p.by_group);
         const int head = walk.head * p.group + remainder(row0 + r, p.by_group);
-        const uint32_t* q = (const uint32_t*)((const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + kOwn * lane);
+        const uint16_t* from_q = (const uint16_t*)p.q.p + token * p.q.token + head * p.q.head + 16 * c;
 #pragma unroll
-        for (int i = 0; i < kOwn / 2; ++i) {
-          const float2 f = pair_to_float(q[i], p.type);
-          v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        for (int i = 0; i < kHalves * 2; ++i) {
+          const uint4 w = *(const uint4*)(from_q + (i >> 1) * 64 + (i & 1) * 8);
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = pair_to_float(x[k], p.type);
+            v[8 * i + 2 * k] = f.x, v[8 * i + 2 * k + 1] = f.y;
+          }
         }
       }
-      turn_row<DIM>(v, p.rot_bits, lane);
-      const float norm = rotation_norm(p.rot_bits);
-      uint32_t top = 0;
+      const int bits = p.rot_bits;
+      if (bits > 0) turn_own<kHalves * 16, 1>(v);
+      if (bits > 1) turn_own<kHalves * 16, 2>(v);
+      if (bits > 2) turn_own<kHalves * 16, 4>(v);
+      if (bits > 3) turn_own<kHalves * 16, 8>(v);
+      if (bits > 4) turn_lanes(v, 1, lane);
+      if (bits > 5) turn_lanes(v, 2, lane);
+      if constexpr (DIM == 128)
+        if (bits > 6) turn_own<kHalves * 16, 16>(v);
+      const float norm = rotation_norm(bits);
+      uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
+      for (int i = 0; i < kHalves * 16; ++i) {
         v[i] *= norm;
-        top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+        most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
       }
-      top = __reduce_max_sync(~0u, top);
-      const int e = max((int)(top >> 23), 27);  // (zero, and what is nearly so)
+      most = max(most, __shfl_xor_sync(~0u, most, 1));
+      most = max(most, __shfl_xor_sync(~0u, most, 2));
+      const int e = max((int)(most >> 23), 27);  // (zero, and what is nearly so)
       const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
-      uint32_t* to_q = (uint32_t*)(queries + r * L::kPitchQ) + kOwn / 2 * lane;
 #pragma unroll
-      for (int i = 0; i < kOwn / 2; ++i) to_q[i] = pair_from_float<__half>(v[2 * i] * up, v[2 * i + 1] * up);
-      if (lane == 0) row_scale[r] = p.scale * __uint_as_float((uint32_t)(e - 14) << 23);
-    }
-    __syncthreads();
-    uint32_t q[NT][DIM / 64][8];  // 16 consecutive elements of a row from 64 j + 16 c on
+      for (int i = 0; i < kHalves * 8; ++i) q[n][i / 8][i & 7] = pair_from_float<__half>(v[2 * i] * up, v[2 * i + 1] * up);
+      const float mine = p.scale * __uint_as_float((uint32_t)(e - 14) << 23);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < DIM / 64; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 w = *(const uint4*)(queries + (8 * n + g) * L::kPitchQ + 128 * j + 32 * c + 16 * i);
-          q[n][j][4 * i] = w.x, q[n][j][4 * i + 1] = w.y, q[n][j][4 * i + 2] = w.z, q[n][j][4 * i + 3] = w.w;
-        }
-    float scale[NT][2], top[NT][2], total[NT][2];
-    Keys seen[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * n + 2 * c + e;
-        scale[n][e] = row_scale[r];
-        seen[n][e] = r < rows ? seen_by(p, walk.s, row0 + r) : Keys{0, 0};
-        top[n][e] = -INFINITY, total[n][e] = 0.f;
+      for (int e2 = 0; e2 < 2; ++e2) {  // of the rows that the scores' fragment has here
+        scale[n][e2] = __shfl_sync(~0u, mine, 4 * (2 * c + e2));
+        const int r2 = 8 * n + 2 * c + e2;
+        seen[n][e2] = r2 < rows ? seen_by(p, walk.s, row0 + r2) : Keys{0, 0};
       }
+    }
+    float top[NT][2], total[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) top[n][e] = -INFINITY, total[n][e] = 0.f;
     float o[kTiles][NT][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
@@ -256,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
       for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     int most = 0;  // the largest scale byte of the values so far
 
-    for (int pos = from + warp * kStep; pos < to; pos += kWarps * kStep) {
+    for (int pos = from; pos < to; pos += kStep) {
       asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
       __syncwarp();
       const uint8_t* at = ring + stage * L::kStage;
@@ -400,82 +397,65 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
       if (++stage == L::kStages) stage = 0;
     }
 
-    // the warps' sums together, one after the other
+    // out: the item's rows, or a part of them for launch_attention_join.  Thread (g, c) has of rows
+    // 2 c and 2 c + 1 the DIM / 8 elements from DIM / 8 g on.
+    const bool whole = starts && ends;
+    float* part = p.parts + (2 * (int64_t)worker + (starts ? 1 : 0)) * part_floats(kRows, DIM);
+    // 2^e, e from -142 to 112, in two factors
+    const int e = most - 142, half_e = e >> 1;
+    const float unit[2] = {__uint_as_float((uint32_t)(127 + half_e) << 23), __uint_as_float((uint32_t)(127 + e - half_e) << 23)};
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = total[n][e];
+      for (int k = 0; k < 2; ++k) {
+        const int r = 8 * n + 2 * c + k;
+        float l = total[n][k];
         l += __shfl_xor_sync(~0u, l, 4);
         l += __shfl_xor_sync(~0u, l, 8);
         l += __shfl_xor_sync(~0u, l, 16);
-        if (g == 0) tops[warp][8 * n + 2 * c + e] = top[n][e], totals[warp][8 * n + 2 * c + e] = l;
-      }
-    __syncthreads();
-    float weight[NT][2];
+        float v[DIM / 8];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < DIM / 8; ++i) v[i] = o[i / 2][n][2 * (i & 1) + k] * unit[0] * unit[1];
+        if (whole) {
+          constexpr int kOwn = DIM == 128 ? 4 : 3;  // bits of a thread's own elements
+          const int bits = p.rot_bits;
+          if (bits > 0) turn_own<DIM / 8, 1>(v);
+          if (bits > 1) turn_own<DIM / 8, 2>(v);
+          if (bits > 2) turn_own<DIM / 8, 4>(v);
+          if constexpr (DIM == 128)
+            if (bits > 3) turn_own<DIM / 8, 8>(v);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = -INFINITY;
+          for (int bit = 0; bit < 3; ++bit)
+            if (bits > kOwn + bit) turn_lanes(v, 4 << bit, lane);
+          const float norm = l == 0.f ? 0.f : rotation_norm(bits) / l;
+          if (r < rows) {
+            const int token = walk.s.row + quotient(row0 + r, p.by_group);
+            const int head = walk.head * p.group + remainder(row0 + r, p.by_group);
+            uint16_t* to_out = (uint16_t*)p.out.p + token * p.out.token + head * p.out.head + DIM / 8 * g;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[w][8 * n + 2 * c + e]);
-        weight[n][e] = m == -INFINITY ? (total[n][e] == total[n][e] ? 0.f : 1.f) : exp2_fast(top[n][e] - m);
-      }
-#pragma unroll 1
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
+            for (int i = 0; i < DIM / 64; ++i) {
+              uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float* sum = sums + (8 * n + 2 * c + (e & 1)) * L::kPitchSum + DIM / 8 * g + 2 * i + (e >> 1);
-              const float v = times_power(o[i][n][e] * weight[n][e & 1], most - 142);
-              *sum = w ? *sum + v : v;
+              for (int j = 0; j < 4; ++j) x[j] = pair_from_float(v[8 * i + 2 * j] * norm, v[8 * i + 2 * j + 1] * norm, p.type);
+              *(uint4*)(to_out + 8 * i) = make_uint4(x[0], x[1], x[2], x[3]);
             }
+          }
+        } else if (r < rows) {
+          float4* to_part = (float4*)(part + r * DIM + DIM / 8 * g);
+#pragma unroll
+          for (int i = 0; i < DIM / 32; ++i) to_part[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          if (g == 0) part[kRows * DIM + r] = top[n][k], part[kRows * DIM + kRows + r] = l;
+        }
       }
-      __syncthreads();
-    }
-
-    // out: the item's rows, or a part of them for launch_attention_join
-    const bool whole = starts && ends;
-    float* part = p.parts + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * part_floats(kRows, DIM);
-    for (int r = warp; r < rows; r += kWarps) {
-      constexpr int kOwn = DIM / 32;
-      float m = -INFINITY, l = 0.f, v[kOwn];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[w][r]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        l += totals[w][r] * (m == -INFINITY ? 1.f : exp2_fast(tops[w][r] - m));
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) v[i] = sums[r * L::kPitchSum + kOwn * lane + i];
-      if (whole) {
-        const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
-        turn_row<DIM>(v, p.rot_bits, lane);
-        const int token = walk.s.row + quotient(row0 + r, p.by_group);
-        const int head = walk.head * p.group + remainder(row0 + r, p.by_group);
-        uint32_t* to_out = (uint32_t*)((uint16_t*)p.out.p + token * p.out.token + head * p.out.head + kOwn * lane);
-#pragma unroll
-        for (int i = 0; i < kOwn / 2; ++i) to_out[i] = pair_from_float(v[2 * i] * norm, v[2 * i + 1] * norm, p.type);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) part[(int64_t)r * DIM + kOwn * lane + i] = v[i];
-        if (lane == 0) part[kRows * DIM + r] = m, part[kRows * DIM + kRows + r] = l;
-      }
-    }
     if (!whole) {
       if (!starts) flags |= kNoteHead | (ends ? kNoteHeadEnds : 0);
       else flags |= kNoteTail, note.y = walk.b, note.z = walk.head, note.w = walk.block;
     }
     advance(walk);
-    __syncthreads();  // (the sums and queries are read)
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   note.x = flags;
-  if (threadIdx.x == 0) p.notes[blockIdx.x] = note;
+  if (lane == 0) p.notes[worker] = note;
 }
 
 template <int DIM, int NT>
@@ -485,14 +465,12 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t st) {
   log_kernel("cache_attention tokens=%d heads=%dx%d dim=%d sequences=%d | rows=%d ctas=%d", p.at.tokens,
              p.cache.heads, p.group, DIM, p.at.sequences, 8 * NT, ctas);
   const cudaError_t err = launch_cluster(attention_tokens_kernel<DIM, NT>, ready, (unsigned)ctas, kThreads,
-                                         Layout<DIM, NT>::kBytes, 1, st, p);
-  return err == cudaSuccess ? launch_attention_join(p, 8 * NT, ctas, st) : err;
+                                         Layout<DIM>::kBytes, 1, st, p);
+  return err == cudaSuccess ? launch_attention_join(p, 8 * NT, kWarps * ctas, st) : err;
 }
 template <int DIM>
 cudaError_t launch_rows(const AttentionParams& p, int rows, cudaStream_t st) {
-  if (rows == 8) return launch<DIM, 1>(p, st);
-  if (rows == 16) return launch<DIM, 2>(p, st);
-  return launch<DIM, 4>(p, st);
+  return rows == 8 ? launch<DIM, 1>(p, st) : launch<DIM, 2>(p, st);
 }
 
 }  // namespace
