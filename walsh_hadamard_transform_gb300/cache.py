@@ -97,7 +97,8 @@ def _cache(cache):
     if len(shape) != 4 or v.shape != shape:
         raise ValueError("cache: codes are (pages, heads, page_tokens, dim), of keys and values alike")
     pages, heads, page, dim = shape
-    if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+    of_scales = shape[:3]
+    if k_scale.shape != of_scales or v_scale.shape != of_scales:
         raise ValueError("cache: scales are (pages, heads, page_tokens)")
     if dim != 64 and dim != 128 or page < 16 or page % 16:
         raise ValueError("cache: dim is 64 or 128 and page_tokens a multiple of 16")
@@ -106,15 +107,14 @@ def _cache(cache):
     device = k.get_device()
     if device < 0 or v.get_device() != device or k_scale.get_device() != device or v_scale.get_device() != device:
         raise ValueError("cache: every tensor must be on one CUDA device")
-    strides = []
-    within = (page * dim, dim, 1), (page, 1)
-    for i, t in enumerate((k, v, k_scale, v_scale)):
-        stride = t.stride()
-        strides.append(stride[0])
-        if stride[1:] != within[i >> 1] and not _within(t, within[i >> 1]):
-            raise ValueError("cache: each page must be contiguous")
-    return _CacheArgument(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *strides,
-                          pages, heads, page, dim), device, heads, dim
+    of_k, of_v, of_ks, of_vs = k.stride(), v.stride(), k_scale.stride(), v_scale.stride()
+    within = (page * dim, dim, 1)
+    if of_k[1:] != within or of_v[1:] != within or of_ks[1:] != (page, 1) or of_vs[1:] != (page, 1):
+        for t in cache:
+            if not _within(t, within if t.dim() == 4 else (page, 1)):
+                raise ValueError("cache: each page must be contiguous")
+    return _CacheArgument(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), of_k[0],
+                          of_v[0], of_ks[0], of_vs[0], pages, heads, page, dim), device, heads, dim
 
 
 def _within(t, strides):
@@ -124,21 +124,25 @@ def _within(t, strides):
 
 def _sequences(table, starts, lengths, device):
     """The C argument of a call's sequences."""
-    if table.dim() != 2 or starts.dim() != 1 or lengths.dim() != 1:
+    size, of_starts, of_lengths = table.shape, starts.shape, lengths.shape
+    if len(size) != 2 or len(of_starts) != 1 or len(of_lengths) != 1:
         raise ValueError("table is (sequences, most pages), starts (sequences + 1), lengths (sequences)")
-    count, most = table.shape
-    if starts.shape[0] != count + 1 or lengths.shape[0] != count:
+    count, most = size
+    if of_starts[0] != count + 1 or of_lengths[0] != count:
         raise ValueError(f"table names {count} sequences: starts must have {count + 1} entries and "
-                         f"lengths {count}, not {starts.shape[0]} and {lengths.shape[0]}")
-    for name, t in (("table", table), ("starts", starts), ("lengths", lengths)):
-        if t.dtype is not _I32:
-            raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
-        if t.get_device() != device:
-            raise ValueError(f"{name}: every tensor must be on one CUDA device")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError(f"{name}: entries must be contiguous")
-    return _SequencesArgument(table.data_ptr(), table.stride(0), most, starts.data_ptr(),
-                              lengths.data_ptr(), count)
+                         f"lengths {count}, not {of_starts[0]} and {of_lengths[0]}")
+    row, column = table.stride()
+    if not (table.dtype is _I32 and starts.dtype is _I32 and lengths.dtype is _I32
+            and table.get_device() == device and starts.get_device() == device
+            and lengths.get_device() == device and (column == 1 or most <= 1)
+            and (starts.stride(0) == 1 or count == 0) and (lengths.stride(0) == 1 or count <= 1)):
+        for name, t in (("table", table), ("starts", starts), ("lengths", lengths)):
+            if t.dtype is not _I32:
+                raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
+            if t.get_device() != device:
+                raise ValueError(f"{name}: every tensor must be on one CUDA device")
+        raise ValueError("the entries of table's rows, of starts and of lengths must be contiguous")
+    return _SequencesArgument(table.data_ptr(), row, most, starts.data_ptr(), lengths.data_ptr(), count)
 
 
 def _rows(t, name, device, dtype, shape):

@@ -652,16 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   if (warp == 12) tmem_free<1>(tmem, kColumns);
   // what there is to join (warp 14 has kept the share's start and walks it once more)
   if (warp == 14) {
-    int4 note = make_int4(0, 0, 0, 0);
+    bool tail = false;
     while (walk.left > 0) {
-      const int count = piece_units(walk);
-      const bool starts = walk.unit == 0, ends = walk.unit + count == walk.units;
-      if (!starts) note.x |= kNoteHead | (ends ? kNoteHeadEnds : 0);
-      else if (!ends) note.x |= kNoteTail, note.y = walk.b, note.z = walk.head, note.w = walk.block;
+      if (walk.unit == 0 && piece_units(walk) < walk.units && !gave_up) {
+        if (lane == 0) note_tail(walk, blockIdx.x, p.notes);
+        tail = true;
+      }
       advance(walk);
     }
-    if (gave_up) note.x &= kNoteHead | kNoteHeadEnds;
-    if (lane == 0) p.notes[blockIdx.x] = note;
+    if (lane == 0 && !tail) p.notes[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
 }
 

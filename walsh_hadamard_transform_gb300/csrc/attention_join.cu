@@ -26,21 +26,12 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams
   const int lane = threadIdx.x & 31;
   const int owner = blockIdx.x % workers, r = blockIdx.x / workers * kWarps + (threadIdx.x >> 5);
   pdl_begin();
-  const int4 note = p.notes[owner];
+  const int4 note = p.notes[2 * owner], at = p.notes[2 * owner + 1];
   if (!(note.x & kNoteTail)) return;
-  const Sequence s = sequence(p.at, p.cache.page_tokens, note.y);
-  const int64_t row = (int64_t)note.w * rows_all + r;
-  if (r >= rows_all || row >= (int64_t)s.count * p.group) return;
+  const int row = note.w * rows_all + r;
+  if (r >= rows_all || row >= at.y * p.group) return;
   const int64_t floats = part_floats(rows_all, DIM);
-  // parts: 2 owner + 1, then 2 i of the CTAs that follow, up to the one that ends the item
-  int last = workers - 1;
-  for (int i0 = owner + 1; i0 < workers; i0 += 32) {
-    const uint32_t ends = __ballot_sync(~0u, i0 + lane < workers && (p.notes[min(i0 + lane, workers - 1)].x & kNoteHeadEnds));
-    if (ends) {
-      last = i0 + __ffs(ends) - 1;
-      break;
-    }
-  }
+  const int last = min(note.y, workers - 1);  // parts: 2 owner + 1, then 2 i of the workers that follow
   constexpr int kOwn = DIM / 32;
   float m = -INFINITY;
   for (int i = owner + lane; i <= last; i += 32)
@@ -51,19 +42,36 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttentionParams
   float l = 0.f, v[kOwn];
 #pragma unroll
   for (int j = 0; j < kOwn; ++j) v[j] = 0.f;
-#pragma unroll 8
-  for (int i = owner; i <= last; ++i) {
-    const float* part = p.parts + (2 * (int64_t)i + (i == owner)) * floats;
-    const float top = part[rows_all * DIM + r], total = part[rows_all * DIM + rows_all + r];
-    // (a part with no maximum has seen nothing, or only what is not a number)
-    const float w = top == -INFINITY ? 1.f : exp2f(top - base);
-    l = fmaf(total, w, l);
+  constexpr int kBatch = 8;  // parts on their way at a time
+#pragma unroll 1
+  for (int i0 = owner; i0 <= last; i0 += kBatch) {
+    float part_v[kBatch][kOwn], top[kBatch], total[kBatch];
 #pragma unroll
-    for (int j = 0; j < kOwn; ++j) v[j] = fmaf(part[(int64_t)r * DIM + kOwn * lane + j], w, v[j]);
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = min(i0 + k, last);
+      const float* part = p.parts + (2 * (int64_t)i + (i == owner)) * floats;
+      top[k] = part[rows_all * DIM + r], total[k] = part[rows_all * DIM + rows_all + r];
+      if constexpr (kOwn == 4) {
+        const float4 x = *(const float4*)(part + r * DIM + 4 * lane);
+        part_v[k][0] = x.x, part_v[k][1] = x.y, part_v[k][2] = x.z, part_v[k][3] = x.w;
+      } else {
+        const float2 x = *(const float2*)(part + r * DIM + 2 * lane);
+        part_v[k][0] = x.x, part_v[k][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k <= last) {
+        // (a part with no maximum has seen nothing, or only what is not a number)
+        const float w = top[k] == -INFINITY ? 1.f : exp2f(top[k] - base);
+        l = fmaf(total[k], w, l);
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) v[j] = fmaf(part_v[k][j], w, v[j]);
+      }
   }
   turn_row<DIM>(v, p.rot_bits, lane);
   const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
-  const int token = s.row + quotient((int)row, p.by_group), head = note.z * p.group + remainder((int)row, p.by_group);
+  const int token = at.x + quotient(row, p.by_group), head = note.z * p.group + remainder(row, p.by_group);
   uint32_t* out = (uint32_t*)((uint16_t*)p.out.p + token * p.out.token + head * p.out.head + kOwn * lane);
 #pragma unroll
   for (int j = 0; j < kOwn / 2; ++j) out[j] = pair_from_float(v[2 * j] * norm, v[2 * j + 1] * norm, p.type);

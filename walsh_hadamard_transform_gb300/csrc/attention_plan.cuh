@@ -20,10 +20,9 @@
 namespace fwt {
 namespace ff {
 
-// notes[i]: x flags, then sequence, key head and block of part 2 i + 1.
-constexpr int kNoteHead = 1;      // part 2 i is there
-constexpr int kNoteHeadEnds = 2;  // and reaches the item's end
-constexpr int kNoteTail = 4;      // part 2 i + 1 is there
+// notes[2 i]: x flags, and of part 2 i + 1 the last worker with a part of its item, the key head and
+// the block; notes[2 i + 1]: its sequence's first packed row and number of rows.
+constexpr int kNoteTail = 1;  // part 2 i + 1 is there
 
 // The keys of an item: [low, high), low a multiple of 16.
 struct Keys {
@@ -84,6 +83,8 @@ struct Walk {
   Keys keys;
   int unit, units;  // of the item: the next one, and all
   int64_t left;     // units of the share from `unit` on
+  int64_t each;     // of every share, and one more of the first `more`
+  int more;
 };
 
 constexpr int kGroups = 256;  // that the sequences are added up in
@@ -128,12 +129,14 @@ __device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker,
     total += __shfl_sync(~0u, upto(i0 + lane < groups ? scratch.units[i0 + lane] : 0), 31);
   total *= heads;
   Walk walk;
-  walk.left = 0, walk.unit = walk.units = 0, walk.b = walk.head = walk.block = 0;
+  walk.left = walk.each = 0, walk.more = 0, walk.unit = walk.units = 0, walk.b = walk.head = walk.block = 0;
   walk.s = Sequence{0, 0, 0}, walk.keys = Keys{0, 0};
   const int shares = (int)min((int64_t)workers, (total + LEAST - 1) / LEAST);
   if (worker >= shares) return walk;
-  const int64_t each = total / shares, more = total - each * shares;
-  int64_t rem = each * worker + min((int64_t)worker, more);
+  const int64_t each = total < 0x7fffffff ? (int)total / shares : total / shares;
+  const int more = (int)(total - each * shares);
+  walk.each = each, walk.more = more;
+  int64_t rem = each * worker + min(worker, more);
   walk.left = each + (worker < more);
   // its group, its sequence, its head, its block: each time 32 at once, the first beyond `rem`
   const auto find = [&](int count, int64_t times, const auto& units_of_one) {
@@ -149,12 +152,13 @@ __device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker,
     }
     return at;
   };
-  const int group = find(groups, heads, [&](int i) { return i < groups ? scratch.units[i] : 0; });
+  const int group = groups == 1 ? 0 : find(groups, heads, [&](int i) { return i < groups ? scratch.units[i] : 0; });
   walk.b = group * span + find(span, heads, [&](int i) { return units_at(group * span + i); });
   walk.s = sequence(p.at, p.cache.page_tokens, walk.b);
   const int blocks = blocks_of<ROWS>(p, walk.s);
   const int64_t per_head = __shfl_sync(~0u, units_at(walk.b + lane), 0);
-  walk.head = (int)(rem / per_head), rem -= walk.head * per_head;
+  walk.head = rem < 0x7fffffff && per_head < 0x7fffffff ? (int)rem / (int)per_head : (int)(rem / per_head);
+  rem -= walk.head * per_head;
   walk.block = find(blocks, 1, [&](int i) {
     return (int64_t)(i < blocks ? units_of<UNIT>(keys_of<ROWS>(p, walk.s, i)) : 0);
   });
@@ -190,6 +194,16 @@ __device__ __forceinline__ void next_piece(const AttentionParams& p, Walk& w) {
   }
   w.keys = keys_of<ROWS>(p, w.s, w.block);
   w.units = units_of<UNIT>(w.keys);
+}
+
+// The notes on the share's last piece, an item that begins in it and ends in another: `walk` stands there.
+__device__ __forceinline__ void note_tail(const Walk& w, int worker, int4* notes) {
+  // the item's last unit, counted from the first of all
+  const int64_t end = w.each * (worker + 1) + min(worker + 1, w.more);
+  const int64_t unit = end + (w.units - w.unit - piece_units(w)) - 1, longer = (w.each + 1) * w.more;
+  const int64_t last = unit < longer ? unit / (w.each + 1) : w.more + (unit - longer) / w.each;
+  notes[2 * worker] = make_int4(kNoteTail, (int)last, w.head, w.block);
+  notes[2 * worker + 1] = make_int4(w.s.row, w.s.count, 0, 0);
 }
 
 // What keys row `r` (a new token and query head of the sequence) sees: [low, high).

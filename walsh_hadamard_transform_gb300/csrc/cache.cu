@@ -26,8 +26,10 @@ namespace ff {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kReadRows = 2;  // of a group of lanes that reads back: their places are looked up together
 
 struct MoveParams {
+  Divisor by_head;
   CacheView cache;
   Places at;
   Rows rows[2];
@@ -42,6 +44,21 @@ __device__ __forceinline__ int sequences_before(const Places& at, int row) {
     before += __syncthreads_count(b < at.sequences && at.starts[b + 1] <= row);
   }
   return before;
+}
+
+// Token and head of row `row` of a CTA's, which begin with row `first` of all.
+struct FirstRow {
+  int token, head;
+};
+__device__ __forceinline__ FirstRow first_row(const MoveParams& p, int64_t first) {
+  FirstRow at;
+  at.token = first < 0x7fffffff ? quotient((int)first, p.by_head) : (int)(first / p.cache.heads);
+  at.head = (int)(first - (int64_t)at.token * p.cache.heads);
+  return at;
+}
+__device__ __forceinline__ void row_at(const MoveParams& p, const FirstRow& at, int row, int& token, int& head) {
+  const int more = quotient(at.head + row, p.by_head);
+  token = at.token + more, head = at.head + row - more * p.cache.heads;
 }
 
 // The sequence of row `row`, from `b` on, and its place: the page and the slot in it, page -1 for
@@ -94,24 +111,25 @@ template <typename T, int DIM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
   constexpr int kLanes = DIM / 16, kRows = kThreads / kLanes;
   const int lane = threadIdx.x & (kLanes - 1), r = p.rot_bits;
-  const int64_t first = (int64_t)blockIdx.x * kRows, pair = first + threadIdx.x / kLanes;
+  const FirstRow first = first_row(p, (int64_t)blockIdx.x * kRows);
+  int token, head;
+  row_at(p, first, threadIdx.x / kLanes, token, head);
   pdl_begin();
-  const int before = sequences_before(p.at, (int)(first / p.cache.heads));
-  const int token = (int)(pair / p.cache.heads), head = (int)(pair - (int64_t)token * p.cache.heads);
-  int page, slot;
-  if (token >= p.at.tokens || !locate(p, token, before, page, slot)) page = -1;
   // (lanes of a warp exchange: those without a row go along with zeros)
   float v[2][16];
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
     const T* from = (const T*)p.rows[o].p + token * p.rows[o].token + head * p.rows[o].head + 8 * lane;
-    if (page >= 0) {
+    if (token < p.at.tokens) {  // on their way while the place is looked up
       load8(from, v[o]), load8(from + DIM / 2, v[o] + 8);
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[o][i] = 0.f;
     }
   }
+  const int before = sequences_before(p.at, first.token);
+  int page, slot;
+  if (token >= p.at.tokens || !locate(p, token, before, page, slot)) page = -1;
   const float norm = 16.f * rotation_norm(r);
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
@@ -122,9 +140,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[o][i] *= norm;
     }
-    uint32_t top = 0;  // of magnitudes as bits: NaN is above all
+    float most = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[o][i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; ++i)
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(v[o][i])));
+    uint32_t top = __float_as_uint(most) & 0x7fffffffu;  // NaN is above all
 #pragma unroll
     for (int step = 1; step < kLanes; step *= 2) top = max(top, __shfl_xor_sync(~0u, top, step));
     const uint32_t byte = scale_byte(__uint_as_float(top));
@@ -149,49 +169,56 @@ template <typename T, int DIM>
 __global__ void __launch_bounds__(kThreads) read_kernel(const MoveParams p) {
   constexpr int kLanes = DIM / 16, kRows = kThreads / kLanes;
   const int lane = threadIdx.x & (kLanes - 1), r = p.rot_bits;
-  const int64_t first = (int64_t)blockIdx.x * kRows, pair = first + threadIdx.x / kLanes;
+  const FirstRow first = first_row(p, (int64_t)blockIdx.x * (kRows * kReadRows));
   pdl_begin();
-  const int before = sequences_before(p.at, (int)(first / p.cache.heads));
-  const int token = (int)(pair / p.cache.heads), head = (int)(pair - (int64_t)token * p.cache.heads);
-  int page = -1, slot = 0;
-  const bool row = token < p.at.tokens && locate(p, token, before, page, slot);
-  uint2 w[2][2];
-  uint32_t byte[2];
+  const int before = sequences_before(p.at, first.token);
+  int token[kReadRows], head[kReadRows];
+  bool row[kReadRows];
+  uint2 w[kReadRows][2][2];
+  uint32_t byte[kReadRows][2];
 #pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    w[o][0] = w[o][1] = make_uint2(0, 0), byte[o] = 127;
-    if (page >= 0) {
-      const int64_t at = (int64_t)head * p.cache.page_tokens + slot;
-      const uint8_t* codes = p.cache.codes[o] + page * p.cache.code_stride[o] + at * DIM + 8 * lane;
-      w[o][0] = *(const uint2*)codes, w[o][1] = *(const uint2*)(codes + DIM / 2);
-      byte[o] = p.cache.scales[o][page * p.cache.scale_stride[o] + at];
+  for (int k = 0; k < kReadRows; ++k) {
+    row_at(p, first, k * kRows + threadIdx.x / kLanes, token[k], head[k]);
+    int page = -1, slot = 0;
+    row[k] = token[k] < p.at.tokens && locate(p, token[k], before, page, slot);
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      w[k][o][0] = w[k][o][1] = make_uint2(0, 0), byte[k][o] = 127;
+      if (page >= 0) {
+        const int64_t at = (int64_t)head[k] * p.cache.page_tokens + slot;
+        const uint8_t* codes = p.cache.codes[o] + page * p.cache.code_stride[o] + at * DIM + 8 * lane;
+        w[k][o][0] = *(const uint2*)codes, w[k][o][1] = *(const uint2*)(codes + DIM / 2);
+        byte[k][o] = p.cache.scales[o][page * p.cache.scale_stride[o] + at];
+      }
     }
   }
   const float norm = rotation_norm(r);
 #pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    float v[16];
+  for (int k = 0; k < kReadRows; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t q = i & 1 ? w[o][i / 2].y : w[o][i / 2].x;
-      const float2 lo = pair_to_float<__half>(e4m3_to_f16x2(q));
-      const float2 hi = pair_to_float<__half>(e4m3_to_f16x2(q >> 16));
-      v[4 * i] = lo.x, v[4 * i + 1] = lo.y, v[4 * i + 2] = hi.x, v[4 * i + 3] = hi.y;
-    }
-    turn_spread<DIM>(v, r, lane);  // of codes: their sums are exact or nearly so
-    const float scale = scale_value(byte[o]);
+    for (int o = 0; o < 2; ++o) {
+      float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = v[i] * norm * scale;
-    if (row) {
-      T* to = (T*)p.rows[o].p + token * p.rows[o].token + head * p.rows[o].head + 8 * lane;
-      store8(to, v), store8(to + DIM / 2, v + 8);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t q = i & 1 ? w[k][o][i / 2].y : w[k][o][i / 2].x;
+        const float2 lo = pair_to_float<__half>(e4m3_to_f16x2(q));
+        const float2 hi = pair_to_float<__half>(e4m3_to_f16x2(q >> 16));
+        v[4 * i] = lo.x, v[4 * i + 1] = lo.y, v[4 * i + 2] = hi.x, v[4 * i + 3] = hi.y;
+      }
+      turn_spread<DIM>(v, r, lane);  // of codes: their sums are exact or nearly so
+      const float scale = scale_value(byte[k][o]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = v[i] * norm * scale;
+      if (row[k]) {
+        T* to = (T*)p.rows[o].p + token[k] * p.rows[o].token + head[k] * p.rows[o].head + 8 * lane;
+        store8(to, v), store8(to + DIM / 2, v + 8);
+      }
     }
-  }
 }
 
 template <template <typename, int> class Kernel, typename T>
 cudaError_t launch_dim(const MoveParams& p, int dim, const char* what, cudaStream_t st) {
-  const int64_t pairs = (int64_t)p.at.tokens * p.cache.heads, rows = kThreads / (dim / 16);
+  const int64_t pairs = (int64_t)p.at.tokens * p.cache.heads, rows = kThreads / (dim / 16) * Kernel<T, 64>::rows_each();
   const int64_t grid = (pairs + rows - 1) / rows;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   log_kernel("%s tokens=%d heads=%d dim=%d | rows a CTA=%lld", what, p.at.tokens, p.cache.heads, dim,
@@ -201,10 +228,12 @@ cudaError_t launch_dim(const MoveParams& p, int dim, const char* what, cudaStrea
 }
 template <typename T, int DIM>
 struct Append {
+  static int rows_each() { return 1; }
   static auto get() { return append_kernel<T, DIM>; }
 };
 template <typename T, int DIM>
 struct Read {
+  static int rows_each() { return kReadRows; }
   static auto get() { return read_kernel<T, DIM>; }
 };
 template <template <typename, int> class Kernel>
@@ -218,12 +247,12 @@ cudaError_t launch_type(const MoveParams& p, int type, int dim, const char* what
 
 cudaError_t launch_cache_append(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
                                 const Places& at, cudaStream_t st) {
-  return launch_type<Append>(MoveParams{cache, at, {k, v}, rot_bits}, type, dim, "cache_append", st);
+  return launch_type<Append>(MoveParams{divisor((uint32_t)cache.heads), cache, at, {k, v}, rot_bits}, type, dim, "cache_append", st);
 }
 
 cudaError_t launch_cache_read(Rows k, Rows v, int type, int dim, int rot_bits, const CacheView& cache,
                               const Places& at, cudaStream_t st) {
-  return launch_type<Read>(MoveParams{cache, at, {k, v}, rot_bits}, type, dim, "cache_read", st);
+  return launch_type<Read>(MoveParams{divisor((uint32_t)cache.heads), cache, at, {k, v}, rot_bits}, type, dim, "cache_read", st);
 }
 
 }  // namespace ff

@@ -210,7 +210,7 @@ size_t fwt_cache_attention_workspace_bytes(int q_heads, int heads, int dim, int6
       longest < 0 || longest > kMostTokens)
     return 0;
   const int rows = item_rows(std::max<int64_t>(longest, 1), q_heads / heads);
-  return (size_t)workers_of(rows) * (sizeof(int4) + 2 * 4 * (size_t)part_floats(rows, dim));
+  return (size_t)workers_of(rows) * (2 * sizeof(int4) + 2 * 4 * (size_t)part_floats(rows, dim));
 }
 
 int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* out, int64_t out_token,
@@ -255,7 +255,7 @@ int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* ou
   p.scale = scale * 1.44269504088896341f;  // scores in powers of two
   p.causal = causal, p.window = (int)std::min<int64_t>(window, 1 << 30);
   const int rows_each = item_rows(longest, p.group);
-  p.notes = (int4*)workspace, p.parts = (float*)((char*)workspace + workers_of(rows_each) * sizeof(int4));
+  p.notes = (int4*)workspace, p.parts = (float*)((char*)workspace + workers_of(rows_each) * 2 * sizeof(int4));
   return done(rows_each == kChunkRows ? launch_attention_chunk(p, (cudaStream_t)stream)
                                       : launch_attention_tokens(p, rows_each, (cudaStream_t)stream));
 }
