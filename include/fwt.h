@@ -396,7 +396,7 @@ typedef struct fwt_cache {
  * starts[b] + i is the token at position lengths[b] - n + i, in page table[b][position / page_tokens].
  *
  * The host reads none of it.  `starts` rises from 0 to at most `tokens`; rows behind starts[sequences]
- * belong to no sequence: they are not read, and rows of outputs there not written.  What could point
+ * belong to no sequence: what they hold does not matter, and rows of outputs there are not written.  What could point
  * outside is taken as it would be nearest: starts beyond `tokens` as `tokens`, lengths below 0
  * as 0 and beyond the table as the table's room; a page below 0 or not below `pages` holds no tokens,
  * and nor do positions below 0.

@@ -28,7 +28,7 @@ ENTRY = {"append": ("fwt_cache_append", APPEND), "read": ("fwt_cache_read", READ
 OF_CACHE = [
     (dict(dim=96), E), (dict(dim=256), E), (dict(heads=0), E), (dict(heads=65537), E), (dict(page_tokens=8), E),
     (dict(page_tokens=24), E), (dict(page_tokens=1 << 21), E), (dict(pages=-1), E), (dict(pages=1 << 31), E),
-    (dict(k=None), E), (dict(v_scale=None), E), (dict(k_stride=PAGE - 16), E), (dict(v_scale_stride=48), E),
+    (dict(heads=4096, page_tokens=1 << 20), E), (dict(k=None), E), (dict(v_scale=None), E), (dict(k_stride=PAGE - 16), E), (dict(v_scale_stride=48), E),
     (dict(k_stride=1 << 56), E), (dict(k=A + 8), MIS), (dict(v_scale=A + 3 * GiB + 4), MIS),
     (dict(v_stride=PAGE + 8), MIS), (dict(k_scale_stride=72), MIS),
 ]

@@ -18,7 +18,8 @@
 // when one is more than 2^3 above it; what lies more than 2^19 below it keeps fewer bits
 // (float16's smallest step).  So c is one number a row and the softmax has no scales to look up.
 // Values the same, with O in units of 2^e_ref.  Queries are rounded to float16 once after their rotation,
-// each row at a power of two.
+// each row at a power of two (for outputs of float16 and heads of 64, where there is room, as two float16:
+// their rounding would add as much again as the output's own).
 //
 // Warps: 0 to 3 and 4 to 7 softmax and output of tile 0 and 1, 8 to 11 operands, 12 products, 13 the
 // pages and scales of the steps ahead, 14 what there is to join.
@@ -64,7 +65,9 @@ struct Layout {
   static constexpr uint32_t kChunk = 128 * 128;            // bytes
   static constexpr uint32_t kTile = kChunks * kChunk;      // 128 rows
   static constexpr uint32_t kKeysAt = 2 * kTile, kValuesAt = kKeysAt + kStages * kTile;
-  static constexpr uint32_t kStepsAt = kValuesAt + kStages * kTile;
+  static constexpr bool kFine = DIM == 64;  // room for what the queries' rounding leaves
+  static constexpr uint32_t kRestAt = kValuesAt + kStages * kTile;
+  static constexpr uint32_t kStepsAt = kRestAt + (kFine ? 2 * kTile : 0);
   static constexpr size_t kBytes = kStepsAt + kAhead * sizeof(Step) + 1024;
 };
 
@@ -108,7 +111,7 @@ template <int N>
 __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-constexpr int kSoftmaxRegisters = 176, kOperandRegisters = 104, kProductRegisters = 56;
+constexpr int kSoftmaxRegisters = 184, kOperandRegisters = 96, kProductRegisters = 48;
 static_assert(2 * kSoftmaxRegisters + kOperandRegisters + kProductRegisters <= 4 * 128, "what the CTA has");
 
 // 2^e in two factors, for -252 <= e <= 254.
@@ -191,8 +194,16 @@ __device__ __noinline__ void stage_queries(const AttentionParams& p, const Walk&
       uint32_t x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = pair_from_float<__half>(v[8 * k + 2 * j] * up, v[8 * k + 2 * j + 1] * up);
-      *(uint4*)(memory + t * L::kTile + (DIM == 128 ? k * L::kChunk : 0) + r * 128 + ((piece ^ (r & 7)) << 4)) =
-          make_uint4(x[0], x[1], x[2], x[3]);
+      uint8_t* to = memory + t * L::kTile + (DIM == 128 ? k * L::kChunk : 0) + r * 128 + ((piece ^ (r & 7)) << 4);
+      *(uint4*)to = make_uint4(x[0], x[1], x[2], x[3]);
+      if (L::kFine && p.type == FWT_F16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 high = pair_to_float<__half>(x[j]);
+          x[j] = pair_from_float<__half>(v[8 * k + 2 * j] * up - high.x, v[8 * k + 2 * j + 1] * up - high.y);
+        }
+        *(uint4*)(to + L::kRestAt) = make_uint4(x[0], x[1], x[2], x[3]);
+      }
     }
     if (part == 0) row_scale[128 * t + r] = fabsf(p.scale) * __uint_as_float((uint32_t)(e - 14) << 23);
   }
@@ -517,6 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           for (int kk = 0; kk < DIM / 16; ++kk) {
             const uint32_t at = (kk >> 2) * (L::kChunk >> 4) + (kk & 3) * 2;
             mma_tile<1, 2>(tmem + kScoresAt + 128 * t, a + at, b + at, kOfScores, kk > 0);
+            if (L::kFine && p.type == FWT_F16)
+              mma_tile<1, 2>(tmem + kScoresAt + 128 * t, a + (L::kRestAt >> 4) + at, b + at, kOfScores, 1);
           }
           mma_commit<1>(&s_full[t]);
         }
@@ -539,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           const bool more = step + 1 < count;
           for (int t = 0; t < tiles; ++t) {
             if (t == 0 && !wait_or_leave(&v_full[stage], steps / kStages & 1, &gave_up)) return;
+            const uint64_t b = operand(base + L::kValuesAt + stage * L::kTile, L::kChunk);
             if (!wait_or_leave(&p_full[t], turns[t] & 1, &gave_up)) return;
             ++turns[t];
             tmem_fence_after();
-            const uint64_t b = operand(base + L::kValuesAt + stage * L::kTile, L::kChunk);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 rows of values, 8 columns of pairs of P

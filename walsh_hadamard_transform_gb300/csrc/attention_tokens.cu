@@ -16,7 +16,8 @@
 // values multiply p.  P is rounded to float16 as p * 2^(15 + e - e_max), at most 2^15, e the scale's
 // exponent and e_max the largest so far: half a unit in 2^-11, down to 2^-29 of the largest possible.
 // Queries are rounded to float16 once after their rotation, each row at a power of two that takes
-// its largest to 2^14.
+// its largest to 2^14.  (For outputs of float16 both keep what the rounding leaves as a second float16:
+// errors against 64 bits are 2.0e-4 then, the output's own rounding, and 3.6e-4 without.)
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -78,8 +79,15 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
   return row * DIM + ((piece ^ (DIM == 128 ? row & 6 : (row >> 1) & 3)) << 4);
 }
 
-// NT: groups of 8 rows.
-template <int DIM, int NT>
+// The part of a pair that its rounding to float16 `high` leaves, rounded to float16.
+__device__ __forceinline__ uint32_t rest_f16x2(float a, float b, uint32_t high) {
+  const float2 h = pair_to_float<__half>(high);
+  return pair_from_float<__half>(a - h.x, b - h.y);
+}
+
+// NT: groups of 8 rows.  FINE: queries and p as two float16 each, for outputs of float16, whose own half
+// unit one rounding of them would pass (the tensor cores have time to spare here).
+template <int DIM, int NT, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const AttentionParams p) {
   using L = Layout<DIM>;
   constexpr int kRows = 8 * NT, kTiles = DIM / 16, kHalves = DIM / 64;
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
 
     // queries: rotated, a power of two for each row, float16; thread (g, c) has of row g the 16
     // elements from 64 j + 16 c on
-    uint32_t q[NT][kHalves][8];
+    uint32_t q[NT][kHalves][8], q_rest[FINE ? NT : 1][kHalves][8];
     float scale[NT][2];
     Keys seen[NT][2];
 #pragma unroll
@@ -233,7 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
       const int e = max((int)(most >> 23), 27);  // (zero, and what is nearly so)
       const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
 #pragma unroll
-      for (int i = 0; i < kHalves * 8; ++i) q[n][i / 8][i & 7] = pair_from_float<__half>(v[2 * i] * up, v[2 * i + 1] * up);
+      for (int i = 0; i < kHalves * 8; ++i) {
+        q[n][i / 8][i & 7] = pair_from_float<__half>(v[2 * i] * up, v[2 * i + 1] * up);
+        if constexpr (FINE) q_rest[n][i / 8][i & 7] = rest_f16x2(v[2 * i] * up, v[2 * i + 1] * up, q[n][i / 8][i & 7]);
+      }
       const float mine = p.scale * __uint_as_float((uint32_t)(e - 14) << 23);
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {  // of the rows that the scores' fragment has here
@@ -288,7 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
             const uint32_t a0 = e4m3_to_f16x2(lo[i]), a2 = e4m3_to_f16x2(lo[i] >> 16);
             const uint32_t a1 = e4m3_to_f16x2(hi[i]), a3 = e4m3_to_f16x2(hi[i] >> 16);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(s[t][n], a0, a1, a2, a3, q[n][j][2 * i], q[n][j][2 * i + 1]);
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(s[t][n], a0, a1, a2, a3, q[n][j][2 * i], q[n][j][2 * i + 1]);
+              if constexpr (FINE) mma_f16(s[t][n], a0, a1, a2, a3, q_rest[n][j][2 * i], q_rest[n][j][2 * i + 1]);
+            }
           }
         }
       }
@@ -356,15 +370,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
             for (int e = 0; e < 4; ++e) o[i][n][e] *= keep[n][e & 1] * less;
       }
       // p with the values' scales, as the second product's columns
-      uint32_t b[2][NT][2];
+      uint32_t b[2][NT][2], b_rest[2][FINE ? NT : 1][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float f = __uint_as_float((uint32_t)max(127 + 15 + value_byte[t][h] - most, 0) << 23);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            b[t][n][h] = transpose8x8(pair_from_float<__half>(s[t][n][2 * h] * f, s[t][n][2 * h + 1] * f));
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t high = pair_from_float<__half>(s[t][n][2 * h] * f, s[t][n][2 * h + 1] * f);
+            b[t][n][h] = transpose8x8(high);
+            if constexpr (FINE) b_rest[t][n][h] = transpose8x8(rest_f16x2(s[t][n][2 * h] * f, s[t][n][2 * h + 1] * f, high));
+          }
         }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -389,7 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
           const uint32_t a0 = e4m3_to_f16x2(w0), a1 = e4m3_to_f16x2(w0 >> 16);
           const uint32_t a2 = e4m3_to_f16x2(w1), a3 = e4m3_to_f16x2(w1 >> 16);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[i][n], a0, a1, a2, a3, b[t][n][0], b[t][n][1]);
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[i][n], a0, a1, a2, a3, b[t][n][0], b[t][n][1]);
+            if constexpr (FINE) mma_f16(o[i][n], a0, a1, a2, a3, b_rest[t][n][0], b_rest[t][n][1]);
+          }
         }
       }
       __syncwarp();
@@ -458,19 +478,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
   if (lane == 0 && !tail) p.notes[2 * worker] = make_int4(0, 0, 0, 0);
 }
 
-template <int DIM, int NT>
+template <int DIM, int NT, bool FINE>
 cudaError_t launch(const AttentionParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const int ctas = std::min(multiprocessors(), kMostCtas);
   log_kernel("cache_attention tokens=%d heads=%dx%d dim=%d sequences=%d | rows=%d ctas=%d", p.at.tokens,
              p.cache.heads, p.group, DIM, p.at.sequences, 8 * NT, ctas);
-  const cudaError_t err = launch_cluster(attention_tokens_kernel<DIM, NT>, ready, (unsigned)ctas, kThreads,
+  const cudaError_t err = launch_cluster(attention_tokens_kernel<DIM, NT, FINE>, ready, (unsigned)ctas, kThreads,
                                          Layout<DIM>::kBytes, 1, st, p);
   return err == cudaSuccess ? launch_attention_join(p, 8 * NT, kWarps * ctas, st) : err;
 }
 template <int DIM>
 cudaError_t launch_rows(const AttentionParams& p, int rows, cudaStream_t st) {
-  return rows == 8 ? launch<DIM, 1>(p, st) : launch<DIM, 2>(p, st);
+  if (p.type == FWT_F16) return rows == 8 ? launch<DIM, 1, true>(p, st) : launch<DIM, 2, true>(p, st);
+  return rows == 8 ? launch<DIM, 1, false>(p, st) : launch<DIM, 2, false>(p, st);
 }
 
 }  // namespace

@@ -80,7 +80,7 @@ struct Call {
 
 int check_cache(const fwt_cache* c, Call& call) {
   if (!c || (c->dim != 64 && c->dim != 128) || c->heads < 1 || c->heads > 65536 || c->page_tokens < 16 ||
-      c->page_tokens > (1 << 20) || c->page_tokens % 16 || c->pages < 0 || c->pages > 0x7fffffff)
+      c->page_tokens > (1 << 20) || c->page_tokens % 16 || (int64_t)c->heads * c->page_tokens > 0x7fffffff || c->pages < 0 || c->pages > 0x7fffffff)
     return FWT_ERR_INVALID_ARG;
   uint8_t* const codes[2] = {(uint8_t*)c->k, (uint8_t*)c->v};
   uint8_t* const scales[2] = {(uint8_t*)c->k_scale, (uint8_t*)c->v_scale};
@@ -226,7 +226,7 @@ int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* ou
   if (st == FWT_ERR_INVALID_ARG || rot_bits < 0 || rot_bits > most_rotation(cache->dim)) return FWT_ERR_INVALID_ARG;
   if (q_heads < 1 || q_heads > 65536 || q_heads % cache->heads) return FWT_ERR_INVALID_ARG;
   const int places = check_places(sequences, tokens, call);
-  if (places == FWT_ERR_INVALID_ARG || tokens * q_heads > 0x7fffffff) return FWT_ERR_INVALID_ARG;
+  if (places == FWT_ERR_INVALID_ARG || tokens * q_heads > 0x7ffffe00) return FWT_ERR_INVALID_ARG;
   if (tokens == 0 || sequences->sequences == 0) return FWT_OK;
   const Rows rows[2] = {{const_cast<void*>(q), q_token, q_head}, {out, out_token, out_head}};
   Span spans[2];
