@@ -2,7 +2,7 @@
 //
 // An item is a block of ROWS rows (new tokens x query heads of one key head) of a sequence with one
 // key head; its keys, from the first that one of its rows sees, are cut into units of UNIT tokens, at
-// least one.  All units of the call, in the order of sequences, key heads, blocks, are dealt out in
+// least one; what an item costs besides its keys counts as EXTRA units before them.  All units of the call, in the order of sequences, key heads, blocks, are dealt out in
 // equal consecutive shares, so that no worker's time depends on how lengths are spread; a share
 // begins and ends inside an item as it may.  Workers are CTAs, or warps where an item has few rows.
 // The host does not know the lengths: every CTA adds them up for itself.
@@ -51,16 +51,22 @@ __device__ __forceinline__ int units_of(const Keys& k) {
   return max(1, (k.high - k.low + UNIT - 1) / UNIT);
 }
 
+// The same with what stands for the item itself.
+template <int UNIT, int EXTRA>
+__device__ __forceinline__ int cost_of(const Keys& k) {
+  return EXTRA + units_of<UNIT>(k);
+}
+
 // Units of one key head of the sequences of a warp's lanes (sequence b in each; count 0: none).
 // (Loops here are not unrolled, and divisions few: code that runs once comes from memory, and with 150 and
 // 320 KB of it the kernels took twice as long.)
-template <int ROWS, int UNIT>
+template <int ROWS, int UNIT, int EXTRA>
 __device__ __forceinline__ int64_t units_of_sequence(const AttentionParams& p, const Sequence& s, int lane) {
   constexpr int kAlone = 4;  // blocks that a lane counts by itself
   const int blocks = blocks_of<ROWS>(p, s);
   int64_t units = 0;
   if (blocks <= kAlone)
-    for (int i = 0; i < blocks; ++i) units += units_of<UNIT>(keys_of<ROWS>(p, s, i));
+    for (int i = 0; i < blocks; ++i) units += cost_of<UNIT, EXTRA>(keys_of<ROWS>(p, s, i));
   for (uint32_t many = __ballot_sync(~0u, blocks > kAlone); many; many &= many - 1) {
     const int from = __ffs(many) - 1;
     Sequence t;
@@ -68,7 +74,7 @@ __device__ __forceinline__ int64_t units_of_sequence(const AttentionParams& p, c
     t.count = __shfl_sync(~0u, s.count, from), t.length = __shfl_sync(~0u, s.length, from);
     const int n = __shfl_sync(~0u, blocks, from);
     int64_t sum = 0;
-    for (int i = lane; i < n; i += 32) sum += units_of<UNIT>(keys_of<ROWS>(p, t, i));
+    for (int i = lane; i < n; i += 32) sum += cost_of<UNIT, EXTRA>(keys_of<ROWS>(p, t, i));
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     if (lane == from) units = sum;
@@ -81,8 +87,9 @@ struct Walk {
   int b, head, block;
   Sequence s;
   Keys keys;
-  int unit, units;  // of the item: the next one, and all
-  int64_t left;     // units of the share from `unit` on
+  int unit, units;  // of the item's keys: the next one, and all
+  int skip;         // units before them
+  int64_t left;     // units of the share, `skip` among them; more than that, or 0 at its end
   int64_t each;     // of every share, and one more of the first `more`
   int more;
 };
@@ -94,7 +101,7 @@ struct PlanScratch {
 
 // The share of worker `worker` of `workers`, at least LEAST units while there are enough; every thread of
 // the CTA calls it, with a worker of its warp's.  left = 0: there is none.
-template <int ROWS, int UNIT, int LEAST, int THREADS>
+template <int ROWS, int UNIT, int EXTRA, int LEAST, int THREADS>
 __device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker, int workers, PlanScratch& scratch) {
   const int lane = threadIdx.x & 31, heads = p.cache.heads;
   const int span = (p.at.sequences + 32 * kGroups - 1) / (32 * kGroups) * 32;  // sequences of a group
@@ -103,7 +110,7 @@ __device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker,
   const auto units_at = [&](int b) {
     s.count = 0;
     if (b < p.at.sequences) s = sequence(p.at, p.cache.page_tokens, b);
-    return units_of_sequence<ROWS, UNIT>(p, s, lane);
+    return units_of_sequence<ROWS, UNIT, EXTRA>(p, s, lane);
   };
   // (32 values of a warp added up from the first on)
   const auto upto = [&](int64_t v) {
@@ -129,7 +136,7 @@ __device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker,
     total += __shfl_sync(~0u, upto(i0 + lane < groups ? scratch.units[i0 + lane] : 0), 31);
   total *= heads;
   Walk walk;
-  walk.left = walk.each = 0, walk.more = 0, walk.unit = walk.units = 0, walk.b = walk.head = walk.block = 0;
+  walk.left = walk.each = 0, walk.more = 0, walk.unit = walk.units = walk.skip = 0, walk.b = walk.head = walk.block = 0;
   walk.s = Sequence{0, 0, 0}, walk.keys = Keys{0, 0};
   const int shares = (int)min((int64_t)workers, (total + LEAST - 1) / LEAST);
   if (worker >= shares) return walk;
@@ -160,24 +167,29 @@ __device__ __forceinline__ Walk find_share(const AttentionParams& p, int worker,
   walk.head = rem < 0x7fffffff && per_head < 0x7fffffff ? (int)rem / (int)per_head : (int)(rem / per_head);
   rem -= walk.head * per_head;
   walk.block = find(blocks, 1, [&](int i) {
-    return (int64_t)(i < blocks ? units_of<UNIT>(keys_of<ROWS>(p, walk.s, i)) : 0);
+    return (int64_t)(i < blocks ? cost_of<UNIT, EXTRA>(keys_of<ROWS>(p, walk.s, i)) : 0);
   });
-  walk.unit = (int)rem;
+  walk.skip = max(EXTRA - (int)rem, 0), walk.unit = max((int)rem - EXTRA, 0);
+  if (walk.left <= walk.skip) walk.left = 0;  // (the next worker has the item)
   walk.keys = keys_of<ROWS>(p, walk.s, walk.block);
   walk.units = units_of<UNIT>(walk.keys);
   return walk;
 }
 
-// Units of the share that are the present item's.
+// Units of the present item's keys in the share.
 __device__ __forceinline__ int piece_units(const Walk& w) {
-  return (int)min(w.left, (int64_t)(w.units - w.unit));
+  return (int)min(w.left - w.skip, (int64_t)(w.units - w.unit));
 }
 
 // On to the next item of the share, if there is one.
-template <int ROWS, int UNIT>
+template <int ROWS, int UNIT, int EXTRA>
 __device__ __forceinline__ void next_piece(const AttentionParams& p, Walk& w) {
-  w.left -= piece_units(w);
-  if (w.left <= 0) return;
+  w.left -= w.skip + piece_units(w);
+  w.skip = EXTRA;
+  if (w.left <= EXTRA) {
+    w.left = 0;
+    return;
+  }
   w.unit = 0;
   if (++w.block == blocks_of<ROWS>(p, w.s)) {
     w.block = 0;

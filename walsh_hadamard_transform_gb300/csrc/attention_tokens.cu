@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kWarps = kTokenWorkers, kThreads = kWarps * 32;
 constexpr int kStep = 32;   // tokens that a warp takes at a time
+constexpr int kExtra = 1;   // steps that an item costs besides
 constexpr int kLeast = 4;   // steps of a share: fewer cost more in joining than they save (one sequence of 4099: 20.3 us,
                             // with 2 22.4, 8 22.7, 16 31.0)
 
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
   // (in shared memory: a step needs little of them)
   Walk &walk = walks[warp][0], &ahead = walks[warp][1];
   {
-    const Walk share = find_share<kRows, kStep, kLeast, kThreads>(p, worker, kWarps * (int)gridDim.x, scratch);
+    const Walk share = find_share<kRows, kStep, kExtra, kLeast, kThreads>(p, worker, kWarps * (int)gridDim.x, scratch);
     if (lane == 0) walk = ahead = share;
     __syncwarp();
   }
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
   }
   const auto advance = [&](Walk& w) {
     __syncwarp();
-    if (lane == 0) next_piece<kRows, kStep>(p, w);
+    if (lane == 0) next_piece<kRows, kStep, kExtra>(p, w);
     __syncwarp();
   };
 
