@@ -447,7 +447,10 @@ int fwt_cache_read(const fwt_cache* cache, const fwt_sequences* sequences, int r
  *
  * Scores, softmax and sums are fp32.  Queries after the rotation, and p = 2^(score - maximum), are
  * rounded to float16 (tensor-core operands; half a unit is 2^-11), both held at powers of two that
- * keep them in its range; codes become float16 exactly.
+ * keep them in its range; codes become float16 exactly.  For FWT_F16 and at most 16 rows (longest new
+ * tokens x q_heads / heads) both are two float16 each, and for heads of 64 and more rows queries are.
+ * Where there are more rows, what lies more than 2^19 below the largest scale among the first 128 keys
+ * of a sequence and head (or a later one over eight times that) keeps fewer bits.
  *
  * longest: the most new tokens of any sequence, as far as the host knows (0: as if all had the
  * same); it chooses between kernels and sizes the workspace, and a wrong one costs only time.

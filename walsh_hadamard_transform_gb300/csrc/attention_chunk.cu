@@ -21,6 +21,14 @@
 // each row at a power of two (for outputs of float16 and heads of 64, where there is room, as two float16:
 // their rounding would add as much again as the output's own).
 //
+// Bound, large: the chain of a tile, softmax (some 2000 clocks) and its two products (1000), of which
+// two are under way at a time; the issue slots and the exponentials (32 a clock an SM, 1024 clocks a step
+// of both tiles) are not full.  4096 tokens by 32 query and 8 key heads of 128 over 32768: 1.87 ms, 1.1
+// PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries and output, some eight steps an item;
+// 8192 tokens by 16 heads 0.42 ms, 0.66 PFLOP/s.  With scores read twice instead of held in 128 registers
+// (so no split of registers among the warps) the first took 4.9 ms; with the softmax at 176 and the operands
+// at 104 registers 1.88, at 192 and 80, which spills, 2.24.
+//
 // Warps: 0 to 3 and 4 to 7 softmax and output of tile 0 and 1, 8 to 11 operands, 12 products, 13 the
 // pages and scales of the steps ahead, 14 what there is to join.
 #include <algorithm>
@@ -45,7 +53,9 @@ constexpr int kThreads = 512;
 constexpr int kKeys = 128;    // of a step; a unit of the plan
 constexpr int kStages = 2;    // of keys, and of values
 constexpr int kAhead = 4;     // steps known at a time
-constexpr int kExtra = 6;     // steps that an item costs besides: its queries and its output
+// Steps that an item costs besides, its queries and its output (measured, us, at 0, 6, 10, 16: 8192 tokens by 16
+// heads 481, 431, 414, 423; five ragged chunks of up to 701 tokens 74, 58, 61, 65).
+constexpr int kExtra = 8;
 constexpr float kLag = 8.f;   // of a row's maximum, in powers of two
 
 // What a step's keys are, found by one warp some steps ahead and kept until its last product.
@@ -86,23 +96,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // Registers a thread from here on, for whole warpgroups: their sum stays what the CTA started with
 // (4 x 128 x 128).
 template <int N>

@@ -12,8 +12,12 @@
 // of a key, and of two values that are neighbours in P one byte each side by side.  Queries and
 // outputs are turned in those fragments' layouts too.  (With the warps of a CTA on one item, and their sums
 // joined in shared memory, an item cost 15,000 clocks besides its keys: 64 sequences of 256 to 16384 tokens
-// 237 us.)  Codes become float16 without a rounding; the scales of keys multiply scores, those of
-// values multiply p.  P is rounded to float16 as p * 2^(15 + e - e_max), at most 2^15, e the scale's
+// 237 us.)  These, 32 query and 8 key heads of 128, now take 98 us, 5.1 TB/s; what is left is the copies'
+// own pace (they stall on a full queue, no wait for data) and items of few keys.  One sequence of 4099
+// tokens: 19 us in both launches, mostly a chain of lookups (sequence, page, codes) and the join.
+//
+// Codes become float16 without a rounding; the scales of keys multiply scores, those of values
+// multiply p.  P is rounded to float16 as p * 2^(15 + e - e_max), at most 2^15, e the scale's
 // exponent and e_max the largest so far: half a unit in 2^-11, down to 2^-29 of the largest possible.
 // Queries are rounded to float16 once after their rotation, each row at a power of two that takes
 // its largest to 2^14.  (For outputs of float16 both keep what the rounding leaves as a second float16:
@@ -37,7 +41,8 @@ namespace {
 
 constexpr int kWarps = kTokenWorkers, kThreads = kWarps * 32;
 constexpr int kStep = 32;   // tokens that a warp takes at a time
-constexpr int kExtra = 1;   // steps that an item costs besides
+// Steps that an item costs besides (64 decoding sequences: 109 us at 0, 102 at 1, 98 at 2).
+constexpr int kExtra = 2;
 constexpr int kLeast = 4;   // steps of a share: fewer cost more in joining than they save (one sequence of 4099: 20.3 us,
                             // with 2 22.4, 8 22.7, 16 31.0)
 

@@ -11,6 +11,10 @@
 //
 // Rows of several sequences lie one after the other; a CTA counts how many sequences end at or
 // before its first row, and its rows go on from there.
+//
+// Bound, large: issue slots, some 600 instructions a thread for a key's and a value's 16 elements each (of
+// 8192 x 8 x 128 bf16 18 us, 2.7 TB/s; every byte once takes 7.4).  Reading back 4 x 4096 x 8 x 128 27 us,
+// 3.7 TB/s (14.8).  Small: the chain of lookups, 3.3 us.
 #include <cstdint>
 #include <type_traits>
 
@@ -108,7 +112,7 @@ __device__ __forceinline__ void store8(T* to, const float* v) {
 }
 
 template <typename T, int DIM>
-__global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const MoveParams p) {
   constexpr int kLanes = DIM / 16, kRows = kThreads / kLanes;
   const int lane = threadIdx.x & (kLanes - 1), r = p.rot_bits;
   const FirstRow first = first_row(p, (int64_t)blockIdx.x * kRows);
@@ -130,31 +134,45 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
   const int before = sequences_before(p.at, first.token);
   int page, slot;
   if (token >= p.at.tokens || !locate(p, token, before, page, slot)) page = -1;
-  const float norm = 16.f * rotation_norm(r);
+  // 16 * 2^(-r/2) in two floats, and the product with them to the last bit but rarely: codes then differ from
+  // those of exact arithmetic only where the sums do
+  const float norm = r ? 16.f * rotation_norm(r) : 1.f;
+  const float norm_rest = r & 1 ? 16.f * __uint_as_float((uint32_t)(127 - r / 2) << 23) * 1.21016171e-8f : 0.f;
+  const auto times = [](float2 x, float high, float rest) {
+    const float2 h = make_float2(high, high), l = make_float2(rest, rest);
+    const float2 p = fma_pair(x, h, make_float2(-0.f, -0.f));
+    return add_pair(p, fma_pair(x, l, fma_pair(x, h, make_float2(-p.x, -p.y))));
+  };
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
     if (r) {  // 1/16 first, so that no sum of 128 overflows before the norm
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[o][i] *= 0.0625f;
       turn_spread<DIM>(v[o], r, lane);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[o][i] *= norm;
     }
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(v[o][i])));
+    most = times(make_float2(most, most), norm, norm_rest).x;
     uint32_t top = __float_as_uint(most) & 0x7fffffffu;  // NaN is above all
 #pragma unroll
     for (int step = 1; step < kLanes; step *= 2) top = max(top, __shfl_xor_sync(~0u, top, step));
     const uint32_t byte = scale_byte(__uint_as_float(top));
-    const float inverse = __uint_as_float((254u - byte) << 23);
+    // the norm and 1 / s in one product (in two where that could overflow)
+    const uint32_t inverse = 254u - byte;
+    const float power = __uint_as_float(min(inverse, 240u) << 23), factor = power * norm, factor_rest = power * norm_rest;
+    if (inverse > 240u) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[o][i] *= __uint_as_float((127u + min(inverse - 240u, 14u)) << 23);
+    }
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = byte == 255u ? 0u
-                          : f32x2_to_e4m3(v[o][4 * i] * inverse, v[o][4 * i + 1] * inverse) |
-                                f32x2_to_e4m3(v[o][4 * i + 2] * inverse, v[o][4 * i + 3] * inverse) << 16;
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = times(make_float2(v[o][4 * i], v[o][4 * i + 1]), factor, factor_rest);
+      const float2 y = times(make_float2(v[o][4 * i + 2], v[o][4 * i + 3]), factor, factor_rest);
+      w[i] = byte == 255u ? 0u : f32x2_to_e4m3(x.x, x.y) | f32x2_to_e4m3(y.x, y.y) << 16;
+    }
     if (page >= 0) {
       const int64_t at = (int64_t)head * p.cache.page_tokens + slot;
       uint8_t* codes = p.cache.codes[o] + page * p.cache.code_stride[o] + at * DIM + 8 * lane;
@@ -166,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const MoveParams p) {
 }
 
 template <typename T, int DIM>
-__global__ void __launch_bounds__(kThreads) read_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 4) read_kernel(const MoveParams p) {
   constexpr int kLanes = DIM / 16, kRows = kThreads / kLanes;
   const int lane = threadIdx.x & (kLanes - 1), r = p.rot_bits;
   const FirstRow first = first_row(p, (int64_t)blockIdx.x * (kRows * kReadRows));
