@@ -34,7 +34,7 @@ OF_CACHE = [
 ]
 OF_PLACES = [
     (dict(table=None), E), (dict(starts=None), E), (dict(lengths=None), E), (dict(sequences=-1), E),
-    (dict(sequences=1 << 31), E), (dict(most_pages=-1), E), (dict(most_pages=1 << 31), E), (dict(ld_table=4), E),
+    (dict(sequences=(1 << 30) + 1), E), (dict(most_pages=-1), E), (dict(most_pages=1 << 31), E), (dict(ld_table=4), E),
     (dict(ld_table=1 << 60), E), (dict(starts=A + 2), MIS), (dict(table=A + 1), MIS),
 ]
 REFUSED = {

@@ -87,3 +87,22 @@ def test_calls_after_one_another(new):
     assert torch.isfinite(results[0][0]).all()
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_thousands_of_sequences():
+    """More sequences than one group of the plan holds: as in calls of a few thousand each.  (No item is cut:
+    each has one step.)"""
+    n = 9001
+    pr = Problem([1 + i % 2 for i in range(n)], [2 + i % 30 for i in range(n)], 1, 64, 16, seed=24)
+    q = (torch.randn(pr.tokens, 2, 64) * 0.3).bfloat16().cuda()
+    for longest in (1, 40):  # both kernels
+        got = fwt.cache_attention(q, *pr.places(), longest=longest)
+        for b0 in range(0, n, 3001):
+            b1 = min(n, b0 + 3001)
+            first, last = int(pr.starts[b0]), int(pr.starts[b1])
+            part = fwt.cache_attention(q[first:last], pr.cache, pr.table[b0:b1], pr.starts[b0:b1 + 1] - first,
+                                       pr.lengths[b0:b1], longest=longest)
+            assert torch.equal(part, got[first:last])
+        few = Problem.__new__(Problem)
+        few.__dict__.update(pr.__dict__, starts=pr.starts[:40], lengths=pr.lengths[:39], table=pr.table[:39])
+        check_attention(got, few, q, 6, "bf16")

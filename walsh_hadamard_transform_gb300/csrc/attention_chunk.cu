@@ -696,6 +696,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
 template <int DIM>
 cudaError_t launch(const AttentionParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
+  // The warpgroups' registers come out of what the CTA starts with; with less they would wait for ever.
+  static std::atomic<int> registers{0};
+  int each = registers.load(std::memory_order_relaxed);
+  if (!each) {
+    cudaFuncAttributes attributes;
+    const cudaError_t err = cudaFuncGetAttributes(&attributes, (const void*)attention_chunk_kernel<DIM>);
+    if (err != cudaSuccess) return err;
+    registers.store(each = attributes.numRegs, std::memory_order_relaxed);
+  }
+  if (4 * each < 2 * kSoftmaxRegisters + kOperandRegisters + kProductRegisters) return cudaErrorInvalidConfiguration;
   const int ctas = std::min(multiprocessors(), kMostCtas);
   log_kernel("cache_attention tokens=%d heads=%dx%d dim=%d sequences=%d | rows=%d ctas=%d", p.at.tokens,
              p.cache.heads, p.group, DIM, p.at.sequences, kChunkRows, ctas);

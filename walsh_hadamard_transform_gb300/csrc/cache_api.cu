@@ -105,7 +105,7 @@ int check_cache(const fwt_cache* c, Call& call) {
 }
 
 int check_places(const fwt_sequences* s, int64_t tokens, Call& call) {
-  if (!s || s->sequences < 0 || s->sequences > 0x7fffff00 || s->most_pages < 0 ||
+  if (!s || s->sequences < 0 || s->sequences > kMostTokens || s->most_pages < 0 ||
       s->most_pages > 0x7fffffff || tokens < 0 || tokens > kMostTokens)
     return FWT_ERR_INVALID_ARG;
   if (s->sequences && (!s->starts || !s->lengths || (s->most_pages && !s->table))) return FWT_ERR_INVALID_ARG;
