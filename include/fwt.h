@@ -447,7 +447,8 @@ int fwt_cache_read(const fwt_cache* cache, const fwt_sequences* sequences, int r
  *
  * Scores, softmax and sums are fp32.  Queries after the rotation, and p = 2^(score - maximum), are
  * rounded to float16 (tensor-core operands; half a unit is 2^-11), both held at powers of two that
- * keep them in its range; codes become float16 exactly.  For FWT_F16 and at most 16 rows (longest new
+ * keep them in its range: p keeps its bits down to 2^-25 of a row's largest, and below has steps of 2^-35
+ * of it.  Codes become float16 exactly.  For FWT_F16 and at most 16 rows (longest new
  * tokens x q_heads / heads) both are two float16 each, and for heads of 64 and more rows queries are.
  * Where there are more rows, what lies more than 2^19 below the largest scale among the first 128 keys
  * of a sequence and head (or a later one over eight times that) keeps fewer bits.

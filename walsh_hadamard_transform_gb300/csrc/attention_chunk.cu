@@ -5,12 +5,14 @@
 // step
 //
 //   S = Q K^T            128 x 128 in tensor memory
-//   P = 2^(c S - m)      a row a thread; float16, over S in tensor memory; l += P in fp32
+//   P = 2^(c S - m + 11) a row a thread; float16, over S in tensor memory; l += P in fp32
 //   O += P V             in tensor memory, fp32
 //
 // and the two tiles take turns: while the tensor cores work on one, the other's softmax runs.  m is a
-// maximum of the row that may lag behind by a factor of 2^8 in P: only a larger step multiplies O
-// again, which is rare after the first keys.
+// maximum of the row that may lag behind by a factor of 2^4 in P: only a larger step multiplies O
+// again, which is rare after the first keys.  So P is at most 2^15, and of a probability p, the row's largest 1,
+// float16 keeps all its bits down to 2^-25 and steps of 2^-35 below: many small ones next to a large one are
+// a part of the output, whether the large one's value is or not.  (Both times 2^11, so O / l is the output.)
 //
 // Four warps turn codes into float16 operands in the layout the products read (128-byte swizzle; keys
 // along the contraction, values across it).  The scales go in with them, exactly: a key's
@@ -56,7 +58,9 @@ constexpr int kAhead = 4;     // steps known at a time
 // Steps that an item costs besides, its queries and its output (measured, us, at 0, 6, 10, 16: 8192 tokens by 16
 // heads 481, 431, 414, 423; five ragged chunks of up to 701 tokens 74, 58, 61, 65).
 constexpr int kExtra = 8;
-constexpr float kLag = 8.f;   // of a row's maximum, in powers of two
+// How far P may pass a row's maximum, in powers of two, and what lifts P: together 15, what float16 has.  (8 and 7
+// lose small P sooner and measured 0.5% faster: 8192 tokens by 16 heads 421 and 423 us.)
+constexpr float kLag = 4.f, kLift = 11.f;
 
 // What a step's keys are, found by one warp some steps ahead and kept until its last product.
 struct alignas(16) Step {  // (its factors are written 16 bytes at a time)
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
             if (most > top) top = most;
           }
           const bool moved = step > 0 && __any_sync(~0u, again || new_ref != value_ref);
-          const float shift = top == -INFINITY ? 0.f : -top;
+          const float shift = top == -INFINITY ? 0.f : kLift - top;
           const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
           float2 sums[4];
 #pragma unroll
