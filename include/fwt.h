@@ -398,7 +398,7 @@ typedef struct fwt_cache {
  * The host reads none of it.  `starts` rises from 0 to at most `tokens`; rows behind starts[sequences]
  * belong to no sequence: what they hold does not matter, and rows of outputs there are not written.  What could point
  * outside is taken as it would be nearest: starts beyond `tokens` as `tokens`, lengths below 0
- * as 0 and beyond the table as the table's room; a page below 0 or not below `pages` holds no tokens,
+ * as 0 and beyond the table's room, or 2^31 - 2^16, as that; a page below 0 or not below `pages` holds no tokens,
  * and nor do positions below 0.
  */
 typedef struct fwt_sequences {

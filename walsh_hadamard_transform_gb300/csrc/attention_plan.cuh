@@ -42,7 +42,7 @@ __device__ __forceinline__ Keys keys_of(const AttentionParams& p, const Sequence
   const int own = s.length - s.count;  // position of the first new token
   Keys k;
   k.high = p.causal ? min(s.length, max(own + last + 1, 0)) : s.length;
-  k.low = p.window ? min(max(own + first + 1 - p.window, 0), k.high) & ~15 : 0;
+  k.low = p.window ? min(max(max(own + first + 1, 0) - p.window, 0), k.high) & ~15 : 0;  // (of 31 bits each)
   return k;
 }
 
@@ -223,7 +223,7 @@ __device__ __forceinline__ Keys seen_by(const AttentionParams& p, const Sequence
   const int own = s.length - s.count + quotient(r, p.by_group);
   Keys k;
   k.high = p.causal ? min(s.length, max(own + 1, 0)) : s.length;
-  k.low = p.window ? max(own + 1 - p.window, 0) : 0;
+  k.low = p.window ? max(max(own + 1, 0) - p.window, 0) : 0;
   return k;
 }
 
