@@ -156,7 +156,7 @@ __device__ __forceinline__ void stage_queries(const AttentionParams& p, const Wa
   const int lane = threadIdx.x & 31, sub = lane / kLanes, part = lane & (kLanes - 1);
   const int row0 = 32 * (threadIdx.x >> 5 & 3) + sub, rows = rows_of(p, w) - 128 * t;
   if (rows <= 0) return;
-  const float norm = rotation_norm(p.rot_bits) * (p.scale < 0.f ? -1.f : 1.f);
+  const float before = rotation_before(p.rot_bits), norm = rotation_after(p.rot_bits) * (p.scale < 0.f ? -1.f : 1.f);
   constexpr int kBatch = 2;  // rows on their way at a time
 #pragma unroll 1
   for (int r0 = row0; r0 < row0 + 32; r0 += kBatch * kRows) {
@@ -182,7 +182,7 @@ __device__ __forceinline__ void stage_queries(const AttentionParams& p, const Wa
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = pair_to_float(x[j], p.type);
-          v[8 * k + 2 * j] = f.x, v[8 * k + 2 * j + 1] = f.y;
+          v[8 * k + 2 * j] = f.x * before, v[8 * k + 2 * j + 1] = f.y * before;
         }
       }
       turn_spread<DIM>(v, p.rot_bits, part);

@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
     Keys seen[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + g;
+      const int r = 8 * n + g, bits = p.rot_bits;
+      const float before = rotation_before(bits), norm = rotation_after(bits);
       float v[kHalves * 16];
 #pragma unroll
       for (int i = 0; i < kHalves * 16; ++i) v[i] = 0.f;
@@ -222,11 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 f = pair_to_float(x[k], p.type);
-            v[8 * i + 2 * k] = f.x, v[8 * i + 2 * k + 1] = f.y;
+            v[8 * i + 2 * k] = f.x * before, v[8 * i + 2 * k + 1] = f.y * before;
           }
         }
       }
-      const int bits = p.rot_bits;
       if (bits > 0) turn_own<kHalves * 16, 1>(v);
       if (bits > 1) turn_own<kHalves * 16, 2>(v);
       if (bits > 2) turn_own<kHalves * 16, 4>(v);
@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
       if (bits > 5) turn_lanes(v, 2, lane);
       if constexpr (DIM == 128)
         if (bits > 6) turn_own<kHalves * 16, 16>(v);
-      const float norm = rotation_norm(bits);
       uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < kHalves * 16; ++i) {
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
               const int token = pos + 16 * t + 8 * h + g;
               float& v = s[t][n][2 * h + e];
               v = there[t][h] && token >= seen[n][e].low && token < seen[n][e].high
-                      ? v * scale[n][e] * key_scale[t][h]
+                      ? v * (scale[n][e] * key_scale[t][h])  // (v is up to 2^30, and v times one of them may pass fp32)
                       : -INFINITY;
               x = fmaxf(x, v);
             }

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const MoveParams p)
   if (token >= p.at.tokens || !locate(p, token, before, page, slot)) page = -1;
   // 16 * 2^(-r/2) in two floats, and the product with them to the last bit but rarely: codes then differ from
   // those of exact arithmetic only where the sums do
-  const float norm = r ? 16.f * rotation_norm(r) : 1.f;
+  const float norm = rotation_after(r);
   const float norm_rest = r & 1 ? 16.f * __uint_as_float((uint32_t)(127 - r / 2) << 23) * 1.21016171e-8f : 0.f;
   const auto times = [](float2 x, float high, float rest) {
     const float2 h = make_float2(high, high), l = make_float2(rest, rest);
@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const MoveParams p)
   };
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
-    if (r) {  // 1/16 first, so that no sum of 128 overflows before the norm
+    if (r) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[o][i] *= 0.0625f;
+      for (int i = 0; i < 16; ++i) v[o][i] *= rotation_before(r);
       turn_spread<DIM>(v[o], r, lane);
     }
     float most = 0.f;

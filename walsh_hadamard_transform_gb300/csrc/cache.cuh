@@ -193,6 +193,11 @@ __device__ __forceinline__ float rotation_norm(int r) {
   return __uint_as_float((uint32_t)(127 - r / 2) << 23) * (r & 1 ? 0.70710678118654752f : 1.f);
 }
 
+// The same around the sums: 1/16 before them and the rest after, so that no sum of 128 passes fp32 where the
+// rotated row does not.
+__device__ __forceinline__ float rotation_before(int r) { return r ? 0.0625f : 1.f; }
+__device__ __forceinline__ float rotation_after(int r) { return r ? 16.f * rotation_norm(r) : 1.f; }
+
 // One bit of the rotation among a thread's own values, STEP apart.
 template <int N, int STEP>
 __device__ __forceinline__ void turn_own(float (&v)[N]) {
