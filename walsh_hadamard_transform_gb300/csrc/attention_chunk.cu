@@ -61,6 +61,9 @@ constexpr int kExtra = 8;
 // How far P may pass a row's maximum, in powers of two, and what lifts P: together 15, what float16 has.  (8 and 7
 // lose small P sooner and measured 0.5% faster: 8192 tokens by 16 heads 421 and 423 us.)
 constexpr float kLag = 4.f, kLift = 11.f;
+// With c above 2^-15 a score may pass 2^23 (S is at most 2^38).  What the row's maximum lost to its rounding, and
+// fma() keeps of a score, is then whole powers of two, so such scores are rounded first.
+constexpr float kLargeFactor = 0x1p-15f;
 
 // What a step's keys are, found by one warp some steps ahead and kept until its last product.
 struct alignas(16) Step {  // (its factors are written 16 bytes at a time)
@@ -373,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         const Keys seen = valid ? seen_by(p, walk.s, walk.block * kChunkRows + 128 * t + mine) : Keys{0, 0x7fffffff};
         const int first_key = walk.keys.low + walk.unit * kKeys;
         const float scale = row_scale[128 * t + mine];
+        // (scale bytes of keys up to which no row of the warp has such a c)
+        const int key_limit = -16 + (127 + kRaise) + 127 - (int)__reduce_max_sync(~0u, __float_as_uint(scale) >> 23);
         top = -INFINITY, total = make_float2(0.f, 0.f), value_ref = 0;
         for (int step = 0; step < count; ++step, ++steps, ++turns) {
           const int pos = first_key + step * kKeys;
@@ -381,11 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           if (step == 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
           if (!wait_or_leave(&known[steps % kAhead], steps / kAhead & 1, &gave_up)) return;
           const Step& info = ring[steps % kAhead];
-          const float c = fmaxf(times_power(scale, info.key_ref - (127 + kRaise)), 0x1p-120f);
+          float c = fmaxf(times_power(scale, info.key_ref - (127 + kRaise)), 0x1p-120f);
           const int new_ref = info.value_ref;
           const int from = seen.low - pos, to = seen.high - pos;  // of the step's keys
           const bool special = info.special != 0;
-          const bool masked = special || __any_sync(~0u, from > 0 || to < kKeys);
+          const bool large = info.key_ref > key_limit;
+          const bool masked = special || large || __any_sync(~0u, from > 0 || to < kKeys);
           if (step > 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
           tmem_fence_after();
 
@@ -394,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           for (int i = 0; i < 4; ++i) tmem_load32(scores + 32 * i, v[i]);
           tmem_wait_loads();
           if (masked) {
+            const bool first = c > kLargeFactor;  // (each row for itself: what others hold does not matter)
+            const float factor = first ? c : 1.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // bits of keys 32 i on: those below `to`, less those below `from`
@@ -402,12 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
               uint32_t poison = 0;
               if (special) see &= ~info.hidden[i], poison = info.poison[i] & see;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[i][j] = see & 1u << j ? v[i][j] : 0xff800000u;
+              for (int j = 0; j < 32; ++j) v[i][j] = see & 1u << j ? __float_as_uint(__uint_as_float(v[i][j]) * factor) : 0xff800000u;
               if (__any_sync(~0u, poison != 0)) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[i][j] = poison & 1u << j ? 0x7fc00000u : v[i][j];
               }
             }
+            if (first) c = 1.f;
           }
           float m[8];
 #pragma unroll
@@ -420,13 +429,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           const float most = max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c;  // (c > 0)
           float less = 1.f;
           bool again = false;
-          if (most > top + kLag || top == -INFINITY) {
+          if (most > __fadd_rd(top, kLag) || top == -INFINITY) {
             again = most > top && top != -INFINITY;
             if (again) less = exp2_fast(top - most);
             if (most > top) top = most;
           }
           const bool moved = step > 0 && __any_sync(~0u, again || new_ref != value_ref);
-          const float shift = top == -INFINITY ? 0.f : kLift - top;
+          // (down, as above: no P passes 2^15, whatever the size of the scores)
+          const float shift = top == -INFINITY ? 0.f : __fadd_rd(kLift, -top);
           const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
           float2 sums[4];
 #pragma unroll
