@@ -440,10 +440,10 @@ int fwt_cache_read(const fwt_cache* cache, const fwt_sequences* sequences, int r
  *
  * R the rotation, K and V the cache's codes times their scales, over the positions j that the token
  * at position i sees: 0 <= j < length; with `causal` j <= i; with window > 0 j > i - window.  A token
- * that sees none gets zeros.  q and out: (tokens, q_heads, dim) of `type` (FWT_BF16 or FWT_F16), q_heads
- * a multiple of the cache's heads.  A key or value whose scale is NaN makes NaN whatever sees
- * it, and nothing else; codes of NaN, which fwt_cache_append does not write, may make NaN any row of
- * the sequence and head.
+ * that sees none gets zeros.  `scale` is finite, times log2(e) too.  q and out: (tokens, q_heads, dim) of
+ * `type` (FWT_BF16 or FWT_F16), q_heads a multiple of the cache's heads.  A key or value whose scale is NaN
+ * makes NaN whatever sees it, and nothing else; codes of NaN, which fwt_cache_append does not write, may make
+ * NaN any row of the sequence and head.
  *
  * Scores, softmax and sums are fp32.  Queries after the rotation, and p = 2^(score - maximum), are
  * rounded to float16 (tensor-core operands; half a unit is 2^-11), both held at powers of two that

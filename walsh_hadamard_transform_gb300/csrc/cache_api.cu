@@ -219,6 +219,7 @@ int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* ou
                         int64_t window, int64_t longest, void* workspace, size_t workspace_bytes,
                         fwt_stream_t stream) {
   Call call;
+  scale *= 1.44269504088896341f;  // scores in powers of two
   if ((type != FWT_BF16 && type != FWT_F16) || (causal != 0 && causal != 1) || window < 0 || longest < 0 ||
       !(scale - scale == 0.f))
     return FWT_ERR_INVALID_ARG;
@@ -252,7 +253,7 @@ int fwt_cache_attention(const void* q, int64_t q_token, int64_t q_head, void* ou
   AttentionParams p;
   p.cache = call.view, p.at = call.at, p.q = rows[0], p.out = rows[1];
   p.type = type, p.group = q_heads / cache->heads, p.by_group = divisor((uint32_t)p.group), p.dim = cache->dim, p.rot_bits = rot_bits;
-  p.scale = scale * 1.44269504088896341f;  // scores in powers of two
+  p.scale = scale;
   p.causal = causal, p.window = window < kMostLength ? (int)window : 0;  // (as long as any sequence: none)
   const int rows_each = item_rows(longest, p.group);
   p.notes = (int4*)workspace, p.parts = (float*)((char*)workspace + workers_of(rows_each) * 2 * sizeof(int4));
