@@ -293,9 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         // 2^e, e from -131 to 123, in two factors
         const int e = value_ref - (127 + kRaise), half_e = e >> 1;
         const float units[2] = {__uint_as_float((uint32_t)(127 + half_e) << 23), __uint_as_float((uint32_t)(127 + e - half_e) << 23)};
+        // (in units of the scales up to the end: sums of values and of rows may pass fp32 where the output does not)
+        const float norm = l == 0.f ? 0.f : (starts && ends ? rotation_norm(p.rot_bits) : 1.f) / l;
+        const float unit[2] = {norm * units[0], units[1]};
         if (starts && ends) {
-          const float norm = l == 0.f ? 0.f : rotation_norm(p.rot_bits) / l;
-          const float unit[2] = {norm * units[0], units[1]};
           const int row = walk.block * kChunkRows + 128 * t + mine;  // of the sequence's with this head
           const int token = walk.s.row + quotient(row, p.by_group), head = walk.head * p.group + remainder(row, p.by_group);
           uint16_t* to = (uint16_t*)p.out.p + token * p.out.token + head * p.out.head;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
               for (int j = 0; j < 8; ++j) {
                 float o[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = __uint_as_float(v[4 * j + k]) * units[0] * units[1];
+                for (int k = 0; k < 4; ++k) o[k] = __uint_as_float(v[4 * j + k]) * unit[0] * unit[1];
                 to[j] = make_float4(o[0], o[1], o[2], o[3]);
               }
             }

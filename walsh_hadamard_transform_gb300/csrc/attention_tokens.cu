@@ -439,12 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
         l += __shfl_xor_sync(~0u, l, 4);
         l += __shfl_xor_sync(~0u, l, 8);
         l += __shfl_xor_sync(~0u, l, 16);
+        // (in units of the scales up to the end: sums of values and of rows may pass fp32 where the output does not)
+        const int bits = p.rot_bits;
+        const float norm = l == 0.f ? 0.f : (whole ? rotation_norm(bits) : 1.f) / l;
         float v[DIM / 8];
 #pragma unroll
-        for (int i = 0; i < DIM / 8; ++i) v[i] = o[i / 2][n][2 * (i & 1) + k] * unit[0] * unit[1];
+        for (int i = 0; i < DIM / 8; ++i) v[i] = o[i / 2][n][2 * (i & 1) + k] * norm;
         if (whole) {
           constexpr int kOwn = DIM == 128 ? 4 : 3;  // bits of a thread's own elements
-          const int bits = p.rot_bits;
           if (bits > 0) turn_own<DIM / 8, 1>(v);
           if (bits > 1) turn_own<DIM / 8, 2>(v);
           if (bits > 2) turn_own<DIM / 8, 4>(v);
@@ -453,7 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
 #pragma unroll
           for (int bit = 0; bit < 3; ++bit)
             if (bits > kOwn + bit) turn_lanes(v, 4 << bit, lane);
-          const float norm = l == 0.f ? 0.f : rotation_norm(bits) / l;
+        }
+#pragma unroll
+        for (int i = 0; i < DIM / 8; ++i) v[i] = v[i] * unit[0] * unit[1];
+        if (whole) {
           if (r < rows) {
             const int token = walk.s.row + quotient(row0 + r, p.by_group);
             const int head = walk.head * p.group + remainder(row0 + r, p.by_group);
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
             for (int i = 0; i < DIM / 64; ++i) {
               uint32_t x[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = pair_from_float(v[8 * i + 2 * j] * norm, v[8 * i + 2 * j + 1] * norm, p.type);
+              for (int j = 0; j < 4; ++j) x[j] = pair_from_float(v[8 * i + 2 * j], v[8 * i + 2 * j + 1], p.type);
               *(uint4*)(to_out + 8 * i) = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }

@@ -85,7 +85,7 @@ cudaError_t launch_attention_join(const AttentionParams& p, int rows, int worker
 constexpr int kMostCtas = 192;   // of an attention kernel
 constexpr int kTokenWorkers = 8;  // of a CTA there, where rows are few; the workspace has room for their parts
 
-// A worker's two parts: rows x dim sums, then a maximum and a total for each row.
+// A worker's two parts: rows x dim means, then a maximum and a total for each row.
 __host__ __device__ constexpr int64_t part_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
 
 constexpr int kMostLength = 0x7fff0000;  // tokens of a sequence (sums with a tile's fit 31 bits)
