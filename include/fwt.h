@@ -450,11 +450,14 @@ int fwt_cache_read(const fwt_cache* cache, const fwt_sequences* sequences, int r
  * keep them in its range: p keeps its bits down to 2^-25 of a row's largest, and below has steps of 2^-35
  * of it.  Codes become float16 exactly.  For FWT_F16 and at most 16 rows (longest new
  * tokens x q_heads / heads) both are two float16 each, and for heads of 64 and more rows queries are.
- * Where there are more rows, what lies more than 2^19 below the largest scale among the first 128 keys
- * of a sequence and head (or a later one over eight times that) keeps fewer bits.
+ * Where there are more rows, keys and values are held in units of the largest scale among 128 keys: the first
+ * ones that a block of 256 rows sees, or those at which a multiprocessor takes the block over from another, or
+ * a later one over eight times that; whether each of the rows sees that key or not.  What lies more than 2^19
+ * below keeps fewer bits, more than 2^28 below none.
  *
  * longest: the most new tokens of any sequence, as far as the host knows (0: as if all had the
- * same); it chooses between kernels and sizes the workspace, and a wrong one costs only time.
+ * same).  It chooses between the kernels, with the roundings said above, and sizes the workspace; a wrong one costs
+ * time, and the result is the same but for those.
  * workspace: DEVICE memory, 16-byte aligned, of at least fwt_cache_attention_workspace_bytes(q_heads, heads, dim,
  * longest) bytes, for longest = 0 that of ceil(tokens / sequences); calls that may run at the same time
  * need one each.

@@ -259,7 +259,7 @@ def cache_attention(q, cache, table, starts, lengths, rotate=None, scale=None, c
     cache was written.
 
     ``longest``: the most new tokens of any sequence as far as the caller knows, 0 as if all had
-    the same; it chooses the kernel and costs only time where it is wrong.  ``out``: the tensor to
+    the same; it chooses the kernel (whose roundings differ) and costs time where it is wrong.  ``out``: the tensor to
     write to.  ``workspace``: a CUDA tensor of ``fwt_cache_attention_workspace_bytes`` (allocated here
     when None), for one call at a time.  Returns out (tokens, q_heads, dim)."""
     if _lib is None:

@@ -25,9 +25,10 @@
 //
 // Bound, large: the chain of a tile, softmax (some 2000 clocks) and its two products (1000), of which
 // two are under way at a time; the issue slots and the exponentials (32 a clock an SM, 1024 clocks a step
-// of both tiles) are not full.  4096 tokens by 32 query and 8 key heads of 128 over 32768: 1.87 ms, 1.1
-// PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries and output, some eight steps an item;
-// 8192 tokens by 16 heads 0.42 ms, 0.66 PFLOP/s.  With scores read twice instead of held in 128 registers
+// of both tiles) are not full (over 8192: tensor cores 38% active, exponentials 19%, issue 39%).  4096 tokens by 32 query
+// and 8 key heads of 128 over 32768: 1.88 ms, 1.09 PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries
+// and output, some eight steps an item; 8192 tokens by 16 heads 0.42 ms, 0.65 PFLOP/s, with a window of 1024 0.20 ms,
+// not causal 0.63 ms.  With scores read twice instead of held in 128 registers
 // (so no split of registers among the warps) the first took 4.9 ms; with the softmax at 176 and the operands
 // at 104 registers 1.88, at 192 and 80, which spills, 2.24.
 //
@@ -54,9 +55,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kKeys = 128;    // of a step; a unit of the plan
 constexpr int kStages = 2;    // of keys, and of values
-constexpr int kAhead = 4;     // steps known at a time
-// Steps that an item costs besides, its queries and its output (measured, us, at 0, 6, 10, 16: 8192 tokens by 16
-// heads 481, 431, 414, 423; five ragged chunks of up to 701 tokens 74, 58, 61, 65).
+constexpr int kAhead = 4;     // steps known at a time (4096 tokens over 32768: 3 2.09 ms, 4 1.88, 6 1.99)
+// Steps that an item costs besides, its queries and its output (measured, us, at 6, 8 and 10: 8192 tokens by 16
+// heads 438, 421, 419; five ragged chunks of up to 701 tokens 58.0, 59.3, 59.9; a chunk of 512 and 32 single tokens
+// 199, 194, 194; the first two at 0 481 and 74, at 16 423 and 65).
 constexpr int kExtra = 8;
 // How far P may pass a row's maximum, in powers of two, and what lifts P: together 15, what float16 has.  (8 and 7
 // lose small P sooner and measured 0.5% faster: 8192 tokens by 16 heads 421 and 423 us.)

@@ -5,7 +5,8 @@
 // O_i is the mean of the part's values: a sum of all their weights, and of a row for the rotation, may pass fp32 where
 // the output does not.  A warp takes a row; its lanes first a part's maximum and total each, then all of the row's
 // elements, parts in the order of the keys.  Bound: latency, a few microseconds less what the launch
-// overlaps; the parts were written just before and come from L2.
+// overlaps (of items of 8 rows: those of 16 and 256 make grids of over 2048 CTAs, which start when the
+// kernel before has ended); the parts were written just before and come from L2.
 #include <cstdint>
 
 #include <cuda_runtime.h>

@@ -12,9 +12,11 @@
 // Rows of several sequences lie one after the other; a CTA counts how many sequences end at or
 // before its first row, and its rows go on from there.
 //
-// Bound, large: issue slots, some 600 instructions a thread for a key's and a value's 16 elements each (of
-// 8192 x 8 x 128 bf16 18 us, 2.7 TB/s; every byte once takes 7.4).  Reading back 4 x 4096 x 8 x 128 27 us,
-// 3.7 TB/s (14.8).  Small: the chain of lookups, 3.3 us.
+// Bound, large: instructions, some 600 a thread for a key's and a value's 16 elements each, and between them waits
+// that 28 warps of a multiprocessor do not cover: issue slots are 63% busy, warps that could issue and were not chosen
+// wait about as long as those whose loads are on their way.  8192 x 8 x 128 bf16 18.5 us, 2.7 TB/s (every byte once
+// takes 7.4); f32 18.6 us, 4.5 TB/s (12.4).  Reading back 4 x 4096 x 8 x 128 27.7 us, 3.7 TB/s (14.9), issue slots 75%
+// busy; into f32 33.4 us, 5.0 TB/s (24.7).  Small: the chain of lookups, 3.3 us.
 #include <cstdint>
 #include <type_traits>
 
