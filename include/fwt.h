@@ -445,7 +445,8 @@ int fwt_cache_read(const fwt_cache* cache, const fwt_sequences* sequences, int r
  * makes NaN whatever sees it, and nothing else; codes of NaN, which fwt_cache_append does not write, may make
  * NaN any row of the sequence and head.
  *
- * Scores, softmax and sums are fp32.  Queries after the rotation, and p = 2^(score - maximum), are
+ * Scores, softmax and sums are fp32.  (Tensor cores round sums toward zero; those of many keys are added up in
+ * parts, so that outputs lose some 2^-13 at most.)  Queries after the rotation, and p = 2^(score - maximum), are
  * rounded to float16 (tensor-core operands; half a unit is 2^-11), both held at powers of two that
  * keep them in its range: p keeps its bits down to 2^-25 of a row's largest, and below has steps of 2^-35
  * of it.  Codes become float16 exactly.  For FWT_F16 and at most 16 rows (longest new

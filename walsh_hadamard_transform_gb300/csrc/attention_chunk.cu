@@ -6,7 +6,7 @@
 //
 //   S = Q K^T            128 x 128 in tensor memory
 //   P = 2^(c S - m + 11) a row a thread; float16, over S in tensor memory; l += P in fp32
-//   O += P V             in tensor memory, fp32
+//   O += P V             in tensor memory, fp32; every 8192 keys added to those before
 //
 // and the two tiles take turns: while the tensor cores work on one, the other's softmax runs.  m is a
 // maximum of the row that may lag behind by a factor of 2^4 in P: only a larger step multiplies O
@@ -26,7 +26,7 @@
 // Bound, large: the chain of a tile, softmax (some 2000 clocks) and its two products (1000), of which
 // two are under way at a time; the issue slots and the exponentials (32 a clock an SM, 1024 clocks a step
 // of both tiles) are not full (over 8192: tensor cores 38% active, exponentials 19%, issue 39%).  4096 tokens by 32 query
-// and 8 key heads of 128 over 32768: 1.88 ms, 1.09 PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries
+// and 8 key heads of 128 over 32768: 1.90 ms, 1.09 PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries
 // and output, some eight steps an item; 8192 tokens by 16 heads 0.42 ms, 0.65 PFLOP/s, with a window of 1024 0.20 ms,
 // not causal 0.63 ms.  With scores read twice instead of held in 128 registers
 // (so no split of registers among the warps) the first took 4.9 ms; with the softmax at 176 and the operands
@@ -78,6 +78,7 @@ struct alignas(16) Step {  // (its factors are written 16 bytes at a time)
   uint32_t hidden[4];          // bit i of word j: token 32 j + i is no token
   uint32_t poison[4];          //                   its key or value is not a number
 };
+constexpr int kSumSteps = kSumKeys / kKeys;
 constexpr int kRaise = 4;  // the largest scale at first; it may rise to 2^7 before the unit moves
 
 template <int DIM>
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   __shared__ uint64_t known[kAhead], done[kAhead];  // steps that are found, and over
-  __shared__ float row_scale[kChunkRows];
+  __shared__ float row_scale[kChunkRows], sums_top[kChunkRows];
+  __shared__ int sums_ref[8];
   __shared__ PlanScratch scratch;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int gave_up;
@@ -286,6 +288,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
       int rows = 0, value_ref = 0;
       float top = -INFINITY;
       float2 total = make_float2(0.f, 0.f);
+      // Where sums of the piece's earlier keys wait (kSumKeys), 32 i + 4 j on of this thread's row: within what the
+      // warp's rows have in the part, the lanes' side by side; and what brings them to the units of now.
+      const auto sums_at = [&](int i, int j) {
+        return (float4*)(p.parts + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * part_floats(kChunkRows, DIM) +
+                         (128 * t + 32 * quarter) * DIM + (8 * i + j) * 128 + 4 * lane);
+      };
+      const auto since = [&](float top, int value_ref) {
+        const float before = sums_top[128 * t + mine];
+        return (before == -INFINITY ? 1.f : exp2_fast(before - top)) *
+               __uint_as_float((uint32_t)max(127 + sums_ref[warp] - value_ref, 0) << 23);
+      };
       const auto output = [&] {
         const bool valid = 128 * t + mine < rows;
         if (!wait_or_leave(&o_full[t], pieces & 1, &gave_up)) return false;
@@ -382,100 +395,136 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
         // (scale bytes of keys up to which no row of the warp has such a c)
         const int key_limit = -16 + (127 + kRaise) + 127 - (int)__reduce_max_sync(~0u, __float_as_uint(scale) >> 23);
         top = -INFINITY, total = make_float2(0.f, 0.f), value_ref = 0;
-        for (int step = 0; step < count; ++step, ++steps, ++turns) {
-          const int pos = first_key + step * kKeys;
-          // (the scores before the first look at the ring: a tile that sits items out would see it long
-          // before its step)
-          if (step == 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
-          if (!wait_or_leave(&known[steps % kAhead], steps / kAhead & 1, &gave_up)) return;
-          const Step& info = ring[steps % kAhead];
-          float c = fmaxf(times_power(scale, info.key_ref - (127 + kRaise)), 0x1p-120f);
-          const int new_ref = info.value_ref;
-          const int from = seen.low - pos, to = seen.high - pos;  // of the step's keys
-          const bool special = info.special != 0;
-          const bool large = info.key_ref > key_limit;
-          const bool masked = special || large || __any_sync(~0u, from > 0 || to < kKeys);
-          if (step > 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
-          tmem_fence_after();
+        int step = 0;
+#pragma unroll 1
+        while (true) {
+          const int until = count > 2 * kSumSteps ? min(step + kSumSteps, count) : count;
+#pragma unroll 1
+          for (; step < until; ++step, ++steps, ++turns) {
+            const int pos = first_key + step * kKeys;
+            // (the scores before the first look at the ring: a tile that sits items out would see it long
+            // before its step)
+            if (step == 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
+            if (!wait_or_leave(&known[steps % kAhead], steps / kAhead & 1, &gave_up)) return;
+            const Step& info = ring[steps % kAhead];
+            float c = fmaxf(times_power(scale, info.key_ref - (127 + kRaise)), 0x1p-120f);
+            const int new_ref = info.value_ref;
+            const int from = seen.low - pos, to = seen.high - pos;  // of the step's keys
+            const bool special = info.special != 0;
+            const bool large = info.key_ref > key_limit;
+            const bool masked = special || large || __any_sync(~0u, from > 0 || to < kKeys);
+            if (step > 0 && !wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
+            tmem_fence_after();
 
-          uint32_t v[4][32];
+            uint32_t v[4][32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_load32(scores + 32 * i, v[i]);
-          tmem_wait_loads();
-          if (masked) {
-            const bool first = c > kLargeFactor;  // (each row for itself: what others hold does not matter)
-            const float factor = first ? c : 1.f;
+            for (int i = 0; i < 4; ++i) tmem_load32(scores + 32 * i, v[i]);
+            tmem_wait_loads();
+            if (masked) {
+              const bool first = c > kLargeFactor;  // (each row for itself: what others hold does not matter)
+              const float factor = first ? c : 1.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // bits of keys 32 i on: those below `to`, less those below `from`
+                const int low = min(max(from - 32 * i, 0), 32), high = min(max(to - 32 * i, 0), 32);
+                uint32_t see = (uint32_t)((1ull << high) - 1) & ~(uint32_t)((1ull << low) - 1);
+                uint32_t poison = 0;
+                if (special) see &= ~info.hidden[i], poison = info.poison[i] & see;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[i][j] = see & 1u << j ? __float_as_uint(__uint_as_float(v[i][j]) * factor) : 0xff800000u;
+                if (__any_sync(~0u, poison != 0)) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) v[i][j] = poison & 1u << j ? 0x7fc00000u : v[i][j];
+                }
+              }
+              if (first) c = 1.f;
+            }
+            float m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 32; j += 2)
+                m[j / 2 & 7] = max3(m[j / 2 & 7], __uint_as_float(v[i][j]), __uint_as_float(v[i][j + 1]));
+            const float most = max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c;  // (c > 0)
+            float less = 1.f;
+            bool again = false;
+            if (most > __fadd_rd(top, kLag) || top == -INFINITY) {
+              again = most > top && top != -INFINITY;
+              if (again) less = exp2_fast(top - most);
+              if (most > top) top = most;
+            }
+            const bool moved = step > 0 && __any_sync(~0u, again || new_ref != value_ref);
+            // (down, as above: no P passes 2^15, whatever the size of the scores)
+            const float shift = top == -INFINITY ? 0.f : __fadd_rd(kLift, -top);
+            const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+            float2 sums[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[i] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // bits of keys 32 i on: those below `to`, less those below `from`
-              const int low = min(max(from - 32 * i, 0), 32), high = min(max(to - 32 * i, 0), 32);
-              uint32_t see = (uint32_t)((1ull << high) - 1) & ~(uint32_t)((1ull << low) - 1);
-              uint32_t poison = 0;
-              if (special) see &= ~info.hidden[i], poison = info.poison[i] & see;
+              uint32_t packed[16];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[i][j] = see & 1u << j ? __float_as_uint(__uint_as_float(v[i][j]) * factor) : 0xff800000u;
-              if (__any_sync(~0u, poison != 0)) {
+              for (int j = 0; j < 16; ++j) {
+                float2 x = fma_pair(make_float2(__uint_as_float(v[i][2 * j]), __uint_as_float(v[i][2 * j + 1])), c2, shift2);
+                x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+                sums[j & 3] = add_pair(sums[j & 3], x);
+                packed[j] = pair_from_float<__half>(x.x, x.y);
+              }
+              tmem_store16(scores + 16 * i, packed);
+            }
+            if (moved) {  // what is there so far, in the new units
+              total.x *= less, total.y *= less;
+              less *= __uint_as_float((uint32_t)max(127 + value_ref - new_ref, 0) << 23);
+#pragma unroll 1
+              for (int i = 0; i < DIM / 32; ++i) {
+                uint32_t o[32];
+                tmem_load32(out + 32 * i, o);
+                tmem_wait_loads();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[i][j] = poison & 1u << j ? 0x7fc00000u : v[i][j];
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * less);
+                tmem_store16(out + 32 * i, o);
+                tmem_store16(out + 32 * i + 16, o + 16);
               }
             }
-            if (first) c = 1.f;
+            value_ref = new_ref;
+            total = add_pair(total, add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])));
+            tmem_wait_stores();
+            tmem_fence_before();
+            __syncwarp();
+            mbar_arrive(&p_full[t], lane == 0);
           }
-          float m[8];
+          if (step == count) break;
+          // The sums so far, done when the next step's scores are there, and those before them: to wait, and that
+          // step's products begin again, or back for the last keys to be added to.
+          const bool last = step + kSumSteps >= count;
+          if (!wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
+          tmem_fence_after();
+          const float f = step > kSumSteps ? since(top, value_ref) : 0.f;
+#pragma unroll 2
+          for (int i = 0; i < DIM / 32; ++i) {
+            uint32_t o[32];
+            tmem_load32(out + 32 * i, o);
+            float4 sums[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m[i] = -INFINITY;
+            for (int j = 0; j < 8; ++j) sums[j] = step > kSumSteps ? *sums_at(i, j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            tmem_wait_loads();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              m[j / 2 & 7] = max3(m[j / 2 & 7], __uint_as_float(v[i][j]), __uint_as_float(v[i][j + 1]));
-          const float most = max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c;  // (c > 0)
-          float less = 1.f;
-          bool again = false;
-          if (most > __fadd_rd(top, kLag) || top == -INFINITY) {
-            again = most > top && top != -INFINITY;
-            if (again) less = exp2_fast(top - most);
-            if (most > top) top = most;
-          }
-          const bool moved = step > 0 && __any_sync(~0u, again || new_ref != value_ref);
-          // (down, as above: no P passes 2^15, whatever the size of the scores)
-          const float shift = top == -INFINITY ? 0.f : __fadd_rd(kLift, -top);
-          const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-          float2 sums[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sums[i] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t packed[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float2 x = fma_pair(make_float2(__uint_as_float(v[i][2 * j]), __uint_as_float(v[i][2 * j + 1])), c2, shift2);
-              x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
-              sums[j & 3] = add_pair(sums[j & 3], x);
-              packed[j] = pair_from_float<__half>(x.x, x.y);
+            for (int j = 0; j < 8; ++j) {
+              const float4 x = sums[j];
+              const float4 sum = make_float4(fmaf(x.x, f, __uint_as_float(o[4 * j])), fmaf(x.y, f, __uint_as_float(o[4 * j + 1])),
+                                             fmaf(x.z, f, __uint_as_float(o[4 * j + 2])), fmaf(x.w, f, __uint_as_float(o[4 * j + 3])));
+              if (!last) *sums_at(i, j) = sum;
+              o[4 * j] = __float_as_uint(sum.x), o[4 * j + 1] = __float_as_uint(sum.y);
+              o[4 * j + 2] = __float_as_uint(sum.z), o[4 * j + 3] = __float_as_uint(sum.w);
             }
-            tmem_store16(scores + 16 * i, packed);
+            if (last) tmem_store16(out + 32 * i, o), tmem_store16(out + 32 * i + 16, o + 16);
           }
-          if (moved) {  // what is there so far, in the new units
-            total.x *= less, total.y *= less;
-            less *= __uint_as_float((uint32_t)max(127 + value_ref - new_ref, 0) << 23);
-#pragma unroll 1
-            for (int i = 0; i < DIM / 32; ++i) {
-              uint32_t o[32];
-              tmem_load32(out + 32 * i, o);
-              tmem_wait_loads();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * less);
-              tmem_store16(out + 32 * i, o);
-              tmem_store16(out + 32 * i + 16, o + 16);
-            }
-          }
-          value_ref = new_ref;
-          total = add_pair(total, add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])));
           tmem_wait_stores();
-          tmem_fence_before();
+          sums_top[128 * t + mine] = top;
+          if (lane == 0) sums_ref[warp] = value_ref;
           __syncwarp();
-          mbar_arrive(&p_full[t], lane == 0);
         }
       }
     }();
@@ -591,11 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
             if (!wait_or_leave(&p_full[t], turns[t] & 1, &gave_up)) return;
             ++turns[t];
             tmem_fence_after();
+            const bool begins = count > 2 * kSumSteps && step % kSumSteps == 0 && step + kSumSteps < count;
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 rows of values, 8 columns of pairs of P
                 mma_tile_from_tmem(tmem + kOutAt + DIM * t, tmem + kScoresAt + 128 * t + 8 * kk, b + kk * 128,
-                                   kOfOut, step + kk > 0);
+                                   kOfOut, (begins ? 0 : step) + kk > 0);
               if (t + 1 == tiles) mma_commit<1>(&v_empty[stage]), mma_commit<1>(&done[steps % kAhead]);
               if (!more) mma_commit<1>(&o_full[t]);
             }

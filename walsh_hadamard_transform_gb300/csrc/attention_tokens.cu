@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
   extern __shared__ __align__(16) uint8_t memory[];
   __shared__ PlanScratch scratch;
   __shared__ Walk walks[kWarps][2];  // of each warp: where it stands, and where its copies do
+  __shared__ float sums_top[kWarps][kRows];  // what the sums that wait (kSumKeys) are in units of
+  __shared__ int sums_most[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   // (the shares of few go to as many multiprocessors as there are)
   const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
@@ -270,6 +272,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     int most = 0;  // the largest scale byte of the values so far
+    float* part = p.parts + (2 * (int64_t)worker + (starts ? 1 : 0)) * part_floats(kRows, DIM);
+    // The sums together with those that wait, if any, in the present units: to wait in turn, or for good.
+    const auto add_sums = [&](bool some, bool wait) {
+      float f[NT][2];
+      const float less = __uint_as_float((uint32_t)max(some ? 127 + sums_most[warp] - most : 0, 0) << 23);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float before = sums_top[warp][8 * n + 2 * c + e];
+          f[n][e] = before == -INFINITY ? less : exp2_fast(before - top[n][e]) * less;
+        }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float4* at = (float4*)part + (i * NT + n) * 32 + lane;
+          if (some) {
+            const float4 x = *at;
+            o[i][n][0] = fmaf(x.x, f[n][0], o[i][n][0]), o[i][n][1] = fmaf(x.y, f[n][1], o[i][n][1]);
+            o[i][n][2] = fmaf(x.z, f[n][0], o[i][n][2]), o[i][n][3] = fmaf(x.w, f[n][1], o[i][n][3]);
+          }
+          if (wait) {
+            *at = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+            o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+          }
+        }
+      __syncwarp();  // (and the part's rows are written over other lanes' sums)
+      if (wait) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (g == 0) sums_top[warp][8 * n + 2 * c + e] = top[n][e];
+        if (lane == 0) sums_most[warp] = most;
+        __syncwarp();
+      }
+    };
 
     for (int pos = from; pos < to; pos += kStep) {
       asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
@@ -418,16 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
           }
         }
       }
+      if ((pos + kStep - from) % kSumKeys == 0 && pos + kStep < to) add_sums(pos + kStep - from > kSumKeys, true);
       __syncwarp();
       present >>= 2;
       fill(stage);
       if (++stage == L::kStages) stage = 0;
     }
 
+    if (to - from > kSumKeys) add_sums(true, false);
+
     // out: the item's rows, or a part of them for launch_attention_join.  Thread (g, c) has of rows
     // 2 c and 2 c + 1 the DIM / 8 elements from DIM / 8 g on.
     const bool whole = starts && ends;
-    float* part = p.parts + (2 * (int64_t)worker + (starts ? 1 : 0)) * part_floats(kRows, DIM);
     // 2^e, e from -142 to 112, in two factors
     const int e = most - 142, half_e = e >> 1;
     const float unit[2] = {__uint_as_float((uint32_t)(127 + half_e) << 23), __uint_as_float((uint32_t)(127 + e - half_e) << 23)};
