@@ -1,5 +1,7 @@
 """Attention over many keys in one share: what a tensor core's sums lose to their rounding toward zero does not grow with
 the number of keys."""
+import math
+
 import pytest
 import torch
 
@@ -94,3 +96,30 @@ def test_units_and_maxima_that_move_between_sums(sequences, new, group, longest,
     room = (of_q + 6 * of_p + of_sums).flatten() + HALF_ULP[dtype] * want.norm(dim=-1)
     off = (got - want).norm(dim=-1)
     assert (off <= room).all(), (off / room).max()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gap", [0.3, 0.7, 1.1, 5.3, 25.5])
+@pytest.mark.parametrize("sequences,new,group,longest", WAYS)
+def test_weights_of_a_million_keys_add_up_to_one(sequences, new, group, longest, gap, dim):
+    """One key `gap` powers of two above all others, which are alike, and values of one: a sum of equal numbers is
+    rounded the same way each time."""
+    pages, heads, repeat = 4, 8, 256
+    cache = fwt.new_cache(pages + 1, PAGE, heads, dim)
+    raw(cache.v)[:] = 0x38
+    for t in (cache.k_scale, cache.v_scale):
+        raw(t).fill_(127)
+    raw(cache.k)[pages, :, 5, 0] = 0x38
+    q = torch.zeros(sequences * new, heads * group, dim, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(sequences, repeat)
+    table[:, 3] = pages
+    starts = torch.arange(sequences + 1, dtype=torch.int32, device="cuda") * new
+    lengths = torch.full((sequences,), pages * PAGE * repeat, dtype=torch.int32, device="cuda")
+    got = fwt.cache_attention(q, cache, table, starts, lengths, rotate=0, causal=False, scale=gap * math.log(2),
+                              longest=longest)
+    # sums of p V as above, and half a unit of p and of the output; sums of p to nearest, by 2^-25 of them for each
+    # of 1024 numbers (a step's sum, or every eighth p of 8192 keys) and again for each such sum
+    room = 1.5 * 2.0 ** -13 + 2 * 2.0 ** -11 + (1024 + 128) * 2.0 ** -25
+    off = (got.double() - 1).abs().max().item()
+    assert off <= room, off

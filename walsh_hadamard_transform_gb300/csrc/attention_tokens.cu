@@ -12,7 +12,7 @@
 // of a key, and of two values that are neighbours in P one byte each side by side.  Queries and
 // outputs are turned in those fragments' layouts too.  (With the warps of a CTA on one item, and their sums
 // joined in shared memory, an item cost 15,000 clocks besides its keys: 64 sequences of 256 to 16384 tokens
-// 237 us.)  These, 32 query and 8 key heads of 128, now take 99 us, 5.1 TB/s; what is left is the copies'
+// 237 us.)  These, 32 query and 8 key heads of 128, now take 100 us, 5.0 TB/s; what is left is the copies'
 // own pace (they stall on a full queue, no wait for data) and items of few keys.  One sequence of 4099
 // tokens: 19 us in both launches, mostly a chain of lookups (sequence, page, codes) and the join.
 //
@@ -50,7 +50,7 @@ template <int DIM>
 struct Layout {
   static constexpr int kValues = kStep * DIM, kKeyScales = 2 * kValues, kValueScales = kKeyScales + kStep;
   static constexpr int kStage = kValueScales + kStep;
-  static constexpr int kStages = DIM == 128 ? 3 : 6;  // (what fits; 2 measured 97 us for 99, 64 decoding sequences)
+  static constexpr int kStages = DIM == 128 ? 3 : 6;  // (what fits; 2 measured 2 us less for 64 decoding sequences)
   static constexpr int kRing = kStages * kStage;  // of a warp
   static constexpr int kBytes = kWarps * kRing;
 };
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
   __shared__ Walk walks[kWarps][2];  // of each warp: where it stands, and where its copies do
   __shared__ float sums_top[kWarps][kRows];  // what the sums that wait (kSumKeys) are in units of
   __shared__ int sums_most[kWarps];
+  __shared__ float sums_total[kWarps][2 * NT][32];  // each lane's sums of p that wait with them
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   // (the shares of few go to as many multiprocessors as there are)
   const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
@@ -282,7 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tokens_kernel(const Att
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float before = sums_top[warp][8 * n + 2 * c + e];
-          f[n][e] = before == -INFINITY ? less : exp2_fast(before - top[n][e]) * less;
+          const float f_e = before == -INFINITY ? 1.f : exp2_fast(before - top[n][e]);
+          float& waits = sums_total[warp][2 * n + e][lane];
+          if (some) total[n][e] = fmaf(waits, f_e, total[n][e]);
+          if (wait) waits = total[n][e], total[n][e] = 0.f;
+          f[n][e] = f_e * less;
         }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
