@@ -25,7 +25,7 @@
 //
 // Bound, large: the chain of a tile, softmax (some 2000 clocks) and its two products (1000), of which
 // two are under way at a time; the issue slots and the exponentials (32 a clock an SM, 1024 clocks a step
-// of both tiles) are not full (over 8192: tensor cores 38% active, exponentials 19%, issue 39%).  4096 tokens by 32 query
+// of both tiles) are not full (over 8192: tensor cores 37% active, exponentials 19%, issue 39%).  4096 tokens by 32 query
 // and 8 key heads of 128 over 32768: 1.90 ms, 1.09 PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries
 // and output, some eight steps an item; 8192 tokens by 16 heads 0.42 ms, 0.65 PFLOP/s, with a window of 1024 0.20 ms,
 // not causal 0.63 ms.  With scores read twice instead of held in 128 registers
