@@ -98,13 +98,10 @@ def test_units_and_maxima_that_move_between_sums(sequences, new, group, longest,
     assert (off <= room).all(), (off / room).max()
 
 
-@pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("gap", [0.3, 0.7, 1.1, 5.3, 25.5])
-@pytest.mark.parametrize("sequences,new,group,longest", WAYS)
-def test_weights_of_a_million_keys_add_up_to_one(sequences, new, group, longest, gap, dim):
+def check_weights(sequences, new, group, longest, gap, dim, repeat):
     """One key `gap` powers of two above all others, which are alike, and values of one: a sum of equal numbers is
     rounded the same way each time."""
-    pages, heads, repeat = 4, 8, 256
+    pages, heads = 4, 8
     cache = fwt.new_cache(pages + 1, PAGE, heads, dim)
     raw(cache.v)[:] = 0x38
     for t in (cache.k_scale, cache.v_scale):
@@ -119,7 +116,20 @@ def test_weights_of_a_million_keys_add_up_to_one(sequences, new, group, longest,
     got = fwt.cache_attention(q, cache, table, starts, lengths, rotate=0, causal=False, scale=gap * math.log(2),
                               longest=longest)
     # sums of p V as above, and half a unit of p and of the output; sums of p to nearest, by 2^-25 of them for each
-    # of 1024 numbers (a step's sum, or every eighth p of 8192 keys) and again for each such sum
-    room = 1.5 * 2.0 ** -13 + 2 * 2.0 ** -11 + (1024 + 128) * 2.0 ** -25
+    # of 1024 numbers at most (every eighth p of 8192 keys), and sums of such sums, of p and of p V
+    room = 1.5 * 2.0 ** -13 + 2 * 2.0 ** -11 + (1024 + 2 * pages * PAGE * repeat / 8192) * 2.0 ** -25
     off = (got.double() - 1).abs().max().item()
     assert off <= room, off
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gap", [0.3, 0.7, 1.1, 5.3, 25.5])
+@pytest.mark.parametrize("sequences,new,group,longest", WAYS)
+def test_weights_of_a_million_keys_add_up_to_one(sequences, new, group, longest, gap, dim):
+    check_weights(sequences, new, group, longest, gap, dim, 256)
+
+
+@pytest.mark.parametrize("gap", [0.3, 0.7, 1.1, 5.3])
+@pytest.mark.parametrize("repeat", [4096, 16384])
+def test_weights_of_many_millions_by_many_rows(gap, repeat):
+    check_weights(19, 1, 1, 300, gap, 64, repeat)

@@ -26,7 +26,7 @@
 // Bound, large: the chain of a tile, softmax (some 2000 clocks) and its two products (1000), of which
 // two are under way at a time; the issue slots and the exponentials (32 a clock an SM, 1024 clocks a step
 // of both tiles) are not full (over 8192: tensor cores 37% active, exponentials 19%, issue 39%).  4096 tokens by 32 query
-// and 8 key heads of 128 over 32768: 1.90 ms, 1.09 PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries
+// and 8 key heads of 128 over 32768: 1.88 ms, 1.09 PFLOP/s, 57% of what cuBLAS reaches.  Short items: their queries
 // and output, some eight steps an item; 8192 tokens by 16 heads 0.42 ms, 0.65 PFLOP/s, with a window of 1024 0.20 ms,
 // not causal 0.63 ms.  With scores read twice instead of held in 128 registers
 // (so no split of registers among the warps) the first took 4.9 ms; with the softmax at 176 and the operands
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   __shared__ uint64_t known[kAhead], done[kAhead];  // steps that are found, and over
-  __shared__ float row_scale[kChunkRows], sums_top[kChunkRows];
+  __shared__ float row_scale[kChunkRows], sums_top[kChunkRows], sums_total[kChunkRows];
   __shared__ int sums_ref[8];
   __shared__ PlanScratch scratch;
   __shared__ uint32_t tmem_base;
@@ -289,15 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
       float top = -INFINITY;
       float2 total = make_float2(0.f, 0.f);
       // Where sums of the piece's earlier keys wait (kSumKeys), 32 i + 4 j on of this thread's row: within what the
-      // warp's rows have in the part, the lanes' side by side; and what brings them to the units of now.
+      // warp's rows have in the part, the lanes' side by side.
       const auto sums_at = [&](int i, int j) {
         return (float4*)(p.parts + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * part_floats(kChunkRows, DIM) +
                          (128 * t + 32 * quarter) * DIM + (8 * i + j) * 128 + 4 * lane);
-      };
-      const auto since = [&](float top, int value_ref) {
-        const float before = sums_top[128 * t + mine];
-        return (before == -INFINITY ? 1.f : exp2_fast(before - top)) *
-               __uint_as_float((uint32_t)max(127 + sums_ref[warp] - value_ref, 0) << 23);
       };
       const auto output = [&] {
         const bool valid = 128 * t + mine < rows;
@@ -501,7 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_chunk_kernel(const Atte
           const bool last = step + kSumSteps >= count;
           if (!wait_or_leave(&s_full[t], turns & 1, &gave_up, false, &issued)) return;
           tmem_fence_after();
-          const float f = step > kSumSteps ? since(top, value_ref) : 0.f;
+          float f = 0.f;  // to the units of now
+          if (step > kSumSteps) {
+            const float before = sums_top[128 * t + mine];
+            f = before == -INFINITY ? 1.f : exp2_fast(before - top);
+            total.x = fmaf(sums_total[128 * t + mine], f, total.x);
+            f *= __uint_as_float((uint32_t)max(127 + sums_ref[warp] - value_ref, 0) << 23);
+          }
+          if (!last) sums_total[128 * t + mine] = total.x + total.y, total = make_float2(0.f, 0.f);
 #pragma unroll 2
           for (int i = 0; i < DIM / 32; ++i) {
             uint32_t o[32];

@@ -92,8 +92,8 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int dim) { return (i
 // share outputs were 0.7% short.  So after this many keys a worker adds its sums to those before in fp32, to
 // nearest, and begins again: outputs are then short by some 2^-13 at most.  (With many rows a share of up to twice as
 // many keys goes on in one sum, and the last ones are added to all.)  Sums wait in the worker's part that they would
-// be written to in the end.  (With few rows so do those of p, which else are one lane's sum of every eighth key: equal ones
-// round alike, and a million keys were off by 0.2%.)  4096 tokens over 32768: 1.90 ms, and 1.88 without.
+// be written to in the end, and those of p beside them (one fp32 number of a lane for every eighth of a million keys was off
+// by 0.2%: equal numbers round alike).  4096 tokens over 32768: 1.885 ms, and 1.88 without.
 constexpr int kSumKeys = 8192;
 
 constexpr int kMostLength = 0x7fff0000;  // tokens of a sequence (sums with a tile's fit 31 bits)
